@@ -77,8 +77,9 @@ enum gdn_status {
     GDN_ERR_WORKSPACE = -7, /* caller workspace NULL, too small or misaligned */
     GDN_ERR_NOMEM = -8,     /* stream-ordered workspace allocation failed */
     GDN_ERR_DTYPE = -9,     /* dtype not supported on the requested path (chunked: bf16 only) */
-    GDN_ERR_SHAPE = -10,    /* shape outside the op's scope (flash_attn: 20 or more queries) */
-    GDN_ERR_SCRATCH = -11   /* gdn_forward_noalloc: the call needs more than its fixed scratch */
+    GDN_ERR_SHAPE = -10,    /* shape outside the op's scope (attention: 20 or more queries; page size) */
+    GDN_ERR_SCRATCH = -11,  /* gdn_forward_noalloc: the call needs more than its fixed scratch */
+    GDN_ERR_PAGE = -12      /* 4-bit cache: a page or length outside the cache (device status only) */
 };
 
 /* dtype of q, k, v (F16: decode attention only) */
@@ -223,8 +224,10 @@ int gdn_supports(int head_dim);
 
 /*
  * gdn_get_device_status -- synchronises `stream`, then returns and clears
- * the library's device status word on the current device: GDN_OK, or
- * GDN_ERR_TIMEOUT if a kernel's bounded wait gave up since the last query.
+ * the library's device status word on the current device: GDN_OK, or what
+ * was recorded last since the last query: GDN_ERR_TIMEOUT if a kernel's
+ * bounded wait gave up, GDN_ERR_PAGE if a 4-bit cache call met a page or a
+ * length outside its cache.
  * Returns GDN_ERR_CUDA if the synchronisation itself failed.
  */
 int gdn_get_device_status(gdn_stream_t stream);
@@ -269,6 +272,78 @@ int gdn_flash_attn(const void *q, const void *k, const void *v, const void *mask
  * head_dim_v) in the model card's "Ops" table: 1 if gdn_flash_attn serves
  * that shape, 0 otherwise. */
 int gdn_flash_attn_supports(int n_q, int head_dim_k, int head_dim_v);
+
+/*
+ * The 4-bit key / value cache, for decode attention over long contexts:
+ * gdn_kv4_write quantises rows as they are appended, gdn_kv4_read gives them
+ * back dense (what gdn_flash_attn takes), gdn_flash_attn_kv4 attends over the
+ * cache as it is.
+ *
+ * What is kept.  For every sequence, kv head and token a key row of head_dim_k
+ * and a value row of head_dim_v elements.  Sixteen neighbouring elements share
+ * a scale s; an element x is kept as the nearest of
+ * +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} to x / s (ties to the even one of the eight, by
+ * index; larger magnitudes to 6), times s.  s is max|x| / 6 rounded to a
+ * significand of 4 bits (nearest, ties to even), in steps of 2^-17 below 2^-14,
+ * at most 10240 (so magnitudes above 61440, infinities among them, are kept as
+ * 61440).  A NaN is kept as 0.  Every kept value is finite and exact in f16,
+ * bf16 and fp32.  4.5 bits an element, 9/32 of bf16.
+ *
+ * Layout.  cache: (n_pages, n_heads_kv, page_size / 16, 9 * (head_dim_k +
+ * head_dim_v)) bytes, gdn_kv4_cache_bytes in all; tiles of 16 tokens whose
+ * inner order is the library's own.  It needs no initial contents.
+ * page_table: (n_seqs, max_pages) int32; position p of sequence b lies in page
+ * page_table[b][p / page_size] at p % page_size.  seq_lens: (n_seqs) int32, the
+ * tokens of each sequence.  Both are device memory, read by the kernels, so a
+ * captured graph sees their values of each replay.  Only the entries that the
+ * lengths reach are read.  A negative length counts as 0.  An entry outside
+ * [0, n_pages), or a length above max_pages * page_size, is recorded as
+ * GDN_ERR_PAGE in the device status word: nothing outside the buffers is
+ * touched, and tokens of such a page, or from position max_pages * page_size
+ * on, count as absent (not written, read as zeros, not attended to).
+ * Pages may be shared by sequences for reading; a call that writes a page must
+ * have it through one sequence only.
+ *
+ * Supported: head_dim_k and head_dim_v each 64, 128 or 256 (gdn_kv4_supports,
+ * else GDN_ERR_HEADDIM), page_size a multiple of 16 (else GDN_ERR_SHAPE), cache
+ * 16-byte aligned, any n_heads_kv.
+ */
+int gdn_kv4_supports(int head_dim_k, int head_dim_v);
+
+/* Bytes of a cache; 0 for sizes that are not supported. */
+size_t gdn_kv4_cache_bytes(int n_pages, int n_heads_kv, int page_size, int head_dim_k, int head_dim_v);
+
+/*
+ * gdn_kv4_write -- quantise rows into the cache.
+ * k: (n_seqs, n_heads_kv, n_new, head_dim_k), v: (n_seqs, n_heads_kv, n_new,
+ *   head_dim_v), dtype GDN_DTYPE_F32, _BF16 or _F16.  strides: NULL for dense
+ *   tensors, or 6 host values, in elements: k's of sequence, head and token,
+ *   then v's (none negative; a row is contiguous, so a transposed view of
+ *   token-major projections needs no copy).  Pointers and rows 16-byte aligned.
+ * seq_lens: lengths that COUNT the new tokens: token i of sequence b goes to
+ *   position seq_lens[b] - n + i, with n = new_lens[b] (device int32, clamped to
+ *   [0, n_new]) or n_new where new_lens is NULL.  Tokens from n on, and those at
+ *   negative positions (a padded batch's empty sequence: length 0), are not
+ *   written.  Everything else in the cache keeps its bytes' meaning.
+ * Errors as above; GDN_ERR_ALIAS where the cache overlaps an input.
+ */
+int gdn_kv4_write(const void *k, const void *v, const long long *strides, void *cache,
+                  const int *page_table, const int *seq_lens, const int *new_lens, int n_seqs,
+                  int n_new, int n_heads_kv, int head_dim_k, int head_dim_v, int n_pages,
+                  int page_size, int max_pages, int dtype, gdn_stream_t stream);
+
+/*
+ * gdn_kv4_read -- the rows that a write of the same arguments would write:
+ * k_out (n_seqs, n_heads_kv, n_tokens, head_dim_k) and v_out (..., head_dim_v),
+ * dense, dtype as given, hold the values kept at positions seq_lens[b] - n + i,
+ * n = read_lens[b] (clamped to [0, n_tokens]) or n_tokens; every other row of
+ * k_out and v_out is written as zeros.  With read_lens = seq_lens, row i is
+ * position i.
+ */
+int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, const int *read_lens,
+                 void *k_out, void *v_out, int n_seqs, int n_tokens, int n_heads_kv, int head_dim_k,
+                 int head_dim_v, int n_pages, int page_size, int max_pages, int dtype,
+                 gdn_stream_t stream);
 
 /*
  * gdn_selftest_wait_timeout -- exercises the library's failure path on the

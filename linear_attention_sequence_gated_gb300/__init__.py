@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
 OK = 0
 ERR_ARG, ERR_HEADDIM, ERR_ALIGN, ERR_ALIAS, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_NOMEM, \
-    ERR_DTYPE, ERR_SHAPE, ERR_SCRATCH = -1, -2, -3, -4, -5, -6, -7, -8, -9, -10, -11
+    ERR_DTYPE, ERR_SHAPE, ERR_SCRATCH, ERR_PAGE = -1, -2, -3, -4, -5, -6, -7, -8, -9, -10, -11, -12
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 PATHS = {"auto": 0, "recurrent": 1, "chunked": 2}
 OPT_L2NORM_QK = 0x100
@@ -37,7 +37,8 @@ OPT_OUT_BF16 = 0x200
 EXPORTS = ["gdn_forward", "gdn_forward_bf16", "gdn_forward_ex", "gdn_workspace_bytes",
            "gdn_select_path", "gdn_supports", "gdn_get_device_status", "gdn_status_string",
            "gdn_version", "gdn_flash_attn", "gdn_flash_attn_supports", "gdn_forward_noalloc",
-           "gdn_selftest_wait_timeout"]
+           "gdn_selftest_wait_timeout", "gdn_kv4_supports", "gdn_kv4_cache_bytes", "gdn_kv4_write",
+           "gdn_kv4_read"]
 
 _lib = None
 
@@ -83,6 +84,14 @@ def lib():
         L.gdn_forward_noalloc.restype = i
         L.gdn_selftest_wait_timeout.argtypes = [vp]
         L.gdn_selftest_wait_timeout.restype = i
+        L.gdn_kv4_supports.argtypes = [i, i]
+        L.gdn_kv4_supports.restype = i
+        L.gdn_kv4_cache_bytes.argtypes = [i] * 5
+        L.gdn_kv4_cache_bytes.restype = sz
+        L.gdn_kv4_write.argtypes = [vp] * 7 + [i] * 9 + [vp]
+        L.gdn_kv4_write.restype = i
+        L.gdn_kv4_read.argtypes = [vp] * 6 + [i] * 9 + [vp]
+        L.gdn_kv4_read.restype = i
         _lib = L
     return _lib
 
@@ -252,3 +261,142 @@ def flash_attn(q, k, v, mask=None, scale=None, *, out=None, stream=None):
     if rc != OK:
         raise GdnError(rc, "gdn_flash_attn")
     return out
+
+
+# ------------------------------------------------------------------ 4-bit cache
+
+def _kv4_dtype(dtype, what):
+    import torch
+    dts = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    if dtype not in dts:
+        raise TypeError(f"{what} must be fp32, bf16 or fp16, got {dtype}")
+    return dts[dtype]
+
+
+def _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, lens=None):
+    """Shapes, types and devices of a cache and what goes with it; its page size."""
+    import torch
+    if cache.dim() != 4 or cache.dtype != torch.uint8 or cache.shape[1] != Hkv \
+            or cache.shape[3] != 9 * (dk + dv):
+        raise ValueError(f"cache: expected (n_pages, {Hkv}, page_size / 16, {9 * (dk + dv)}) uint8, got "
+                         f"{tuple(cache.shape)} {cache.dtype}")
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
+        raise ValueError(f"page_table: expected ({B}, max_pages) int32, got {tuple(page_table.shape)} "
+                         f"{page_table.dtype}")
+    for name, t in (("seq_lens", seq_lens), ("lens", lens)):
+        if t is not None and (tuple(t.shape) != (B,) or t.dtype != torch.int32):
+            raise ValueError(f"{name}: expected ({B},) int32, got {tuple(t.shape)} {t.dtype}")
+    for t in (cache, page_table, seq_lens, lens):
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("cache, page_table and lengths must be contiguous CUDA tensors")
+            if t.device != cache.device:
+                raise ValueError("all tensors must be on one CUDA device")
+    return cache.shape[2] * 16
+
+
+def _on(device, stream):
+    """Makes ``device`` current, and ``stream`` if one is given, so that what a
+    call allocates belongs to the stream that the call runs on."""
+    import contextlib
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def kv4_supports(head_dim_k: int, head_dim_v: int) -> bool:
+    """Whether the 4-bit cache serves these widths (each 64, 128 or 256)."""
+    return bool(lib().gdn_kv4_supports(int(head_dim_k), int(head_dim_v)))
+
+
+def kv4_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, head_dim_v=None, *,
+              device="cuda"):
+    """An empty 4-bit cache: (n_pages, n_heads_kv, page_size / 16, 9 (dk + dv))
+    uint8, for keys of ``head_dim_k`` and values of ``head_dim_v`` (the same
+    where it is not given).  page_size is a multiple of 16."""
+    import torch
+    dv = head_dim_k if head_dim_v is None else head_dim_v
+    if not kv4_supports(head_dim_k, dv):
+        raise GdnError(ERR_HEADDIM, "kv4_cache")
+    if page_size < 16 or page_size % 16 != 0:
+        raise GdnError(ERR_SHAPE, "kv4_cache")
+    return torch.zeros((n_pages, n_heads_kv, page_size // 16, 9 * (head_dim_k + dv)), dtype=torch.uint8,
+                       device=device)
+
+
+def kv4_write(k, v, cache, page_table, seq_lens, new_lens=None, *, stream=None):
+    """Quantise new rows into a 4-bit cache and return the cache.
+
+    k: (n_seqs, n_heads_kv, n_new, dk), v: (n_seqs, n_heads_kv, n_new, dv), fp32,
+    bf16 or fp16; any strides with contiguous, 16-byte aligned rows (a transposed
+    view of token-major projections needs no copy).  page_table: (n_seqs,
+    max_pages) int32; seq_lens: (n_seqs,) int32, lengths that count the new
+    tokens: token i of sequence b goes to position seq_lens[b] - n + i, n =
+    new_lens[b] or n_new.  Tokens from n on and at negative positions are not
+    written.  A page outside the cache shows as ERR_PAGE in device_status().
+    The format and the rest of the contract are with gdn_kv4_write in
+    include/gdn.h."""
+    L = lib()
+    dt = _kv4_dtype(k.dtype, "k/v")
+    if k.dim() != 4 or v.dim() != 4 or v.shape[:3] != k.shape[:3] or v.dtype != k.dtype:
+        raise ValueError("k, v: expected (n_seqs, n_heads_kv, n_new, dk / dv) of one dtype, got "
+                         f"{tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
+    B, Hkv, T, dk = k.shape
+    dv = v.shape[3]
+    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, new_lens)
+    for t in (k, v):
+        if t.device != cache.device:
+            raise ValueError("all tensors must be on one CUDA device")
+        if t.stride(3) != 1 and t.numel():
+            raise ValueError("rows of k and v must be contiguous")
+    strides = (ctypes.c_longlong * 6)(*k.stride()[:3], *v.stride()[:3])
+    with _on(cache.device, stream):
+        rc = L.gdn_kv4_write(k.data_ptr(), v.data_ptr(), strides, cache.data_ptr(), page_table.data_ptr(),
+                             seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, T,
+                             Hkv, dk, dv, cache.shape[0], page, page_table.shape[1], dt,
+                             _stream_handle(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_kv4_write")
+    return cache
+
+
+def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_dim_v=None, *, lens=None,
+             dtype=None, k_out=None, v_out=None, stream=None):
+    """The last rows of each sequence in a 4-bit cache, dense: (k, v) of shapes
+    (n_seqs, n_heads_kv, n_tokens, dk) and (..., dv), as flash_attn takes them.
+
+    Row i of sequence b is what is kept at position seq_lens[b] - n + i, n =
+    lens[b] or n_tokens (what a kv4_write of the same lengths wrote); rows from n
+    on and at negative positions are zeros.  With lens = seq_lens row i is
+    position i.  ``dtype``: fp32, bf16 (default) or fp16; every value is exact
+    in each."""
+    import torch
+    L = lib()
+    dk, dv = int(head_dim_k), int(head_dim_k if head_dim_v is None else head_dim_v)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else torch.bfloat16
+    dt = _kv4_dtype(dtype, "dtype")
+    if cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("cache must be 4-D and page_table 2-D")
+    B, Hkv = page_table.shape[0], cache.shape[1]
+    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, lens)
+    with _on(cache.device, stream):
+        outs = []
+        for name, t, d in (("k_out", k_out, dk), ("v_out", v_out, dv)):
+            if t is None:
+                t = torch.empty((B, Hkv, n_tokens, d), dtype=dtype, device=cache.device)
+            elif tuple(t.shape) != (B, Hkv, n_tokens, d) or t.dtype != dtype or not t.is_contiguous() \
+                    or t.device != cache.device:
+                raise ValueError(f"{name} must be contiguous {(B, Hkv, n_tokens, d)} {dtype} on "
+                                 f"{cache.device}")
+            outs.append(t)
+        rc = L.gdn_kv4_read(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                            None if lens is None else lens.data_ptr(), outs[0].data_ptr(),
+                            outs[1].data_ptr(), B, n_tokens, Hkv, dk, dv, cache.shape[0], page,
+                            page_table.shape[1], dt, _stream_handle(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_kv4_read")
+    return outs[0], outs[1]

@@ -1,7 +1,7 @@
 // C-ABI front end of libgdn.so: argument validation, path selection,
 // workspace handling and the device status word.  Every compute step runs in
 // the kernels of gdn_recurrent.cu and gdn_chunked.cu; this file launches
-// nothing else.  Declarations and the full contract are in include/gdn.h.
+// nothing else (the attention and cache entry points are beside their kernels).  Declarations and the full contract are in include/gdn.h.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -61,6 +61,15 @@ cudaMemPool_t pool_for_current_device() {
     }
     return g_pool[dev];
 }
+
+}  // namespace
+
+namespace gdn {
+int *status_word() { return status_word_for_current_device(); }
+cudaMemPool_t workspace_pool() { return pool_for_current_device(); }
+}  // namespace gdn
+
+namespace {
 
 using gdn::host::aligned;
 using gdn::host::mul_ok;
@@ -302,6 +311,7 @@ const char *gdn_status_string(int status) {
         case GDN_ERR_SHAPE: return "shape outside the op's scope (flash_attn: 20 or more queries)";
         case GDN_ERR_SCRATCH:
             return "the call needs more scratch than gdn_forward_noalloc's fixed 64 MiB array";
+        case GDN_ERR_PAGE: return "a page table entry or a length outside the cache (seen on the device)";
         default: return "unknown status";
     }
 }

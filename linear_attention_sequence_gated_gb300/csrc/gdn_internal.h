@@ -88,6 +88,21 @@ WalkSplit walk_split(long long P, int D, int sms);
 // One CTA whose bounded wait gives up and records GDN_ERR_TIMEOUT (self-test).
 cudaError_t launch_wait_selftest(int *status, cudaStream_t stream);
 
+// Device status word of the current device (NULL if it cannot be had), and the
+// library's memory pool there, for stream-ordered workspaces (gdn_api.cu).
+int *status_word();
+cudaMemPool_t workspace_pool();
+
+// The 4-bit cache's checks, shared by its entry points (gdn_kv4.cu).
+namespace kv4 {
+struct Span {
+    unsigned long long cache, table, lens;   // bytes of each buffer
+};
+inline bool width_ok(int d) { return d == 64 || d == 128 || d == 256; }
+int check_cache(const void *cache, const void *table, const void *lens, int n_seqs, int Hkv, int dk,
+                int dv, int n_pages, int page_size, int max_pages, Span *span);
+}  // namespace kv4
+
 // Host-side argument checks shared by the C-ABI front ends.
 namespace host {
 

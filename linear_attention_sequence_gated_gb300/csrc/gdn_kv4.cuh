@@ -1,0 +1,158 @@
+// The 4-bit key / value cache: its tile format, shared by the kernels that
+// write it, read it back and attend over it.
+//
+// Number format.  Sixteen neighbouring elements of a row share one scale s and
+// each is kept as a 4-bit float (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1,
+// 1.5, 2, 3, 4, 6) times s.  s has 5 exponent and 3 mantissa bits and no sign,
+// with a 16-bit float's exponent bias, so its byte is bits 7 to 14 of s as a
+// 16-bit float and one shift decodes a pair; no tensor-wide factor is needed
+// for small or large rows.  A code times its scale has at most 6 significant
+// bits and |value| in [2^-18, 61440]: exact in f16, bf16 and fp32 alike, so
+// the decoded cache feeds f16 tensor-core MMAs without a rounding.
+//
+// Tile: 16 tokens of one kv head, 9 (dk + dv) bytes, in the order in which a
+// warp's MMA fragments want it, so that every lane reads whole 16-byte words
+// and a tile is one contiguous copy:
+//   key codes    [parts of 128 (or 64) elements][16 tokens][part / 2 bytes],
+//                elements in order, the even one in the low nibble;
+//   key scales   [parts][16 tokens][part / 16];
+//   value codes  [dv / 64 blocks r][8 g][4 t][4 w][4 bytes e]: byte e of word w
+//                holds element 128 (r / 2) + L g + 8 (r % 2) + 2 w + e % 2 of
+//                tokens 4 t + 2 (e / 2) (low nibble) and the next (high), with
+//                L = min(16, dv / 8);
+//   value scales [dv / 16 groups][16 tokens].
+// Pages hold page_size / 16 tiles per kv head: cache[page][kv head][tile].
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace gdn {
+namespace kv4 {
+
+constexpr int kTile = 16;              // tokens of a tile
+constexpr int kMaxScale = 0xE2;        // scale byte of 10240: 6 * 10240 is still finite in f16
+constexpr float kMaxValue = 61440.f;
+
+__host__ __device__ constexpr int tile_bytes(int dk, int dv) { return 9 * (dk + dv); }
+
+// The cache, its page table and lengths, as every kernel takes them.
+struct View {
+    uint8_t *data;          // (n_pages, Hkv, tpp, tile bytes)
+    const int *table;       // (n_seqs, max_pages)
+    const int *lens;        // (n_seqs)
+    int *status;            // device status word
+    int n_pages, Hkv, tpp, max_pages;
+    int dk, dv;
+};
+
+__device__ __forceinline__ int capacity(const View &c) { return c.max_pages * c.tpp * kTile; }
+
+// Tokens of sequence b: what the table has room for at most, none if negative.
+__device__ __forceinline__ int length(const View &c, int b) {
+    return min(max(__ldg(c.lens + b), 0), capacity(c));
+}
+
+// Byte offset of tile `in_page` of (page, kv head h), or -1 for a page that the
+// cache does not have.
+__host__ __device__ inline long long tile_offset(int page, int n_pages, int Hkv, int h, int tpp,
+                                                 int in_page, int bytes) {
+    if ((unsigned)page >= (unsigned)n_pages) return -1;
+    return (((long long)page * Hkv + h) * tpp + in_page) * bytes;
+}
+
+// Tile `tile` of (sequence b, kv head h), or NULL (recorded in the status
+// word) where the table names a page that the cache does not have.
+__device__ __forceinline__ uint8_t *tile_ptr(const View &c, int b, int h, int tile) {
+    const int slot = tile / c.tpp;
+    const int page = __ldg(c.table + (size_t)b * c.max_pages + slot);
+    const long long at = tile_offset(page, c.n_pages, c.Hkv, h, c.tpp, tile - slot * c.tpp,
+                                     tile_bytes(c.dk, c.dv));
+    if (at < 0) {
+        *c.status = GDN_ERR_PAGE;
+        return nullptr;
+    }
+    return c.data + at;
+}
+
+// Where the tokens of a call stand: they end the sequence, `raw` tokens long.
+struct Place {
+    int first;              // position of the call's token 0 (may be negative)
+    int tile;               // the j-th tile that they can touch
+    int t0;                 // the call's token at that tile's first place (may be negative)
+    int count, len;         // tokens of the call; of the sequence, as far as the table reaches
+    // token t of the call is one of its count, at a position that the sequence has
+    __host__ __device__ bool present(int t) const {
+        return t >= 0 && t < count && first + t >= 0 && first + t < len;
+    }
+    // the tile holds a position that the sequence has, and one of the call's tokens
+    __host__ __device__ bool held() const {
+        return tile >= 0 && (long long)tile * kTile < len && t0 < count;
+    }
+};
+__host__ __device__ inline Place place_of(int raw, int cap, int count, int j) {
+    Place p;
+    p.count = count;
+    p.len = raw < cap ? raw : cap;
+    p.first = raw - count;
+    p.tile = (p.first >> 4) + j;       // rounds down for a negative position too
+    p.t0 = (int)((long long)p.tile * kTile - p.first);
+    return p;
+}
+
+// Four code bytes -> four f16 pairs (low nibble in the low half).
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+// Scale bytes 0, 1 (or 2, 3) of a word -> an f16 pair.
+__device__ __forceinline__ uint32_t scales01(uint32_t w) { return __byte_perm(w, 0, 0x1404) >> 1; }
+__device__ __forceinline__ uint32_t scales23(uint32_t w) { return __byte_perm(w, 0, 0x3424) >> 1; }
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// (x.lo, x.lo) and (x.hi, x.hi)
+__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, 0, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, 0, 0x3232); }
+
+__host__ __device__ inline float scale_value(int byte) {
+    return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+}
+
+// The scale byte of a group whose largest magnitude is `a` (no NaN): a / 6
+// rounded to nearest, ties to the even byte, at most kMaxScale.  The multiply
+// and the conversion can be off beside a border, so the two borders around the
+// candidate decide: six times a border (5 bits) is exact in fp32.
+__host__ __device__ inline int scale_byte(float a) {
+    a = fminf(a, kMaxValue);
+    const int h = __half_as_ushort(__float2half_rn(a * (1.f / 6.f)));
+    const int c = (h + 63 + ((h >> 7) & 1)) >> 7;
+    const float up = 6.f * __half2float(__ushort_as_half((unsigned short)((c << 7) + 64)));
+    const float dn = c > 0 ? 6.f * __half2float(__ushort_as_half((unsigned short)((c << 7) - 64))) : -1.f;
+    const bool odd = c & 1;
+    if (a > up || (a == up && odd)) return c + 1;
+    if (a < dn || (a == dn && odd)) return c - 1;
+    return c;
+}
+
+// x / s as the conversion to 4 bits takes it.  The quotient is correctly
+// rounded, so it is a border between two codes only where x / s itself is one
+// (a border times s is exact in fp32), and ties go to the even code.
+__device__ __forceinline__ float ratio(float x, float s) { return s > 0.f ? __fdiv_rn(x, s) : x * 0.f; }
+
+// Two codes in a byte (lo in the low nibble), rounded to nearest even, at most 6.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+        : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+}  // namespace kv4
+}  // namespace gdn

@@ -1,0 +1,27 @@
+// The 4-bit cache's index and rounding arithmetic, compiled for the host, so
+// that it is tested where there is no GPU (tests/test_kv4_host.py).
+#include <cstdint>
+
+#include "../include/gdn.h"
+#include "../linear_attention_sequence_gated_gb300/csrc/gdn_kv4.cuh"
+
+extern "C" {
+
+long long kv4_tile_offset(int page, int n_pages, int Hkv, int h, int tpp, int in_page, int bytes) {
+    return gdn::kv4::tile_offset(page, n_pages, Hkv, h, tpp, in_page, bytes);
+}
+
+// tile, t0, held, then 16 flags: token t0 + i is present
+void kv4_place(int raw, int cap, int count, int j, int *out) {
+    const gdn::kv4::Place p = gdn::kv4::place_of(raw, cap, count, j);
+    out[0] = p.tile;
+    out[1] = p.t0;
+    out[2] = p.held();
+    for (int i = 0; i < 16; ++i) out[3 + i] = p.present(p.t0 + i);
+}
+
+void kv4_scale_bytes(const float *a, int n, int *out) {
+    for (int i = 0; i < n; ++i) out[i] = gdn::kv4::scale_byte(a[i]);
+}
+
+}  // extern "C"
