@@ -346,6 +346,42 @@ int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, 
                  gdn_stream_t stream);
 
 /*
+ * gdn_flash_attn_kv4 -- gdn_flash_attn over a 4-bit cache, with each sequence's
+ * own length:
+ *
+ *   out[b, i, h, :] = sum_j softmax_j(scale * q[b,h,i,:] . k[b,hk,j,:]
+ *                                     + mask[b,0,i,j]) * v[b,hk,j,:]
+ *   over 0 <= j < seq_lens[b] (with causal: j <= seq_lens[b] - n_q + i, the
+ *   queries being the sequence's newest tokens); hk = h / (n_heads /
+ *   n_heads_kv); k and v the values that the cache keeps.
+ *
+ * q:    (n_seqs, n_heads, n_q, head_dim_k) dtype (GDN_DTYPE_F32, _BF16, _F16)
+ * mask: (n_seqs, 1, n_q, max_pages * page_size) dtype, additive (-inf hides a
+ *   token), or NULL
+ * out:  (n_seqs, n_q, n_heads, head_dim_v) of out_dtype
+ * causal: 0 or 1.  scale: finite.
+ * A row that sees no token (an empty sequence, a causal query before the
+ * sequence's start, every token hidden by -inf) is zeros.  A mask of the type's
+ * lowest finite value takes part in the softmax as the number it is.
+ * Accumulation is fp32; the cache's values enter exactly, q exactly (fp32 as 22
+ * bits), the softmax weights with 22 bits.  Results do not depend on timing.
+ * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), the cache's widths and page
+ * sizes, n_heads_kv dividing n_heads.  q and out 16-byte aligned; out must not
+ * overlap an input.
+ * workspace: caller's device buffer of gdn_flash_attn_kv4_workspace_bytes, 256-
+ *   byte aligned, its contents ignored on entry and garbage on return, for one
+ *   call at a time; or NULL: allocated and freed in stream order as by
+ *   gdn_forward_ex.
+ */
+int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, const int *seq_lens,
+                       const void *mask, void *out, int n_seqs, int n_heads, int n_heads_kv, int n_q,
+                       int head_dim_k, int head_dim_v, int n_pages, int page_size, int max_pages,
+                       float scale, int causal, int dtype, int out_dtype, void *workspace,
+                       size_t workspace_bytes, gdn_stream_t stream);
+size_t gdn_flash_attn_kv4_workspace_bytes(int n_seqs, int n_heads, int n_heads_kv, int n_q, int head_dim_k,
+                                          int head_dim_v, int page_size, int max_pages);
+
+/*
  * gdn_selftest_wait_timeout -- exercises the library's failure path on the
  * GPU without faulting it: enqueues on `stream` one small kernel whose
  * bounded wait (on a barrier nothing ever completes) gives up after about

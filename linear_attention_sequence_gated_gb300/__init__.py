@@ -38,7 +38,7 @@ EXPORTS = ["gdn_forward", "gdn_forward_bf16", "gdn_forward_ex", "gdn_workspace_b
            "gdn_select_path", "gdn_supports", "gdn_get_device_status", "gdn_status_string",
            "gdn_version", "gdn_flash_attn", "gdn_flash_attn_supports", "gdn_forward_noalloc",
            "gdn_selftest_wait_timeout", "gdn_kv4_supports", "gdn_kv4_cache_bytes", "gdn_kv4_write",
-           "gdn_kv4_read"]
+           "gdn_kv4_read", "gdn_flash_attn_kv4", "gdn_flash_attn_kv4_workspace_bytes"]
 
 _lib = None
 
@@ -92,6 +92,10 @@ def lib():
         L.gdn_kv4_write.restype = i
         L.gdn_kv4_read.argtypes = [vp] * 6 + [i] * 9 + [vp]
         L.gdn_kv4_read.restype = i
+        L.gdn_flash_attn_kv4.argtypes = [vp] * 6 + [i] * 9 + [ctypes.c_float, i, i, i, vp, sz, vp]
+        L.gdn_flash_attn_kv4.restype = i
+        L.gdn_flash_attn_kv4_workspace_bytes.argtypes = [i] * 8
+        L.gdn_flash_attn_kv4_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -400,3 +404,65 @@ def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_d
     if rc != OK:
         raise GdnError(rc, "gdn_kv4_read")
     return outs[0], outs[1]
+
+
+def flash_attn_kv4_workspace_bytes(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, page_size,
+                                   max_pages) -> int:
+    """Bytes that ``flash_attn_kv4`` needs as its ``workspace``."""
+    return int(lib().gdn_flash_attn_kv4_workspace_bytes(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k,
+                                                        head_dim_v, page_size, max_pages))
+
+
+def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, scale=None, *,
+                   causal: bool = False, out=None, out_dtype=None, workspace=None, stream=None):
+    """Decode attention over a 4-bit cache: out[b, i, h] = softmax_j(scale
+    q[b,h,i] . k[b,hk,j] + mask[b,0,i,j]) v[b,hk,j] over the seq_lens[b] tokens of
+    each sequence (with ``causal``, j <= seq_lens[b] - n_q + i), hk = h //
+    (n_heads / n_heads_kv).
+
+    q: (n_seqs, n_heads, n_q, dk) fp32, bf16 or fp16; cache, page_table,
+    seq_lens as for kv4_write; head_dim_v: the values' width (default dk); mask:
+    (n_seqs, 1, n_q, max_pages * page_size) of q's dtype, additive, or None; scale
+    defaults to 1/sqrt(dk).  Returns out (n_seqs, n_q, n_heads, dv) of
+    ``out_dtype`` (fp32 by default, or a given out's dtype).  Rows that see no
+    token are zeros.  ``workspace``: an optional uint8 CUDA tensor of
+    flash_attn_kv4_workspace_bytes(...) bytes for one call at a time; without it
+    the library allocates in stream order."""
+    import math
+    import torch
+    L = lib()
+    dt = _kv4_dtype(q.dtype, "q")
+    if q.dim() != 4 or cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q and cache must be 4-D and page_table 2-D")
+    B, H, n_q, dk = q.shape
+    dv = int(dk if head_dim_v is None else head_dim_v)
+    Hkv = cache.shape[1]
+    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv)
+    max_pages = page_table.shape[1]
+    if mask is not None and (tuple(mask.shape) != (B, 1, n_q, max_pages * page) or mask.dtype != q.dtype):
+        raise ValueError(f"mask: expected {(B, 1, n_q, max_pages * page)} {q.dtype}, got "
+                         f"{tuple(mask.shape)} {mask.dtype}")
+    for t in (q, mask, workspace):
+        if t is not None and (t.device != cache.device or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.float32
+    odt = _kv4_dtype(out_dtype, "out_dtype")
+    if scale is None:
+        scale = 1.0 / math.sqrt(dk)
+    with _on(cache.device, stream):
+        if out is None:
+            out = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=cache.device)
+        elif tuple(out.shape) != (B, n_q, H, dv) or out.dtype != out_dtype or not out.is_contiguous() \
+                or out.device != cache.device:
+            raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype} on {cache.device}")
+        rc = L.gdn_flash_attn_kv4(
+            q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+            None if mask is None else mask.data_ptr(), out.data_ptr(), B, H, Hkv, n_q, dk, dv,
+            cache.shape[0], page, max_pages, float(scale), int(causal), dt, odt,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream_handle(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_flash_attn_kv4")
+    return out

@@ -154,5 +154,17 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
     return r;
 }
 
+// How the attention's work is shared out: all tiles of all units (sequence, kv
+// head, row block), one after another, cut into equal runs, one a warp.
+// Run w of W over T tiles (W <= T, so none is empty), and the run of tile x.
+__host__ __device__ inline long long run_begin(long long T, int W, int w) { return T * w / W; }
+__host__ __device__ inline int run_of(long long T, int W, long long x) {
+    return (int)(((x + 1) * W - 1) / T);
+}
+// A run that covers a unit in part leaves a partial result: in its slot 0 if
+// the unit began in an earlier run, in its slot 1 if it begins in this one (so
+// a run has at most one of each).
+__host__ __device__ inline int partial_slot(int w, bool begins_here) { return 2 * w + (begins_here ? 1 : 0); }
+
 }  // namespace kv4
 }  // namespace gdn

@@ -33,6 +33,9 @@ def H(tmp_path_factory):
                                                           "-o", so, os.path.join(ROOT, "tests", "kv4_host.cu")])
     lib = ctypes.CDLL(so)
     lib.kv4_tile_offset.restype = ctypes.c_longlong
+    lib.kv4_run_begin.restype = ctypes.c_longlong
+    lib.kv4_run_begin.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
+    lib.kv4_run_of.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong]
     return lib
 
 
@@ -110,6 +113,46 @@ def test_places_of_a_calls_tokens(H, raw, cap, count):
                 seen[out[1] + i] = out[0] * 16 + i
     want = {t: raw - count + t for t in range(count) if 0 <= raw - count + t < min(raw, cap)}
     assert seen == want
+
+
+@pytest.mark.parametrize("units,most", [([1], 2432), ([9, 9, 9, 9], 2432), ([1, 0, 5000, 3, 0, 17, 1], 16),
+                                        ([256] * 40, 97), ([6251, 0, 1], 2432), ([1] * 3000, 1216)])
+def test_runs_share_out_every_tile_and_their_parts_join(H, units, most):
+    """Every run is non-empty; together they cover each tile once; a unit's parts are found again by the runs of its
+    first and last tile, no two parts share a slot, and a whole unit leaves none."""
+    T = sum(units)
+    W = min(T, most)
+    begin = np.cumsum([0] + units)
+    slots, parts = set(), {u: [] for u in range(len(units))}
+    for w in range(W):
+        at, stop = H.kv4_run_begin(T, W, w), H.kv4_run_begin(T, W, w + 1)
+        assert at < stop and (w > 0 or at == 0) and (w < W - 1 or stop == T)
+        while at < stop:
+            u = int(np.searchsorted(begin, at, "right") - 1)
+            end = min(stop, begin[u + 1])
+            if not (at == begin[u] and end == begin[u + 1]):
+                slot = H.kv4_partial_slot(w, int(at == begin[u]))
+                assert slot not in slots and 0 <= slot < 2 * W
+                slots.add(slot)
+                parts[u].append((slot, end - at))
+            at = end
+    for u, n in enumerate(units):
+        if n == 0:
+            continue
+        w0, w1 = H.kv4_run_of(T, W, int(begin[u])), H.kv4_run_of(T, W, int(begin[u + 1] - 1))
+        if w0 == w1:
+            assert not parts[u]
+        else:
+            assert [p[0] for p in parts[u]] == [H.kv4_partial_slot(w, int(w == w0)) for w in range(w0, w1 + 1)]
+            assert sum(p[1] for p in parts[u]) == n
+
+
+def test_runs_of_a_very_long_batch(H):
+    T, W = 1 << 48, 2432
+    for w in (0, 1, 1000, W - 1):
+        at = H.kv4_run_begin(T, W, w)
+        assert at == T * w // W and H.kv4_run_of(T, W, at) == w
+        assert H.kv4_run_of(T, W, H.kv4_run_begin(T, W, w + 1) - 1) == w
 
 
 # ------------------------------------------------------------ refusals
@@ -203,6 +246,56 @@ def test_empty_calls_do_nothing(L):
         assert f(L, B=0, **none) == gdn.OK
         assert f(L, Hkv=0, **none) == gdn.OK
         assert f(L, T=0, k=None, v=None) == gdn.OK
+
+
+def attend(L, **kw):
+    a = dict(q=BASE, cache=BASE + 128 * MB, table=BASE + 256 * MB, lens=BASE + 260 * MB, mask=None,
+             out=BASE + 264 * MB, B=2, H=8, Hkv=2, n_q=1, dk=128, dv=128, n_pages=8, page=64, max_pages=4,
+             scale=0.1, causal=0, dtype=1, out_dtype=0, ws=None, ws_bytes=0)
+    a.update(kw)
+    return L.gdn_flash_attn_kv4(ptr(a["q"]), ptr(a["cache"]), ptr(a["table"]), ptr(a["lens"]), ptr(a["mask"]),
+                                ptr(a["out"]), a["B"], a["H"], a["Hkv"], a["n_q"], a["dk"], a["dv"],
+                                a["n_pages"], a["page"], a["max_pages"], ctypes.c_float(a["scale"]),
+                                a["causal"], a["dtype"], a["out_dtype"], ptr(a["ws"]), a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), gdn.ERR_ARG), (dict(H=-1), gdn.ERR_ARG), (dict(n_q=-1), gdn.ERR_ARG), (dict(Hkv=3), gdn.ERR_ARG),
+    (dict(Hkv=0), gdn.ERR_ARG), (dict(n_q=20), gdn.ERR_SHAPE), (dict(dk=96), gdn.ERR_HEADDIM),
+    (dict(dv=512), gdn.ERR_HEADDIM), (dict(page=8), gdn.ERR_SHAPE), (dict(max_pages=1 << 26), gdn.ERR_ARG),
+    (dict(scale=float("nan")), gdn.ERR_ARG), (dict(scale=float("inf")), gdn.ERR_ARG),
+    (dict(causal=2), gdn.ERR_ARG), (dict(dtype=3), gdn.ERR_ARG), (dict(out_dtype=3), gdn.ERR_ARG),
+    (dict(q=None), gdn.ERR_ARG), (dict(out=None), gdn.ERR_ARG), (dict(cache=None), gdn.ERR_ARG),
+    (dict(table=None), gdn.ERR_ARG), (dict(lens=None), gdn.ERR_ARG),
+    (dict(q=BASE + 8), gdn.ERR_ALIGN), (dict(out=BASE + 264 * MB + 8), gdn.ERR_ALIGN),
+    (dict(mask=BASE + 300 * MB + 1), gdn.ERR_ALIGN), (dict(cache=BASE + 128 * MB + 4), gdn.ERR_ALIGN),
+    (dict(out=BASE), gdn.ERR_ALIAS), (dict(out=BASE + 128 * MB + 64), gdn.ERR_ALIAS),
+    (dict(out=BASE + 256 * MB), gdn.ERR_ALIAS), (dict(mask=BASE + 264 * MB), gdn.ERR_ALIAS),
+    (dict(ws=BASE + 512 * MB, ws_bytes=64), gdn.ERR_WORKSPACE),
+    (dict(ws=BASE + 512 * MB + 16, ws_bytes=1 << 30), gdn.ERR_WORKSPACE),
+    (dict(ws=BASE, ws_bytes=1 << 30), gdn.ERR_ALIAS), (dict(ws=BASE + 264 * MB, ws_bytes=1 << 30), gdn.ERR_ALIAS),
+    (dict(B=1 << 20, H=1 << 12, Hkv=1), gdn.ERR_ARG),                # more rows than the join has blocks
+])
+def test_attention_refuses(L, kw, code):
+    assert attend(L, **kw) == code
+
+
+def test_attention_with_nothing_to_do(L):
+    none = dict(q=None, cache=None, table=None, lens=None, out=None)
+    assert attend(L, B=0, **none) == gdn.OK
+    assert attend(L, H=0, Hkv=0, **none) == gdn.OK
+    assert attend(L, n_q=0, q=None, out=None) == gdn.OK
+
+
+def test_attention_workspace_sizes(L):
+    ok = (2, 8, 2, 1, 128, 128, 64, 4)
+    assert L.gdn_flash_attn_kv4_workspace_bytes(*ok) > 0
+    # never more than the grid's runs ask for, however long the cache
+    assert L.gdn_flash_attn_kv4_workspace_bytes(64, 32, 8, 1, 128, 128, 64, 1 << 20) < 64 << 20
+    for i, bad in ((0, 0), (0, -1), (1, 0), (2, 3), (3, 0), (3, 20), (4, 96), (5, 32), (6, 24), (7, 0), (7, 1 << 26)):
+        a = list(ok)
+        a[i] = bad
+        assert L.gdn_flash_attn_kv4_workspace_bytes(*a) == 0
 
 
 def test_binding_refuses():
