@@ -40,6 +40,7 @@
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
 #include "gdn_kv4.cuh"
+#include "gdn_ptx.cuh"
 
 namespace gdn {
 namespace kv4 {
@@ -47,11 +48,26 @@ namespace {
 
 constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for
 
-// Rows of a unit's block (8 per MMA column tile) and warps of a CTA: 16 where
-// 128 registers a thread hold the output tile, else 8.
-constexpr int kMaxRows = 16;
+// Rows of a unit's block: 8 per MMA column tile.
 constexpr int rows_of(long long R) { return R > 8 ? 16 : 8; }
+
+// Shape of the kernel for widths DK, DV and NT column tiles of rows.  Each warp
+// streams its run through a ring of its own in shared memory: stages of U tiles,
+// each tile one bulk copy.  16 warps where 128 registers a thread hold the output
+// tile, else 8.
 constexpr int warps_of(int dk, int dv, int rows) { return rows == 8 && dk <= 128 && dv <= 128 ? 16 : 8; }
+template <int DK, int DV, int NT>
+struct Geo {
+    static constexpr int WARPS = warps_of(DK, DV, 8 * NT);
+    static constexpr int U = 2;
+    static constexpr int TB = tile_bytes(DK, DV);
+    static constexpr int BUDGET = 216 * 1024;
+    static constexpr int FIT = BUDGET / (WARPS * U * TB);
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int RING = STAGES * U * TB;       // of a warp
+    static constexpr int SMEM = WARPS * RING;
+    static_assert(STAGES >= 2 && TB % 16 == 0, "ring");
+};
 
 struct Attn {
     View c;
@@ -175,12 +191,15 @@ template <int DV, int ROWS> constexpr size_t kPartial = (size_t)ROWS * (DV + 2);
 // One warp's share of one unit: an online softmax over tiles.
 template <int DK, int DV, int NT, bool QLO>
 struct Unit {
+    static constexpr int U = Geo<DK, DV, NT>::U, TB = tile_bytes(DK, DV);
     static constexpr int CK = DK > 128 ? 2 : 1;        // key parts
     static constexpr int ST = DK >= 128 ? 8 : 4;       // MMA steps of a part
     static constexpr int VB = DV / 64;                 // value blocks, four M tiles each
     uint32_t qh[NT][CK * ST][2], ql[QLO ? NT : 1][CK * ST][2];
     float f[NT][2];                                    // row factors of the scores
     int lim[NT][2];                                    // tokens that the row sees
+    int all;                                           // tokens that every row sees and no mask changes
+    int rows_left;                                     // rows of the block that there are
     size_t mrow[NT][2];                                // its mask row
     float m[NT][2], l[NT][2];
     float o[NT][VB * 4][4];
@@ -189,6 +208,8 @@ struct Unit {
         const int g = lane >> 2, t = lane & 3;
         const int rep = a.H / a.c.Hkv;
         const int raw = max(__ldg(a.c.lens + b), 0), len = min(raw, capacity(a.c));
+        rows_left = a.R - rb * 8 * NT;
+        all = a.mask ? 0 : (a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = rb * 8 * NT + nt * 8 + g;
@@ -224,7 +245,7 @@ struct Unit {
                 const int mine = rb * 8 * NT + nt * 8 + 2 * t + r, i = mine % a.n_q;
                 // (a length past the table counts in full for the causal limit)
                 const long long own = (long long)raw - (a.n_q - 1) + i;
-                lim[nt][r] = mine >= a.R ? 0 : (a.causal ? (int)min((long long)len, own) : len);
+                lim[nt][r] = a.causal && mine < a.R ? (int)min((long long)len, own) : len;
                 mrow[nt][r] = ((size_t)b * a.n_q + i) * (size_t)capacity(a.c);
                 m[nt][r] = -INFINITY;
                 l[nt][r] = 0.f;
@@ -236,124 +257,161 @@ struct Unit {
         }
     }
 
-    // One tile: `p` its bytes, tokens pos .. pos + 15 of a sequence of len tokens.
-    __device__ __forceinline__ void tile(const Attn &a, const uint8_t *p, int pos, int len, int lane) {
+    // U tiles at `p`, tokens pos .. of a sequence; from `stop` on they are not this
+    // warp's or not there, and tile i counts only if bit i of `good` is set.
+    __device__ __forceinline__ void tiles(const Attn &a, const uint8_t *p, int pos, int stop, unsigned good,
+                                          int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int ka = 4 * (g >> 1) + (g & 1), kb = ka + 2;   // tokens of C rows g, g + 8
-        float s[NT][4];
+        float s[U][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < U; ++u) {
+            const uint8_t *k = p + u * TB;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < CK; ++c) {
-            uint32_t wa[ST / 2], wb[ST / 2];           // four steps' codes: two bytes each
-            uint32_t sa, sb;                           // f16 scales of the lane's one or two groups
-            if constexpr (ST == 8) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p + c * 1024 + ka * 64 + t * 16);
-                const uint4 y = *reinterpret_cast<const uint4 *>(p + c * 1024 + kb * 64 + t * 16);
-                wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
-                wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
-                const uint8_t *sc = p + 8 * DK + c * 128 + 2 * t;
-                sa = scales01(*reinterpret_cast<const uint16_t *>(sc + ka * 8));
-                sb = scales01(*reinterpret_cast<const uint16_t *>(sc + kb * 8));
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(p + ka * 32 + t * 8);
-                const uint2 y = *reinterpret_cast<const uint2 *>(p + kb * 32 + t * 8);
-                wa[0] = x.x; wa[1] = x.y;
-                wb[0] = y.x; wb[1] = y.y;
-                const uint8_t *sc = p + 8 * DK + t;
-                sa = scales01(sc[ka * 4]);
-                sb = scales01(sc[kb * 4]);
-            }
+                for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
 #pragma unroll
-            for (int h = 0; h < ST / 2; ++h) {         // a word a token: two steps
-                uint32_t x[4], y[4];
-                decode4(wa[h], x);
-                decode4(wb[h], y);
-                const bool second = ST == 8 && h >= 2;
-                const uint32_t da = second ? dup_hi(sa) : dup_lo(sa), db = second ? dup_hi(sb) : dup_lo(sb);
+            for (int c = 0; c < CK; ++c) {
+                uint32_t wa[ST / 2], wb[ST / 2];       // two steps' codes a word
+                uint32_t sa, sb;                       // f16 scales of the lane's one or two groups
+                if constexpr (ST == 8) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(k + c * 1024 + ka * 64 + t * 16);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(k + c * 1024 + kb * 64 + t * 16);
+                    wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
+                    wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+                    const uint8_t *sc = k + 8 * DK + c * 128 + 2 * t;
+                    sa = scales01(*reinterpret_cast<const uint16_t *>(sc + ka * 8));
+                    sb = scales01(*reinterpret_cast<const uint16_t *>(sc + kb * 8));
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(k + ka * 32 + t * 8);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(k + kb * 32 + t * 8);
+                    wa[0] = x.x; wa[1] = x.y;
+                    wb[0] = y.x; wb[1] = y.y;
+                    const uint8_t *sc = k + 8 * DK + t;
+                    sa = scales01(sc[ka * 4]);
+                    sb = scales01(sc[kb * 4]);
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t A[4] = {mul2(x[2 * i], da), mul2(y[2 * i], db), mul2(x[2 * i + 1], da),
-                                           mul2(y[2 * i + 1], db)};
-                    const int st = c * ST + 2 * h + i;
+                for (int h = 0; h < ST / 2; ++h) {
+                    uint32_t x[4], y[4];
+                    decode4(wa[h], x);
+                    decode4(wb[h], y);
+                    const bool second = ST == 8 && h >= 2;
+                    const uint32_t da = second ? dup_hi(sa) : dup_lo(sa), db = second ? dup_hi(sb) : dup_lo(sb);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma(s[nt], A, qh[nt][st][0], qh[nt][st][1]);
-                        if constexpr (QLO) mma(s[nt], A, ql[nt][st][0], ql[nt][st][1]);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t A[4] = {mul2(x[2 * i], da), mul2(y[2 * i], db), mul2(x[2 * i + 1], da),
+                                               mul2(y[2 * i + 1], db)};
+                        const int st = c * ST + 2 * h + i;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
+                            if constexpr (QLO) mma(s[u][nt], A, ql[nt][st][0], ql[nt][st][1]);
+                        }
                     }
                 }
             }
         }
         // scores in natural units, so that a mask of the type's lowest value stays finite
-        uint32_t ph[NT][2], pl[NT][2];
+        const bool plain = pos + U * kTile <= min(all, stop) && good == (1u << U) - 1u;
+        uint32_t ph[U][NT][2], pl[U][NT][2];
+        float cf[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = pos + (e < 2 ? ka : kb), r = e & 1;
-                float x = s[nt][e] * f[nt][r];
-                if (key < lim[nt][r]) {
-                    if (a.mask) x += element(a.mask, a.q_type, mrow[nt][r] + key);
-                } else {
-                    x = -INFINITY;
-                }
-                s[nt][e] = x;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][nt][e] *= f[nt][e & 1];
+            if (!plain) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = pos + u * kTile + (e < 2 ? ka : kb), r = e & 1;
+                        if (key < min(lim[nt][r], stop) && (good >> u & 1)) {
+                            if (a.mask && rows_left > nt * 8 + 2 * t + r)
+                                s[u][nt][e] += element(a.mask, a.q_type, mrow[nt][r] + key);
+                        } else {
+                            s[u][nt][e] = -INFINITY;
+                        }
+                    }
             }
-            float pr[4];
-            bool moved = false;
-            float cf[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float mx = fmaxf(s[nt][r], s[nt][r + 2]);
+                float mx = fmaxf(s[0][nt][r], s[0][nt][r + 2]);
+#pragma unroll
+                for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][r], s[u][nt][r + 2]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 const float mn = fmaxf(m[nt][r], mx);
                 const float base = mn == -INFINITY ? 0.f : mn;
-                cf[r] = exp2_approx((m[nt][r] - base) * kLog2e);
-                moved |= mn != m[nt][r];
+                cf[nt][r] = exp2_approx((m[nt][r] - base) * kLog2e);
                 m[nt][r] = mn;
-                pr[r] = exp2_approx(fmaf(s[nt][r] - base, kLog2e, kPBits));
-                pr[r + 2] = exp2_approx(fmaf(s[nt][r + 2] - base, kLog2e, kPBits));
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r] - base, kLog2e, kPBits));
+                    s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2] - base, kLog2e, kPBits));
+                    sum += s[u][nt][r] + s[u][nt][r + 2];
+                }
+                l[nt][r] = fmaf(l[nt][r], cf[nt][r], sum);
             }
-            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) l[nt][r] *= cf[r];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < VB * 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nt][i][e] *= cf[e & 1];
-            }
-            l[nt][0] += pr[0] + pr[2];
-            l[nt][1] += pr[1] + pr[3];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                split2(pr[2 * k], pr[2 * k + 1], ph[nt][k], pl[nt][k]);
-                ph[nt][k] = transpose8(ph[nt][k]);
-                pl[nt][k] = transpose8(pl[nt][k]);
-            }
+                for (int k = 0; k < 2; ++k) {
+                    split2(s[u][nt][2 * k], s[u][nt][2 * k + 1], ph[u][nt][k], pl[u][nt][k]);
+                    ph[u][nt][k] = transpose8(ph[u][nt][k]);
+                    pl[u][nt][k] = transpose8(pl[u][nt][k]);
+                }
         }
-        // tokens behind the sequence's last: their scale bytes may hold anything,
-        // and 0 times infinity would spoil the row
-        const int left = len - pos - 4 * t;
-        const uint32_t live = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+        // The products of U tiles add up in the MMAs, small terms first, and reach
+        // the output by one fp32 FMA that also rescales it: the MMAs' accumulation
+        // truncates, and over thousands of tokens that would show.
 #pragma unroll
         for (int r = 0; r < VB; ++r) {
-            const uint4 w4 = *reinterpret_cast<const uint4 *>(p + 9 * DK + ((r * 8 + g) * 4 + t) * 16);
-            const int group = DV == 64 ? g >> 1 : (r >> 1) * 8 + g;
-            const uint32_t sw = *reinterpret_cast<const uint32_t *>(p + 9 * DK + 8 * DV + group * 16 + 4 * t) & live;
-            const uint32_t s01 = scales01(sw), s23 = scales23(sw);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            uint32_t w[U][4], s01[U], s23[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint8_t *v = p + u * TB + 9 * DK;
+                const uint4 x = *reinterpret_cast<const uint4 *>(v + ((r * 8 + g) * 4 + t) * 16);
+                w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
+                const int group = DV == 64 ? g >> 1 : (r >> 1) * 8 + g;
+                uint32_t sw = *reinterpret_cast<const uint32_t *>(v + 8 * DV + group * 16 + 4 * t);
+                // tokens that are not there: their scale bytes may hold anything, and
+                // 0 times infinity would spoil the row
+                if (!plain) {
+                    const int left = (good >> u & 1) ? stop - (pos + u * kTile + 4 * t) : 0;
+                    sw &= left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+                }
+                s01[u] = scales01(sw);
+                s23[u] = scales23(sw);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t x[4];
-                decode4(w[i], x);
-                const uint32_t A[4] = {mul2(x[0], s01), mul2(x[1], s01), mul2(x[2], s23), mul2(x[3], s23)};
+                float d[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[nt][e] = 0.f;
+                uint32_t A[U][4];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    uint32_t x[4];
+                    decode4(w[u][i], x);
+                    A[u][0] = mul2(x[0], s01[u]); A[u][1] = mul2(x[1], s01[u]);
+                    A[u][2] = mul2(x[2], s23[u]); A[u][3] = mul2(x[3], s23[u]);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma(o[nt][r * 4 + i], A, ph[nt][0], ph[nt][1]);
-                    mma(o[nt][r * 4 + i], A, pl[nt][0], pl[nt][1]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) mma(d[nt], A[u], pl[u][nt][0], pl[u][nt][1]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) mma(d[nt], A[u], ph[u][nt][0], ph[u][nt][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[nt][r * 4 + i][e] = fmaf(o[nt][r * 4 + i][e], cf[nt][e & 1], d[nt][e]);
                 }
             }
         }
@@ -391,115 +449,270 @@ struct Unit {
     }
 };
 
+// A walk over a run: the unit and the tile that it has reached.
+struct Cursor {
+    long long left;                    // tiles of the run from here on
+    int b, u, j, n, len;               // sequence, unit of it, tile of the unit, tiles of a unit, tokens
+    __device__ __forceinline__ int batch(int U) const { return (int)min((long long)min(U, n - j), left); }
+    __device__ __forceinline__ void step(const Attn &a, int units, int k) {
+        left -= k;
+        j += k;
+        if (j < n) return;
+        j = 0;
+        if (++u == units) {
+            u = 0;
+            if (left > 0) {            // the next sequence that holds anything
+                do {
+                    len = length(a.c, ++b);
+                    n = tiles_of(len);
+                } while (n == 0);
+            }
+        }
+    }
+};
+
 template <int DK, int DV, int NT, bool QLO>
-__global__ void __launch_bounds__(warps_of(DK, DV, 8 * NT) * 32, 1) attn_kernel(const Attn a) {
+__global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(const Attn a) {
+    using G = Geo<DK, DV, NT>;
+    constexpr int U = G::U, ST = G::STAGES;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[G::WARPS][ST];
+    __shared__ unsigned good[G::WARPS][ST];            // tiles of the stage whose pages exist
+    __shared__ int gave_up;                            // (a hint only: other waits need not run out too)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) gave_up = 0;
+    if (lane < ST) ptx::mbar_init(&full[warp][lane], 1);
+    if (lane == 0) ptx::fence_mbar_init();
+    __syncthreads();
     const int units = a.c.Hkv * a.n_rb;
     const long long T = total_tiles(a, units, lane);
     const int W = (int)min((long long)a.W, T);
     // neighbouring runs on different SMs: few tiles spread over the GPU
     const int w = warp * gridDim.x + blockIdx.x;
     if (w >= W) return;
-    long long at = run_begin(T, W, w);
-    const long long stop = run_begin(T, W, w + 1);
+    const long long at = run_begin(T, W, w);
     long long before;
-    int b = find_tile(a, units, at, lane, &before);
-    int len = length(a.c, b), n = tiles_of(len);
-    int u = (int)((at - before) / n);
-    int j = (int)((at - before) % n);
+    Cursor c;
+    c.left = run_begin(T, W, w + 1) - at;
+    c.b = find_tile(a, units, at, lane, &before);
+    c.len = length(a.c, c.b);
+    c.n = tiles_of(c.len);
+    c.u = (int)((at - before) / c.n);
+    c.j = (int)((at - before) % c.n);
+
+    uint8_t *ring = smem + warp * G::RING;
+    // Copies run ST - 1 stages ahead.  The tiles' addresses are looked up for a
+    // window of up to 32 tiles of a unit at once, one a lane.
+    Cursor ahead = c;
+    const uint8_t *src = nullptr;
+    unsigned have = 0;                                 // tiles of the window whose pages exist
+    int off = 0, count = 0, put = 0;                   // window's tiles copied, its tiles; next stage
+    auto copy = [&]() {
+        if (off == count) {
+            if (ahead.left <= 0) return;
+            off = 0;
+            count = ahead.batch(32);
+            src = lane < count ? tile_ptr(a.c, ahead.b, ahead.u / a.n_rb, ahead.j + lane) : nullptr;
+            have = __ballot_sync(0xffffffffu, src != nullptr);
+            ahead.step(a, units, count);
+        }
+        const int k = min(U, count - off);
+        const unsigned mine = have >> off & ((1u << k) - 1u);
+        if (lane == 0) {
+            good[warp][put] = mine;
+            ptx::mbar_arrive_expect_tx(&full[warp][put], __popc(mine) * G::TB);
+        }
+        __syncwarp();
+        if (lane >= off && lane < off + k && src)
+            ptx::bulk_load(ring + (put * U + lane - off) * G::TB, src, G::TB, &full[warp][put]);
+        off += k;
+        put = put + 1 == ST ? 0 : put + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) copy();
+
     Unit<DK, DV, NT, QLO> unit;
-    while (at < stop) {
-        const int j0 = j, j1 = (int)min((long long)n, j + (stop - at));
-        const int hk = u / a.n_rb, rb = u - hk * a.n_rb;
+    int get = 0;                                       // stage to read, and its barrier's phase
+    uint32_t phase = 0;
+    while (c.left > 0) {
+        const int b = c.b, hk = c.u / a.n_rb, rb = c.u - hk * a.n_rb, j0 = c.j;
+        const int j1 = (int)min((long long)c.n, c.j + c.left), stop = min(c.len, j1 * kTile);
         unit.begin(a, b, hk, rb, lane);
-        for (; j < j1; ++j) {
-            const uint8_t *p = tile_ptr(a.c, b, hk, j);
-            if (p) unit.tile(a, p, j * kTile, len, lane);
+        for (int j = j0; j < j1; j += U) {
+            copy();                                    // into the stage that the last step left
+            if (!ptx::mbar_wait(&full[warp][get], phase, &gave_up)) {
+                *a.c.status = GDN_ERR_TIMEOUT;
+                gave_up = 1;
+                // the copies in flight still write this block's shared memory
+                const int never = 0;
+                do {
+                    ptx::mbar_wait(&full[warp][get], phase, &never, 1 << 28);
+                    get = get + 1 == ST ? 0 : get + 1;
+                    phase ^= get == 0;
+                } while (get != put);
+                return;
+            }
+            unit.tiles(a, ring + get * U * G::TB, j * kTile, stop, good[warp][get], lane);
+            __syncwarp();                              // the stage is read
+            get = get + 1 == ST ? 0 : get + 1;
+            phase ^= get == 0;
         }
-        unit.end(a, b, hk, rb, j0 == 0 && j1 == n, partial_slot(w, j0 == 0), lane);
-        at += j1 - j0;
-        j = 0;
-        if (++u == units && at < stop) {               // next sequence that holds anything
-            u = 0;
-            do {
-                len = length(a.c, ++b);
-                n = tiles_of(len);
-            } while (n == 0);
-        }
+        unit.end(a, b, hk, rb, j0 == 0 && j1 == c.n, partial_slot(w, j0 == 0), lane);
+        c.step(a, units, j1 - j0);
     }
 }
 
-// Joins the partial results of one row: thread (p, x) adds up parts p, p + PL,
-// ... of 4 columns with a running maximum, then the PL threads of a column join.
-constexpr int kJoinThreads = 256;
+// Joins the partial results of the rows that several runs share.  A block has
+// `rpb` rows, a warp each.  A warp reads the maxima and sums of up to 32 parts at
+// once, so their weights are known before the outputs are read, and those loads
+// do not wait for one another.  A row of more parts is left to the whole block.
+constexpr int kJoinWarps = 8;
 template <int DV, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
-    constexpr int XL = DV / 4, PL = kJoinThreads / XL;
-    __shared__ float sm[PL], sl[PL];
-    __shared__ float4 so[PL][XL];
-    const int lane = threadIdx.x & 31;
-    long long i = blockIdx.x;
-    const int row = (int)(i % a.R);
-    i /= a.R;
-    const int hk = (int)(i % a.c.Hkv), b = (int)(i / a.c.Hkv);
-    const int rb = row / ROWS, local = row % ROWS;
-    const int units = a.c.Hkv * a.n_rb, n = tiles_of(length(a.c, b));
+struct Join {
+    static constexpr int V = DV == 64 ? 2 : 4, C = DV == 256 ? 2 : 1;   // columns of a lane: C times V
+    float x[C * V];
+    float M, L;
+    // parts first, first + step, ... below n of a row; part 0 is in its run's slot 1
+    __device__ __forceinline__ void parts(const float *ws, int w0, int n, int local, int first, int step, int lane) {
+        M = -INFINITY;
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < C * V; ++e) x[e] = 0.f;
+        for (int p0 = first; p0 < n; p0 += 32 * step) {
+            const int mine = p0 + lane * step, cnt = min(32, (n - p0 + step - 1) / step);
+            const float *at = ws + (size_t)partial_slot(w0 + mine, mine == 0) * kPartial<DV, ROWS>;
+            float m = -INFINITY, l = 0.f;
+            if (mine < n) {
+                m = __ldcg(at + ROWS * DV + local);
+                l = __ldcg(at + ROWS * (DV + 1) + local);
+            }
+            float top = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, M);
+            const float base = top == -INFINITY ? 0.f : top;
+            const float old = exp2_approx((M - base) * kLog2e), wt = exp2_approx((m - base) * kLog2e);
+            M = top;
+            float sum = l * wt;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            L = fmaf(L, old, sum);
+#pragma unroll
+            for (int e = 0; e < C * V; ++e) x[e] *= old;
+#pragma unroll 4
+            for (int i = 0; i < cnt; ++i) {
+                const int p = p0 + i * step;
+                const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV, ROWS> + local * DV;
+                const float k = __shfl_sync(0xffffffffu, wt, i);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if constexpr (V == 2) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(row) + lane);
+                        x[0] = fmaf(v.x, k, x[0]); x[1] = fmaf(v.y, k, x[1]);
+                    } else {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(row + 128 * c) + lane);
+                        x[4 * c] = fmaf(v.x, k, x[4 * c]); x[4 * c + 1] = fmaf(v.y, k, x[4 * c + 1]);
+                        x[4 * c + 2] = fmaf(v.z, k, x[4 * c + 2]); x[4 * c + 3] = fmaf(v.w, k, x[4 * c + 3]);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ int column(int c, int e, int lane) const { return c * 128 + lane * V + e; }
+    __device__ __forceinline__ void store(const Attn &a, size_t at, int lane) const {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const size_t i = at + column(c, e, lane);
+                const float u = x[c * V + e] * inv, v = x[c * V + e + 1] * inv;
+                if (a.out_type == GDN_DTYPE_F32)
+                    *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + i) = make_float2(u, v);
+                else if (a.out_type == GDN_DTYPE_BF16)
+                    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) =
+                        __floats2bfloat162_rn(u, v);
+                else
+                    *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(u, v);
+            }
+    }
+};
+
+template <int DV, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, long long n_rows) {
+    __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = a.c.Hkv * a.n_rb;
     const long long T = total_tiles(a, units, lane);
     const int W = (int)min((long long)a.W, T);
-    const int x = threadIdx.x % XL, p = threadIdx.x / XL;
-    const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV + 4 * x;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, L = 0.f;
-    const long long first = tiles_before(a, units, b, lane) + (long long)(hk * a.n_rb + rb) * n;
+    auto place = [&](long long r, int &local) {        // where a row's output goes
+        const int row = (int)(r % a.R), hk = (int)(r / a.R % a.c.Hkv), b = (int)(r / a.R / a.c.Hkv);
+        local = row % ROWS;
+        return (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV;
+    };
+    const long long r0 = (long long)blockIdx.x * rpb, r = r0 + warp;
+    int w0 = 0, n = -1;                                // runs that share the row; -1: none of ours
+    if (warp < rpb && r < n_rows) {
+        const int row = (int)(r % a.R), hk = (int)(r / a.R % a.c.Hkv), b = (int)(r / a.R / a.c.Hkv);
+        const int tiles = tiles_of(length(a.c, b));
+        n = 0;
+        if (tiles > 0) {
+            const long long first = tiles_before(a, units, b, lane) + (long long)(hk * a.n_rb + row / ROWS) * tiles;
+            w0 = run_of(T, W, first);
+            n = run_of(T, W, first + tiles - 1) - w0 + 1;
+        }
+    }
+    if (lane == 0) {
+        s_w0[warp] = w0;
+        s_n[warp] = n;
+    }
     // the attention kernel's results; every block waits, so that this grid never
     // ends before that one
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n > 0) {
-        const int w0 = run_of(T, W, first), w1 = run_of(T, W, first + n - 1);
-        if (w0 == w1) return;                          // one run had it all and wrote it
-        for (int w = w0 + p; w <= w1; w += PL) {
-            const float *part = a.ws + (size_t)partial_slot(w, w == w0) * kPartial<DV, ROWS>;
-            const float m = __ldcg(part + ROWS * DV + local), l = __ldcg(part + ROWS * (DV + 1) + local);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + local * DV) + x);
-            const float mn = fmaxf(M, m), base = mn == -INFINITY ? 0.f : mn;
-            const float c0 = exp2_approx((M - base) * kLog2e), c1 = exp2_approx((m - base) * kLog2e);
-            acc = make_float4(acc.x * c0 + v.x * c1, acc.y * c0 + v.y * c1, acc.z * c0 + v.z * c1,
-                              acc.w * c0 + v.w * c1);
-            L = L * c0 + l * c1;
-            M = mn;
-        }
-    }
-    so[p][x] = acc;
-    if (x == 0) {
-        sm[p] = M;
-        sl[p] = L;
+    Join<DV, ROWS> join;
+    int local;
+    if (n >= 0 && n != 1 && n <= 32) {                 // (one run had it all: written; none: zeros)
+        const size_t at = place(r, local);
+        join.parts(a.ws, w0, n, local, 0, 1, lane);
+        join.store(a, at, lane);
     }
     __syncthreads();
-    if (p != 0) return;
-    float top = -INFINITY;
+    for (int i = 0; i < rpb; ++i) {
+        if (s_n[i] <= 32) continue;
+        const size_t at = place(r0 + i, local);
+        join.parts(a.ws, s_w0[i], s_n[i], local, warp, kJoinWarps, lane);
 #pragma unroll
-    for (int i2 = 0; i2 < PL; ++i2) top = fmaxf(top, sm[i2]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < join.C; ++c)
 #pragma unroll
-    for (int i2 = 0; i2 < PL; ++i2) {
-        const float c = exp2_approx((sm[i2] - base) * kLog2e);
-        const float4 v = so[i2][x];
-        sum += sl[i2] * c;
-        acc = make_float4(acc.x + v.x * c, acc.y + v.y * c, acc.z + v.z * c, acc.w + v.w * c);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (a.out_type == GDN_DTYPE_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = acc;
-    } else if (a.out_type == GDN_DTYPE_BF16) {
-        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(acc.x, acc.y), __floats2bfloat162_rn(acc.z, acc.w)};
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(h);
-    } else {
-        __half2 h[2] = {__floats2half2_rn(acc.x, acc.y), __floats2half2_rn(acc.z, acc.w)};
-        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + at) = *reinterpret_cast<uint2 *>(h);
+            for (int e = 0; e < join.V; ++e) s_x[warp][join.column(c, e, lane)] = join.x[c * join.V + e];
+        if (lane == 0) {
+            s_m[warp] = join.M;
+            s_l[warp] = join.L;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int e = 0; e < join.C * join.V; ++e) join.x[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                const float wt = exp2_approx((s_m[k] - base) * kLog2e);
+                sum = fmaf(s_l[k], wt, sum);
+#pragma unroll
+                for (int c = 0; c < join.C; ++c)
+#pragma unroll
+                    for (int e = 0; e < join.V; ++e)
+                        join.x[c * join.V + e] = fmaf(s_x[k][join.column(c, e, lane)], wt, join.x[c * join.V + e]);
+            }
+            join.L = sum;
+            join.store(a, at, lane);
+        }
+        __syncthreads();
     }
 }
 
@@ -507,20 +720,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
 
 template <int DK, int DV, int NT, bool QLO>
 cudaError_t launch(const Attn &a, cudaStream_t stream) {
-    const int warps = warps_of(DK, DV, 8 * NT);
-    attn_kernel<DK, DV, NT, QLO><<<kGrid, warps * 32, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    using G = Geo<DK, DV, NT>;
+    static PerDeviceOnce attrs;
+    cudaError_t e = attrs.run([] {
+        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    G::SMEM);
+    });
     if (e != cudaSuccess) return e;
+    attn_kernel<DK, DV, NT, QLO><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // few rows: a block each, so that long rows are shared out; many: a warp each
+    const long long n_rows = (long long)a.n_seqs * a.c.Hkv * a.R;
+    const int rpb = (int)(n_rows >= 2 * kGrid * kJoinWarps ? kJoinWarps : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.c.Hkv * a.R));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3((unsigned)((n_rows + rpb - 1) / rpb));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<DV, 8 * NT>, a);
+    return cudaLaunchKernelEx(&cfg, join_kernel<DV, 8 * NT>, a, rpb, n_rows);
 }
 
 template <int DK, int DV>
