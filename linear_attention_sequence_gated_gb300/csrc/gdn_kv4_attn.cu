@@ -93,6 +93,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same with a zero accumulator
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // 8 x 8 transpose of 16-bit elements across the warp: lane (g, t) gives row g,
 // columns 2t, 2t + 1 and gets row g of the transpose.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -189,64 +196,86 @@ __device__ __forceinline__ int find_tile(const Attn &a, int units, long long x, 
 template <int DV, int ROWS> constexpr size_t kPartial = (size_t)ROWS * (DV + 2);
 
 // One warp's share of one unit: an online softmax over tiles.
-template <int DK, int DV, int NT, bool QLO>
+template <int DK, int DV, int NT, bool QLO, bool PLO>
 struct Unit {
     static constexpr int U = Geo<DK, DV, NT>::U, TB = tile_bytes(DK, DV);
     static constexpr int CK = DK > 128 ? 2 : 1;        // key parts
     static constexpr int ST = DK >= 128 ? 8 : 4;       // MMA steps of a part
     static constexpr int VB = DV / 64;                 // value blocks, four M tiles each
     uint32_t qh[NT][CK * ST][2], ql[QLO ? NT : 1][CK * ST][2];
-    float f[NT][2];                                    // row factors of the scores
-    int lim[NT][2];                                    // tokens that the row sees
+    float f[NT][2];                                    // row factors of the scores (not negative)
+    int qi[NT][2];                                     // the row's query; -1: no such row
     int all;                                           // tokens that every row sees and no mask changes
-    int rows_left;                                     // rows of the block that there are
-    size_t mrow[NT][2];                                // its mask row
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];                          // running maximum, sum of the weights
     float o[NT][VB * 4][4];
 
     __device__ __forceinline__ void begin(const Attn &a, int b, int hk, int rb, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int rep = a.H / a.c.Hkv;
         const int raw = max(__ldg(a.c.lens + b), 0), len = min(raw, capacity(a.c));
-        rows_left = a.R - rb * 8 * NT;
         all = a.mask ? 0 : (a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len);
+        // all loads first: a lane's elements are whole 16-byte words
+        constexpr int QE = QLO ? 4 : 8, QW = ST * 4 / QE;   // elements a word, words a part
+        uint4 raw_q[NT][CK][QW];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = rb * 8 * NT + nt * 8 + g;
-            const bool ok = row < a.R;
-            const size_t q0 = ((size_t)(b * (size_t)a.H + hk * rep) * a.n_q + (ok ? row : 0)) * DK;
+            const size_t q0 = ((size_t)(b * (size_t)a.H + hk * rep) * a.n_q + row) * DK;
+            const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
+                                                              (q0 + t * ST * 4) * (16 / QE));
+#pragma unroll
+            for (int c = 0; c < CK; ++c)
+#pragma unroll
+                for (int i = 0; i < QW; ++i)
+                    raw_q[nt][c][i] = row < a.R ? __ldg(at + c * (128 / QE) + i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             float x[CK * ST * 4];
             float big = 0.f;
 #pragma unroll
             for (int c = 0; c < CK; ++c)
 #pragma unroll
-                for (int e = 0; e < ST * 4; ++e) {
-                    const float v = ok ? element(a.q, a.q_type, q0 + c * 128 + t * ST * 4 + e) : 0.f;
-                    x[c * ST * 4 + e] = v;
-                    big = fmaxf(big, fabsf(v));
+                for (int i = 0; i < QW; ++i) {
+                    const uint32_t w[4] = {raw_q[nt][c][i].x, raw_q[nt][c][i].y, raw_q[nt][c][i].z,
+                                           raw_q[nt][c][i].w};
+                    float *y = x + (c * QW + i) * QE;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (QLO) {
+                            y[e] = __uint_as_float(w[e]);
+                        } else if (a.q_type == GDN_DTYPE_BF16) {
+                            y[2 * e] = __uint_as_float(w[e] << 16);
+                            y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                        } else {
+                            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                            y[2 * e] = h.x;
+                            y[2 * e + 1] = h.y;
+                        }
+                    }
                 }
+#pragma unroll
+            for (int e = 0; e < CK * ST * 4; ++e) big = fmaxf(big, fabsf(x[e]));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // 2^14 / (the power of two at or below the row's largest element)
             const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 126);
             const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-            const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * a.scale;
+            const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(a.scale);
+            const float sup = a.scale < 0.f ? -up : up;   // q takes the scale's sign
 #pragma unroll
             for (int s = 0; s < CK * ST; ++s)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const float x0 = x[s * 4 + 2 * p] * up, x1 = x[s * 4 + 2 * p + 1] * up;
+                    const float x0 = x[s * 4 + 2 * p] * sup, x1 = x[s * 4 + 2 * p + 1] * sup;
                     if constexpr (QLO) split2(x0, x1, qh[nt][s][p], ql[nt][s][p]);
                     else qh[nt][s][p] = half2_bits(__floats2half2_rn(x0, x1));
                 }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 f[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
-                const int mine = rb * 8 * NT + nt * 8 + 2 * t + r, i = mine % a.n_q;
-                // (a length past the table counts in full for the causal limit)
-                const long long own = (long long)raw - (a.n_q - 1) + i;
-                lim[nt][r] = a.causal && mine < a.R ? (int)min((long long)len, own) : len;
-                mrow[nt][r] = ((size_t)b * a.n_q + i) * (size_t)capacity(a.c);
+                const int mine = rb * 8 * NT + nt * 8 + 2 * t + r;
+                qi[nt][r] = mine < a.R ? mine % a.n_q : -1;
                 m[nt][r] = -INFINITY;
                 l[nt][r] = 0.f;
             }
@@ -259,7 +288,7 @@ struct Unit {
 
     // U tiles at `p`, tokens pos .. of a sequence; from `stop` on they are not this
     // warp's or not there, and tile i counts only if bit i of `good` is set.
-    __device__ __forceinline__ void tiles(const Attn &a, const uint8_t *p, int pos, int stop, unsigned good,
+    __device__ __forceinline__ void tiles(const Attn &a, const uint8_t *p, int b, int pos, int stop, unsigned good,
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int ka = 4 * (g >> 1) + (g & 1), kb = ka + 2;   // tokens of C rows g, g + 8
@@ -267,10 +296,6 @@ struct Unit {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint8_t *k = p + u * TB;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < CK; ++c) {
                 uint32_t wa[ST / 2], wb[ST / 2];       // two steps' codes a word
@@ -306,37 +331,41 @@ struct Unit {
                         const int st = c * ST + 2 * h + i;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
+                            if (st == 0) mma0(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
+                            else mma(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
                             if constexpr (QLO) mma(s[u][nt], A, ql[nt][st][0], ql[nt][st][1]);
                         }
                     }
                 }
             }
         }
-        // scores in natural units, so that a mask of the type's lowest value stays finite
         const bool plain = pos + U * kTile <= min(all, stop) && good == (1u << U) - 1u;
-        uint32_t ph[U][NT][2], pl[U][NT][2];
+        uint32_t ph[U][NT][2], pl[PLO ? U : 1][NT][2];
         float cf[NT][2];
+        if (!plain) {
+            const int raw = max(__ldg(a.c.lens + b), 0);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    // (a length past the table counts in full for the causal limit)
+                    const int i = qi[nt][r];
+                    const int lim = a.causal ? (int)min((long long)stop, (long long)raw - a.n_q + 1 + i) : stop;
+                    const size_t row = ((size_t)b * a.n_q + i) * (size_t)capacity(a.c);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = r; e < 4; e += 2) {
+                            const int key = pos + u * kTile + (e < 2 ? ka : kb);
+                            float x = s[u][nt][e] * f[nt][r];
+                            if (i < 0 || key >= lim || !(good >> u & 1)) x = -INFINITY;
+                            else if (a.mask) x += element(a.mask, a.q_type, row + key);
+                            s[u][nt][e] = x;
+                        }
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[u][nt][e] *= f[nt][e & 1];
-            if (!plain) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = pos + u * kTile + (e < 2 ? ka : kb), r = e & 1;
-                        if (key < min(lim[nt][r], stop) && (good >> u & 1)) {
-                            if (a.mask && rows_left > nt * 8 + 2 * t + r)
-                                s[u][nt][e] += element(a.mask, a.q_type, mrow[nt][r] + key);
-                        } else {
-                            s[u][nt][e] = -INFINITY;
-                        }
-                    }
-            }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float mx = fmaxf(s[0][nt][r], s[0][nt][r + 2]);
@@ -344,26 +373,45 @@ struct Unit {
                 for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][r], s[u][nt][r + 2]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float mn = fmaxf(m[nt][r], mx);
-                const float base = mn == -INFINITY ? 0.f : mn;
-                cf[nt][r] = exp2_approx((m[nt][r] - base) * kLog2e);
+                // The weight of a score x is 2^((x - maximum) log2 e + 12).  Without a
+                // mask that is one FMA on the MMAs' result, with the maximum's product
+                // rounded the same way wherever it is used.  Scores that took a mask
+                // are differences in natural units first: masks of the type's lowest
+                // value would overflow.
+                const float old = m[nt][r], mn = fmaxf(old, plain ? mx * f[nt][r] : mx);
                 m[nt][r] = mn;
+                const float base = mn == -INFINITY ? 0.f : mn;
+                cf[nt][r] = exp2_approx(a.mask ? (old - base) * kLog2e : old * kLog2e - __fmul_rn(base, kLog2e));
                 float sum = 0.f;
+                if (plain) {
+                    const float k = f[nt][r] * kLog2e, z = kPBits - __fmul_rn(base, kLog2e);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r] - base, kLog2e, kPBits));
-                    s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2] - base, kLog2e, kPBits));
-                    sum += s[u][nt][r] + s[u][nt][r + 2];
+                    for (int u = 0; u < U; ++u) {
+                        s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r], k, z));
+                        s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2], k, z));
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r] - base, kLog2e, kPBits));
+                        s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2] - base, kLog2e, kPBits));
+                    }
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u) sum += s[u][nt][r] + s[u][nt][r + 2];
                 l[nt][r] = fmaf(l[nt][r], cf[nt][r], sum);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    split2(s[u][nt][2 * k], s[u][nt][2 * k + 1], ph[u][nt][k], pl[u][nt][k]);
+                    if constexpr (PLO) {
+                        split2(s[u][nt][2 * k], s[u][nt][2 * k + 1], ph[u][nt][k], pl[u][nt][k]);
+                        pl[u][nt][k] = transpose8(pl[u][nt][k]);
+                    } else {
+                        ph[u][nt][k] = half2_bits(__floats2half2_rn(s[u][nt][2 * k], s[u][nt][2 * k + 1]));
+                    }
                     ph[u][nt][k] = transpose8(ph[u][nt][k]);
-                    pl[u][nt][k] = transpose8(pl[u][nt][k]);
                 }
         }
         // The products of U tiles add up in the MMAs, small terms first, and reach
@@ -390,11 +438,6 @@ struct Unit {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float d[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[nt][e] = 0.f;
                 uint32_t A[U][4];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -405,13 +448,20 @@ struct Unit {
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
+                    float d[4];
+                    if constexpr (PLO) {
+                        mma0(d, A[0], pl[0][nt][0], pl[0][nt][1]);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) mma(d[nt], A[u], pl[u][nt][0], pl[u][nt][1]);
+                        for (int u = 1; u < U; ++u) mma(d, A[u], pl[u][nt][0], pl[u][nt][1]);
+                        mma(d, A[0], ph[0][nt][0], ph[0][nt][1]);
+                    } else {
+                        mma0(d, A[0], ph[0][nt][0], ph[0][nt][1]);
+                    }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) mma(d[nt], A[u], ph[u][nt][0], ph[u][nt][1]);
+                    for (int u = 1; u < U; ++u) mma(d, A[u], ph[u][nt][0], ph[u][nt][1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        o[nt][r * 4 + i][e] = fmaf(o[nt][r * 4 + i][e], cf[nt][e & 1], d[nt][e]);
+                        o[nt][r * 4 + i][e] = fmaf(o[nt][r * 4 + i][e], cf[nt][e & 1], d[e]);
                 }
             }
         }
@@ -451,9 +501,9 @@ struct Unit {
 
 // A walk over a run: the unit and the tile that it has reached.
 struct Cursor {
-    long long left;                    // tiles of the run from here on
+    int left;                          // tiles of the run from here on
     int b, u, j, n, len;               // sequence, unit of it, tile of the unit, tiles of a unit, tokens
-    __device__ __forceinline__ int batch(int U) const { return (int)min((long long)min(U, n - j), left); }
+    __device__ __forceinline__ int batch(int U) const { return min(min(U, n - j), left); }
     __device__ __forceinline__ void step(const Attn &a, int units, int k) {
         left -= k;
         j += k;
@@ -471,7 +521,7 @@ struct Cursor {
     }
 };
 
-template <int DK, int DV, int NT, bool QLO>
+template <int DK, int DV, int NT, bool QLO, bool PLO>
 __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(const Attn a) {
     using G = Geo<DK, DV, NT>;
     constexpr int U = G::U, ST = G::STAGES;
@@ -480,7 +530,6 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
     __shared__ unsigned good[G::WARPS][ST];            // tiles of the stage whose pages exist
     __shared__ int gave_up;                            // (a hint only: other waits need not run out too)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) gave_up = 0;
     if (lane < ST) ptx::mbar_init(&full[warp][lane], 1);
     if (lane == 0) ptx::fence_mbar_init();
@@ -494,12 +543,12 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
     const long long at = run_begin(T, W, w);
     long long before;
     Cursor c;
-    c.left = run_begin(T, W, w + 1) - at;
+    c.left = (int)(run_begin(T, W, w + 1) - at);
     c.b = find_tile(a, units, at, lane, &before);
     c.len = length(a.c, c.b);
     c.n = tiles_of(c.len);
-    c.u = (int)((at - before) / c.n);
-    c.j = (int)((at - before) % c.n);
+    c.u = (int)quotient(at - before, c.n);
+    c.j = (int)(at - before - (long long)c.u * c.n);
 
     uint8_t *ring = smem + warp * G::RING;
     // Copies run ST - 1 stages ahead.  The tiles' addresses are looked up for a
@@ -532,12 +581,12 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) copy();
 
-    Unit<DK, DV, NT, QLO> unit;
+    Unit<DK, DV, NT, QLO, PLO> unit;
     int get = 0;                                       // stage to read, and its barrier's phase
     uint32_t phase = 0;
     while (c.left > 0) {
         const int b = c.b, hk = c.u / a.n_rb, rb = c.u - hk * a.n_rb, j0 = c.j;
-        const int j1 = (int)min((long long)c.n, c.j + c.left), stop = min(c.len, j1 * kTile);
+        const int j1 = min(c.n, c.j + c.left), stop = min(c.len, j1 * kTile);
         unit.begin(a, b, hk, rb, lane);
         for (int j = j0; j < j1; j += U) {
             copy();                                    // into the stage that the last step left
@@ -553,7 +602,7 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
                 } while (get != put);
                 return;
             }
-            unit.tiles(a, ring + get * U * G::TB, j * kTile, stop, good[warp][get], lane);
+            unit.tiles(a, ring + get * U * G::TB, b, j * kTile, stop, good[warp][get], lane);
             __syncwarp();                              // the stage is read
             get = get + 1 == ST ? 0 : get + 1;
             phase ^= get == 0;
@@ -600,21 +649,30 @@ struct Join {
             L = fmaf(L, old, sum);
 #pragma unroll
             for (int e = 0; e < C * V; ++e) x[e] *= old;
-#pragma unroll 4
-            for (int i = 0; i < cnt; ++i) {
-                const int p = p0 + i * step;
-                const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV, ROWS> + local * DV;
-                const float k = __shfl_sync(0xffffffffu, wt, i);
+            constexpr int B = 8;                       // loads in flight (they do not pass the shuffles)
+            for (int i0 = 0; i0 < cnt; i0 += B) {
+                float v[B][C * V];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    if constexpr (V == 2) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(row) + lane);
-                        x[0] = fmaf(v.x, k, x[0]); x[1] = fmaf(v.y, k, x[1]);
-                    } else {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(row + 128 * c) + lane);
-                        x[4 * c] = fmaf(v.x, k, x[4 * c]); x[4 * c + 1] = fmaf(v.y, k, x[4 * c + 1]);
-                        x[4 * c + 2] = fmaf(v.z, k, x[4 * c + 2]); x[4 * c + 3] = fmaf(v.w, k, x[4 * c + 3]);
+                for (int i = 0; i < B; ++i) {
+                    const int p = p0 + min(i0 + i, cnt - 1) * step;
+                    const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV, ROWS> + local * DV;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        if constexpr (V == 2) {
+                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(row) + lane);
+                            v[i][0] = y.x; v[i][1] = y.y;
+                        } else {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(row + 128 * c) + lane);
+                            v[i][4 * c] = y.x; v[i][4 * c + 1] = y.y; v[i][4 * c + 2] = y.z; v[i][4 * c + 3] = y.w;
+                        }
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const float k = __shfl_sync(0xffffffffu, wt, min(i0 + i, 31));
+#pragma unroll
+                    for (int e = 0; e < C * V; ++e)
+                        if (i0 + i < cnt) x[e] = fmaf(v[i][e], k, x[e]);
                 }
             }
         }
@@ -718,16 +776,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
 
 // ------------------------------------------------------------------ host
 
-template <int DK, int DV, int NT, bool QLO>
+template <int DK, int DV, int NT, bool QLO, bool PLO>
 cudaError_t launch(const Attn &a, cudaStream_t stream) {
     using G = Geo<DK, DV, NT>;
     static PerDeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
-    attn_kernel<DK, DV, NT, QLO><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
+    attn_kernel<DK, DV, NT, QLO, PLO><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // few rows: a block each, so that long rows are shared out; many: a warp each
@@ -737,6 +795,10 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)((n_rows + rpb - 1) / rpb));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
+    // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
+    // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
+    // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
+    // as a plain launch.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -745,11 +807,18 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, join_kernel<DV, 8 * NT>, a, rpb, n_rows);
 }
 
+// fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
+// queries are exact in one f16, and 16-bit outputs need 11 bits of the weights.
+template <int DK, int DV, int NT>
+cudaError_t launch_t(const Attn &a, cudaStream_t stream) {
+    if (a.q_type == GDN_DTYPE_F32) return launch<DK, DV, NT, true, true>(a, stream);
+    if (a.out_type == GDN_DTYPE_F32) return launch<DK, DV, NT, false, true>(a, stream);
+    return launch<DK, DV, NT, false, false>(a, stream);
+}
+
 template <int DK, int DV>
 cudaError_t launch_d(const Attn &a, cudaStream_t stream) {
-    const bool lo = a.q_type == GDN_DTYPE_F32;
-    if (rows_of(a.R) == 8) return lo ? launch<DK, DV, 1, true>(a, stream) : launch<DK, DV, 1, false>(a, stream);
-    return lo ? launch<DK, DV, 2, true>(a, stream) : launch<DK, DV, 2, false>(a, stream);
+    return rows_of(a.R) == 8 ? launch_t<DK, DV, 1>(a, stream) : launch_t<DK, DV, 2>(a, stream);
 }
 
 template <int DK>
@@ -761,15 +830,15 @@ cudaError_t launch_k(const Attn &a, cudaStream_t stream) {
     }
 }
 
-// Runs and workspace of a call; false where the tile count passes what the
-// schedule's 64-bit products hold.
+// Runs and workspace of a call; false where there are more tiles than a run's
+// 32-bit count takes (2^40 of them would fill no memory yet made).
 bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, int *W, size_t *bytes) {
     const long long R = (long long)(H / Hkv) * n_q;
     const int rows = rows_of(R);
     const long long n_rb = (R + rows - 1) / rows;
     unsigned long long units, all;
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
-        !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (1ull << 48))
+        !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (1ull << 40))
         return false;
     const int most = kGrid * warps_of(dk, dv, rows);
     *W = (int)(all < (unsigned long long)most ? all : (unsigned long long)most);

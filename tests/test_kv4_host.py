@@ -151,7 +151,7 @@ def test_runs_of_a_very_long_batch(H):
     T, W = 1 << 48, 2432
     for w in (0, 1, 1000, W - 1):
         at = H.kv4_run_begin(T, W, w)
-        assert at == T * w // W and H.kv4_run_of(T, W, at) == w
+        assert at == T // W * w + min(w, T % W) and H.kv4_run_of(T, W, at) == w
         assert H.kv4_run_of(T, W, H.kv4_run_begin(T, W, w + 1) - 1) == w
 
 
