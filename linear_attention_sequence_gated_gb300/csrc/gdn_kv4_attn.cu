@@ -53,13 +53,14 @@ constexpr int rows_of(long long R) { return R > 8 ? 16 : 8; }
 
 // Shape of the kernel for widths DK, DV and NT column tiles of rows.  Each warp
 // streams its run through a ring of its own in shared memory: stages of U tiles,
-// each tile one bulk copy.  16 warps where 128 registers a thread hold the output
-// tile, else 8.
-constexpr int warps_of(int dk, int dv, int rows) { return rows == 8 && dk <= 128 && dv <= 128 ? 16 : 8; }
+// each tile one bulk copy.  12 warps and steps of 4 tiles where 168 registers a
+// thread hold the output tile and two steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x
+// 128: 68 us; 16 warps with steps of 2 tiles 72, 8 warps with steps of 4 82.)
+constexpr int warps_of(int dk, int dv, int rows) { return rows == 8 && dk <= 128 && dv <= 128 ? 12 : 8; }
 template <int DK, int DV, int NT>
 struct Geo {
     static constexpr int WARPS = warps_of(DK, DV, 8 * NT);
-    static constexpr int U = 2;
+    static constexpr int U = WARPS == 12 ? 4 : 2;
     static constexpr int TB = tile_bytes(DK, DV);
     static constexpr int BUDGET = 216 * 1024;
     static constexpr int FIT = BUDGET / (WARPS * U * TB);
@@ -79,6 +80,12 @@ struct Attn {
     int q_type, out_type;
     bool causal;
 };
+
+// How the weights enter the MMAs.  kHi: 11 bits, for 16-bit outputs.  kHiLo: the
+// remainder's 11 bits in a second MMA.  kColumns: of at most 4 rows, the remainder
+// in the other 4 columns of the same MMA, where row r's queries stand again as
+// column r + 4; the two columns' outputs are added at the end.
+enum Weights { kHi = 0, kHiLo = 1, kColumns = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPBits = 12.f;         // probabilities are scaled by 2^12
@@ -196,7 +203,7 @@ __device__ __forceinline__ int find_tile(const Attn &a, int units, long long x, 
 template <int DV, int ROWS> constexpr size_t kPartial = (size_t)ROWS * (DV + 2);
 
 // One warp's share of one unit: an online softmax over tiles.
-template <int DK, int DV, int NT, bool QLO, bool PLO>
+template <int DK, int DV, int NT, bool QLO, int PM>
 struct Unit {
     static constexpr int U = Geo<DK, DV, NT>::U, TB = tile_bytes(DK, DV);
     static constexpr int CK = DK > 128 ? 2 : 1;        // key parts
@@ -219,7 +226,7 @@ struct Unit {
         uint4 raw_q[NT][CK][QW];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = rb * 8 * NT + nt * 8 + g;
+            const int row = PM == kColumns ? g & 3 : rb * 8 * NT + nt * 8 + g;
             const size_t q0 = ((size_t)(b * (size_t)a.H + hk * rep) * a.n_q + row) * DK;
             const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
                                                               (q0 + t * ST * 4) * (16 / QE));
@@ -274,7 +281,7 @@ struct Unit {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 f[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
-                const int mine = rb * 8 * NT + nt * 8 + 2 * t + r;
+                const int mine = PM == kColumns ? (2 * t + r) & 3 : rb * 8 * NT + nt * 8 + 2 * t + r;
                 qi[nt][r] = mine < a.R ? mine % a.n_q : -1;
                 m[nt][r] = -INFINITY;
                 l[nt][r] = 0.f;
@@ -340,7 +347,7 @@ struct Unit {
             }
         }
         const bool plain = pos + U * kTile <= min(all, stop) && good == (1u << U) - 1u;
-        uint32_t ph[U][NT][2], pl[PLO ? U : 1][NT][2];
+        uint32_t ph[U][NT][2], pl[PM == kHiLo ? U : 1][NT][2];
         float cf[NT][2];
         if (!plain) {
             const int raw = max(__ldg(a.c.lens + b), 0);
@@ -405,11 +412,16 @@ struct Unit {
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if constexpr (PLO) {
-                        split2(s[u][nt][2 * k], s[u][nt][2 * k + 1], ph[u][nt][k], pl[u][nt][k]);
+                    const float x = s[u][nt][2 * k], y = s[u][nt][2 * k + 1];
+                    if constexpr (PM == kHi) {
+                        ph[u][nt][k] = half2_bits(__floats2half2_rn(x, y));
+                    } else if constexpr (PM == kHiLo) {
+                        split2(x, y, ph[u][nt][k], pl[u][nt][k]);
                         pl[u][nt][k] = transpose8(pl[u][nt][k]);
                     } else {
-                        ph[u][nt][k] = half2_bits(__floats2half2_rn(s[u][nt][2 * k], s[u][nt][2 * k + 1]));
+                        uint32_t lo;
+                        split2(x, y, ph[u][nt][k], lo);
+                        if (t >= 2) ph[u][nt][k] = lo;
                     }
                     ph[u][nt][k] = transpose8(ph[u][nt][k]);
                 }
@@ -449,7 +461,7 @@ struct Unit {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float d[4];
-                    if constexpr (PLO) {
+                    if constexpr (PM == kHiLo) {
                         mma0(d, A[0], pl[0][nt][0], pl[0][nt][1]);
 #pragma unroll
                         for (int u = 1; u < U; ++u) mma(d, A[u], pl[u][nt][0], pl[u][nt][1]);
@@ -479,6 +491,13 @@ struct Unit {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 const int local = nt * 8 + 2 * t + r, row = rb * 8 * NT + local;
+                if constexpr (PM == kColumns) {
+#pragma unroll
+                    for (int i = 0; i < VB * 4; ++i) {
+                        o[nt][i][r] += __shfl_xor_sync(0xffffffffu, o[nt][i][r], 2);
+                        o[nt][i][r + 2] += __shfl_xor_sync(0xffffffffu, o[nt][i][r + 2], 2);
+                    }
+                }
                 if (row >= a.R) continue;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * rep + row / a.n_q) * DV;
@@ -521,7 +540,7 @@ struct Cursor {
     }
 };
 
-template <int DK, int DV, int NT, bool QLO, bool PLO>
+template <int DK, int DV, int NT, bool QLO, int PM>
 __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(const Attn a) {
     using G = Geo<DK, DV, NT>;
     constexpr int U = G::U, ST = G::STAGES;
@@ -581,7 +600,7 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) copy();
 
-    Unit<DK, DV, NT, QLO, PLO> unit;
+    Unit<DK, DV, NT, QLO, PM> unit;
     int get = 0;                                       // stage to read, and its barrier's phase
     uint32_t phase = 0;
     while (c.left > 0) {
@@ -776,16 +795,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
 
 // ------------------------------------------------------------------ host
 
-template <int DK, int DV, int NT, bool QLO, bool PLO>
+template <int DK, int DV, int NT, bool QLO, int PM>
 cudaError_t launch(const Attn &a, cudaStream_t stream) {
     using G = Geo<DK, DV, NT>;
     static PerDeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO, PM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
-    attn_kernel<DK, DV, NT, QLO, PLO><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
+    attn_kernel<DK, DV, NT, QLO, PM><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // few rows: a block each, so that long rows are shared out; many: a warp each
@@ -809,16 +828,15 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
 // queries are exact in one f16, and 16-bit outputs need 11 bits of the weights.
-template <int DK, int DV, int NT>
-cudaError_t launch_t(const Attn &a, cudaStream_t stream) {
-    if (a.q_type == GDN_DTYPE_F32) return launch<DK, DV, NT, true, true>(a, stream);
-    if (a.out_type == GDN_DTYPE_F32) return launch<DK, DV, NT, false, true>(a, stream);
-    return launch<DK, DV, NT, false, false>(a, stream);
-}
-
 template <int DK, int DV>
 cudaError_t launch_d(const Attn &a, cudaStream_t stream) {
-    return rows_of(a.R) == 8 ? launch_t<DK, DV, 1>(a, stream) : launch_t<DK, DV, 2>(a, stream);
+    const bool two = rows_of(a.R) > 8;
+    if (a.q_type == GDN_DTYPE_F32)
+        return two ? launch<DK, DV, 2, true, kHiLo>(a, stream) : launch<DK, DV, 1, true, kHiLo>(a, stream);
+    if (a.out_type != GDN_DTYPE_F32)
+        return two ? launch<DK, DV, 2, false, kHi>(a, stream) : launch<DK, DV, 1, false, kHi>(a, stream);
+    if (a.R <= 4) return launch<DK, DV, 1, false, kColumns>(a, stream);
+    return two ? launch<DK, DV, 2, false, kHiLo>(a, stream) : launch<DK, DV, 1, false, kHiLo>(a, stream);
 }
 
 template <int DK>
