@@ -268,47 +268,65 @@ def flash_attn(q, k, v, mask=None, scale=None, *, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ 4-bit cache
+#
+# A decode step makes these calls once a layer, so their host side is kept short:
+# no imports, context managers or Stream objects where the current device and
+# stream serve.
+
+_torch = None
+_KV4_DTYPES = {}
+
+
+def _kv4_torch():
+    """The torch module, and the library's codes of its dtypes filled in."""
+    global _torch
+    if _torch is None:
+        import torch
+        _KV4_DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+        _torch = torch
+    return _torch
+
 
 def _kv4_dtype(dtype, what):
-    import torch
-    dts = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-    if dtype not in dts:
+    code = _KV4_DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"{what} must be fp32, bf16 or fp16, got {dtype}")
-    return dts[dtype]
+    return code
 
 
-def _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, lens=None):
-    """Shapes, types and devices of a cache and what goes with it; its page size."""
-    import torch
+def _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, lens=None):
+    """Shapes, types and devices of a cache and what goes with it; its device's index."""
     if cache.dim() != 4 or cache.dtype != torch.uint8 or cache.shape[1] != Hkv \
             or cache.shape[3] != 9 * (dk + dv):
         raise ValueError(f"cache: expected (n_pages, {Hkv}, page_size / 16, {9 * (dk + dv)}) uint8, got "
                          f"{tuple(cache.shape)} {cache.dtype}")
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
+    int32 = torch.int32
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != int32:
         raise ValueError(f"page_table: expected ({B}, max_pages) int32, got {tuple(page_table.shape)} "
                          f"{page_table.dtype}")
-    for name, t in (("seq_lens", seq_lens), ("lens", lens)):
-        if t is not None and (tuple(t.shape) != (B,) or t.dtype != torch.int32):
-            raise ValueError(f"{name}: expected ({B},) int32, got {tuple(t.shape)} {t.dtype}")
-    for t in (cache, page_table, seq_lens, lens):
-        if t is not None:
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("cache, page_table and lengths must be contiguous CUDA tensors")
-            if t.device != cache.device:
-                raise ValueError("all tensors must be on one CUDA device")
-    return cache.shape[2] * 16
+    dev = cache.get_device()
+    for t in (seq_lens,) if lens is None else (seq_lens, lens):
+        if t.dim() != 1 or t.shape[0] != B or t.dtype != int32:
+            raise ValueError(f"lengths: expected ({B},) int32, got {tuple(t.shape)} {t.dtype}")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("lengths must be contiguous and on the cache's device")
+    if dev < 0 or page_table.get_device() != dev or not cache.is_contiguous() or not page_table.is_contiguous():
+        raise ValueError("cache and page_table must be contiguous CUDA tensors on one device")
+    return dev
 
 
-def _on(device, stream):
-    """Makes ``device`` current, and ``stream`` if one is given, so that what a
-    call allocates belongs to the stream that the call runs on."""
-    import contextlib
-    import torch
+def _kv4_call(torch, dev, stream, call):
+    """call(handle of the stream to run on), with ``dev`` current, and ``stream``
+    too if one is given, so that what the call allocates belongs to its stream."""
     if stream is not None:
-        return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        if stream.device.index != dev:
+            raise ValueError("stream must be on the tensors' device")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if dev == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def kv4_supports(head_dim_k: int, head_dim_v: int) -> bool:
@@ -321,7 +339,7 @@ def kv4_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, he
     """An empty 4-bit cache: (n_pages, n_heads_kv, page_size / 16, 9 (dk + dv))
     uint8, for keys of ``head_dim_k`` and values of ``head_dim_v`` (the same
     where it is not given).  page_size is a multiple of 16."""
-    import torch
+    torch = _kv4_torch()
     dv = head_dim_k if head_dim_v is None else head_dim_v
     if not kv4_supports(head_dim_k, dv):
         raise GdnError(ERR_HEADDIM, "kv4_cache")
@@ -343,25 +361,28 @@ def kv4_write(k, v, cache, page_table, seq_lens, new_lens=None, *, stream=None):
     written.  A page outside the cache shows as ERR_PAGE in device_status().
     The format and the rest of the contract are with gdn_kv4_write in
     include/gdn.h."""
-    L = lib()
+    L, torch = lib(), _kv4_torch()
     dt = _kv4_dtype(k.dtype, "k/v")
     if k.dim() != 4 or v.dim() != 4 or v.shape[:3] != k.shape[:3] or v.dtype != k.dtype:
         raise ValueError("k, v: expected (n_seqs, n_heads_kv, n_new, dk / dv) of one dtype, got "
                          f"{tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
     B, Hkv, T, dk = k.shape
     dv = v.shape[3]
-    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, new_lens)
-    for t in (k, v):
-        if t.device != cache.device:
-            raise ValueError("all tensors must be on one CUDA device")
-        if t.stride(3) != 1 and t.numel():
-            raise ValueError("rows of k and v must be contiguous")
-    strides = (ctypes.c_longlong * 6)(*k.stride()[:3], *v.stride()[:3])
-    with _on(cache.device, stream):
-        rc = L.gdn_kv4_write(k.data_ptr(), v.data_ptr(), strides, cache.data_ptr(), page_table.data_ptr(),
-                             seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, T,
-                             Hkv, dk, dv, cache.shape[0], page, page_table.shape[1], dt,
-                             _stream_handle(stream))
+    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, new_lens)
+    ks, vs = k.stride(), v.stride()
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("all tensors must be on one CUDA device")
+    if (ks[3] != 1 or vs[3] != 1) and k.numel():
+        raise ValueError("rows of k and v must be contiguous")
+    strides = None if k.is_contiguous() and v.is_contiguous() else \
+        (ctypes.c_longlong * 6)(ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+
+    def call(handle):
+        return L.gdn_kv4_write(k.data_ptr(), v.data_ptr(), strides, cache.data_ptr(), page_table.data_ptr(),
+                               seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, T,
+                               Hkv, dk, dv, cache.shape[0], cache.shape[2] * 16, page_table.shape[1], dt, handle)
+
+    rc = _kv4_call(torch, dev, stream, call)
     if rc != OK:
         raise GdnError(rc, "gdn_kv4_write")
     return cache
@@ -377,8 +398,7 @@ def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_d
     on and at negative positions are zeros.  With lens = seq_lens row i is
     position i.  ``dtype``: fp32, bf16 (default) or fp16; every value is exact
     in each."""
-    import torch
-    L = lib()
+    L, torch = lib(), _kv4_torch()
     dk, dv = int(head_dim_k), int(head_dim_k if head_dim_v is None else head_dim_v)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else torch.bfloat16
@@ -386,29 +406,28 @@ def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_d
     if cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("cache must be 4-D and page_table 2-D")
     B, Hkv = page_table.shape[0], cache.shape[1]
-    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv, lens)
-    with _on(cache.device, stream):
-        outs = []
-        for name, t, d in (("k_out", k_out, dk), ("v_out", v_out, dv)):
-            if t is None:
-                t = torch.empty((B, Hkv, n_tokens, d), dtype=dtype, device=cache.device)
-            elif tuple(t.shape) != (B, Hkv, n_tokens, d) or t.dtype != dtype or not t.is_contiguous() \
-                    or t.device != cache.device:
-                raise ValueError(f"{name} must be contiguous {(B, Hkv, n_tokens, d)} {dtype} on "
-                                 f"{cache.device}")
-            outs.append(t)
+    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, lens)
+    for name, t, d in (("k_out", k_out, dk), ("v_out", v_out, dv)):
+        if t is not None and (tuple(t.shape) != (B, Hkv, n_tokens, d) or t.dtype != dtype
+                              or not t.is_contiguous() or t.get_device() != dev):
+            raise ValueError(f"{name} must be contiguous {(B, Hkv, n_tokens, d)} {dtype} on the cache's device")
+
+    def call(handle):
+        k = torch.empty((B, Hkv, n_tokens, dk), dtype=dtype, device=cache.device) if k_out is None else k_out
+        v = torch.empty((B, Hkv, n_tokens, dv), dtype=dtype, device=cache.device) if v_out is None else v_out
         rc = L.gdn_kv4_read(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                            None if lens is None else lens.data_ptr(), outs[0].data_ptr(),
-                            outs[1].data_ptr(), B, n_tokens, Hkv, dk, dv, cache.shape[0], page,
-                            page_table.shape[1], dt, _stream_handle(stream))
-    if rc != OK:
-        raise GdnError(rc, "gdn_kv4_read")
-    return outs[0], outs[1]
+                            None if lens is None else lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, n_tokens,
+                            Hkv, dk, dv, cache.shape[0], cache.shape[2] * 16, page_table.shape[1], dt, handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_kv4_read")
+        return k, v
+
+    return _kv4_call(torch, dev, stream, call)
 
 
 def flash_attn_kv4_workspace_bytes(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, page_size,
                                    max_pages) -> int:
-    """Bytes that ``flash_attn_kv4`` needs as its ``workspace``."""
+    """Bytes that ``flash_attn_kv4`` needs as its ``workspace`` (0: none)."""
     return int(lib().gdn_flash_attn_kv4_workspace_bytes(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k,
                                                         head_dim_v, page_size, max_pages))
 
@@ -428,41 +447,42 @@ def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, s
     token are zeros.  ``workspace``: an optional uint8 CUDA tensor of
     flash_attn_kv4_workspace_bytes(...) bytes for one call at a time; without it
     the library allocates in stream order."""
-    import math
-    import torch
-    L = lib()
+    L, torch = lib(), _kv4_torch()
     dt = _kv4_dtype(q.dtype, "q")
     if q.dim() != 4 or cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q and cache must be 4-D and page_table 2-D")
     B, H, n_q, dk = q.shape
     dv = int(dk if head_dim_v is None else head_dim_v)
-    Hkv = cache.shape[1]
-    page = _kv4_check(cache, page_table, seq_lens, B, Hkv, dk, dv)
-    max_pages = page_table.shape[1]
+    Hkv, page, max_pages = cache.shape[1], cache.shape[2] * 16, page_table.shape[1]
+    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv)
     if mask is not None and (tuple(mask.shape) != (B, 1, n_q, max_pages * page) or mask.dtype != q.dtype):
         raise ValueError(f"mask: expected {(B, 1, n_q, max_pages * page)} {q.dtype}, got "
                          f"{tuple(mask.shape)} {mask.dtype}")
     for t in (q, mask, workspace):
-        if t is not None and (t.device != cache.device or not t.is_contiguous()):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("all tensors must be contiguous CUDA tensors on one device")
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.float32
+    if out is not None:
+        if out_dtype is None:
+            out_dtype = out.dtype
+        if tuple(out.shape) != (B, n_q, H, dv) or out.dtype != out_dtype or not out.is_contiguous() \
+                or out.get_device() != dev:
+            raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype} on the cache's device")
+    elif out_dtype is None:
+        out_dtype = torch.float32
     odt = _kv4_dtype(out_dtype, "out_dtype")
     if scale is None:
-        scale = 1.0 / math.sqrt(dk)
-    with _on(cache.device, stream):
-        if out is None:
-            out = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=cache.device)
-        elif tuple(out.shape) != (B, n_q, H, dv) or out.dtype != out_dtype or not out.is_contiguous() \
-                or out.device != cache.device:
-            raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype} on {cache.device}")
+        scale = dk ** -0.5
+
+    def call(handle):
+        o = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=cache.device) if out is None else out
         rc = L.gdn_flash_attn_kv4(
             q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-            None if mask is None else mask.data_ptr(), out.data_ptr(), B, H, Hkv, n_q, dk, dv,
-            cache.shape[0], page, max_pages, float(scale), int(causal), dt, odt,
+            None if mask is None else mask.data_ptr(), o.data_ptr(), B, H, Hkv, n_q, dk, dv, cache.shape[0],
+            page, max_pages, scale, 1 if causal else 0, dt, odt,
             None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream_handle(stream))
-    if rc != OK:
-        raise GdnError(rc, "gdn_flash_attn_kv4")
-    return out
+            0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_flash_attn_kv4")
+        return o
+
+    return _kv4_call(torch, dev, stream, call)

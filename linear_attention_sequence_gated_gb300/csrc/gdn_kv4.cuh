@@ -157,18 +157,14 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
 // How the attention's work is shared out: all tiles of all units (sequence, kv
 // head, row block), one after another, cut into equal runs, one a warp.
 // Run w of W over T tiles (W <= T, so none is empty): T / W of them, one more in the
-// first T % W runs; and the run of tile x.  64-bit divisions are long, and few calls
-// have that many tiles.
-__host__ __device__ inline long long quotient(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-__host__ __device__ inline long long run_begin(long long T, int W, int w) {
-    const long long each = quotient(T, W), more = T - each * W;
+// first T % W runs; and the run of tile x.
+__host__ __device__ inline int run_begin(int T, int W, int w) {
+    const int each = T / W, more = T - each * W;
     return each * w + (w < more ? w : more);
 }
-__host__ __device__ inline int run_of(long long T, int W, long long x) {
-    const long long each = quotient(T, W), more = T - each * W;
-    return (int)(x < (each + 1) * more ? quotient(x, each + 1) : more + quotient(x - (each + 1) * more, each));
+__host__ __device__ inline int run_of(int T, int W, int x) {
+    const int each = T / W, more = T - each * W, big = (each + 1) * more;
+    return x < big ? x / (each + 1) : more + (x - big) / each;
 }
 // A run that covers a unit in part leaves a partial result: in its slot 0 if
 // the unit began in an earlier run, in its slot 1 if it begins in this one (so

@@ -32,7 +32,8 @@
 // to itself writes its output; otherwise it leaves (max, sum, output) in the
 // workspace and a second kernel, launched as a programmatic dependent, joins the
 // parts in a fixed order (results do not depend on timing).  It also writes the
-// zero rows of empty sequences.
+// zero rows of empty sequences.  A call with few units of few tiles gives each unit
+// a CTA instead, whose warps join their parts in shared memory: one launch.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -47,6 +48,8 @@ namespace kv4 {
 namespace {
 
 constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for
+constexpr int kAloneTiles = 4;         // up to so many tiles a warp, and so many units, a unit has
+constexpr int kAloneUnits = 2 * kGrid; // a CTA to itself
 
 // Rows of a unit's block: 8 per MMA column tile.
 constexpr int rows_of(long long R) { return R > 8 ? 16 : 8; }
@@ -79,6 +82,7 @@ struct Attn {
     float scale;
     int q_type, out_type;
     bool causal;
+    bool alone;                        // a block a unit, and no partial results
 };
 
 // How the weights enter the MMAs.  kHi: 11 bits, for 16-bit outputs.  kHiLo: the
@@ -150,6 +154,16 @@ __device__ __forceinline__ void store8(void *out, int type, size_t i, const floa
     *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 2 consecutive outputs
+__device__ __forceinline__ void store2(void *out, int type, size_t i, float x, float y) {
+    if (type == GDN_DTYPE_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(out) + i) = make_float2(x, y);
+    else if (type == GDN_DTYPE_BF16)
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(out) + i) = __floats2bfloat162_rn(x, y);
+    else
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(out) + i) = __floats2half2_rn(x, y);
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 __device__ __forceinline__ long long warp_scan(long long n, int lane) {
@@ -160,43 +174,35 @@ __device__ __forceinline__ long long warp_scan(long long n, int lane) {
     }
     return n;
 }
-// Tiles of all units of sequence b; whole-warp sums over all sequences, and
-// over those before b.
-__device__ __forceinline__ long long tiles_at(const Attn &a, int b, int units) {
-    if (b >= a.n_seqs) return 0;
-    if (__ldg(a.c.lens + b) > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
-    return (long long)tiles_of(length(a.c, b)) * units;
+// Tiles of all units of sequence b.  Whole-warp: their total over the sequences
+// before `end`, and the sequence that tile x lies in with the tiles before it.
+__device__ __forceinline__ int tiles_at(const Attn &a, int b, int units) {
+    return b < a.n_seqs ? tiles_of(length(a.c, b)) * units : 0;
 }
-__device__ __forceinline__ long long total_tiles(const Attn &a, int units, int lane) {
-    long long n = 0;
-    for (int b = lane; b < a.n_seqs; b += 32) n += tiles_at(a, b, units);
+__device__ __forceinline__ int tiles_before(const Attn &a, int units, int end, int lane) {
+    int n = 0;
+    for (int b = lane; b < end; b += 32) n += tiles_at(a, b, units);
+    return __reduce_add_sync(0xffffffffu, n);
+}
+__device__ __forceinline__ int find_tile(const Attn &a, int units, int x, int lane, int *before) {
+    int done = 0;
+    for (int base = 0;; base += 32) {
+        const int n = tiles_at(a, base + lane, units);
+        int incl = n;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    return n;
-}
-__device__ __forceinline__ long long tiles_before(const Attn &a, int units, int b, int lane) {
-    long long n = 0;
-    for (int i = lane; i < b; i += 32) n += tiles_at(a, i, units);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    return n;
-}
-// The sequence that tile x lies in, and the tiles before that sequence.
-__device__ __forceinline__ int find_tile(const Attn &a, int units, long long x, int lane, long long *before) {
-    long long done = 0;
-    for (int base = 0; base < a.n_seqs; base += 32) {
-        const long long n = tiles_at(a, base + lane, units);
-        const long long incl = warp_scan(n, lane) + done;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        incl += done;
         const unsigned hit = __ballot_sync(0xffffffffu, incl > x);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
+        if (hit || base + 32 >= a.n_seqs) {            // (x is below the total, so there is one)
+            const int src = hit ? __ffs(hit) - 1 : 31;
             *before = __shfl_sync(0xffffffffu, incl - n, src);
-            return base + src;
+            return min(base + src, a.n_seqs - 1);
         }
         done = __shfl_sync(0xffffffffu, incl, 31);
     }
-    *before = done;                    // not reached: x is below the total
-    return a.n_seqs - 1;
 }
 
 // A partial result: [rows][DV] outputs, [rows] maxima, [rows] sums.
@@ -480,9 +486,8 @@ struct Unit {
     }
 
     // The unit's rows: outputs where this warp saw all of its tiles, else a partial.
-    __device__ __forceinline__ void end(const Attn &a, int b, int hk, int rb, bool whole, int slot, int lane) {
+    __device__ __forceinline__ void end(const Attn &a, int b, int hk, int rb, bool whole, float *part, int lane) {
         const int g = lane >> 2, t = lane & 3, rep = a.H / a.c.Hkv;
-        float *part = a.ws + (size_t)slot * kPartial<DV, 8 * NT>;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -554,20 +559,31 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
     if (lane == 0) ptx::fence_mbar_init();
     __syncthreads();
     const int units = a.c.Hkv * a.n_rb;
-    const long long T = total_tiles(a, units, lane);
-    const int W = (int)min((long long)a.W, T);
-    // neighbouring runs on different SMs: few tiles spread over the GPU
-    const int w = warp * gridDim.x + blockIdx.x;
-    if (w >= W) return;
-    const long long at = run_begin(T, W, w);
-    long long before;
     Cursor c;
-    c.left = (int)(run_begin(T, W, w + 1) - at);
-    c.b = find_tile(a, units, at, lane, &before);
-    c.len = length(a.c, c.b);
-    c.n = tiles_of(c.len);
-    c.u = (int)quotient(at - before, c.n);
-    c.j = (int)(at - before - (long long)c.u * c.n);
+    int w = 0, parts = 0;                              // this run's number; runs of the block's own unit
+    if (a.alone) {
+        c.b = blockIdx.x / units;
+        c.u = blockIdx.x - c.b * units;
+        c.len = length(a.c, c.b);
+        c.n = tiles_of(c.len);
+        parts = min(G::WARPS, c.n);
+        c.j = warp < parts ? run_begin(c.n, parts, warp) : 0;
+        c.left = warp < parts ? run_begin(c.n, parts, warp + 1) - c.j : 0;
+    } else {
+        const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+        // neighbouring runs on different SMs: few tiles spread over the GPU
+        w = warp * gridDim.x + blockIdx.x;
+        if (w >= W) return;
+        const int at = run_begin(T, W, w);
+        int before;
+        c.left = run_begin(T, W, w + 1) - at;
+        c.b = find_tile(a, units, at, lane, &before);
+        c.len = length(a.c, c.b);
+        c.n = tiles_of(c.len);
+        c.u = (at - before) / c.n;
+        c.j = at - before - c.u * c.n;
+    }
+    if (c.left > 0 && lane == 0 && __ldg(a.c.lens + c.b) > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
 
     uint8_t *ring = smem + warp * G::RING;
     // Copies run ST - 1 stages ahead.  The tiles' addresses are looked up for a
@@ -619,15 +635,46 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
                     get = get + 1 == ST ? 0 : get + 1;
                     phase ^= get == 0;
                 } while (get != put);
-                return;
+                c.left = 0;
+                break;
             }
             unit.tiles(a, ring + get * U * G::TB, b, j * kTile, stop, good[warp][get], lane);
             __syncwarp();                              // the stage is read
             get = get + 1 == ST ? 0 : get + 1;
             phase ^= get == 0;
         }
-        unit.end(a, b, hk, rb, j0 == 0 && j1 == c.n, partial_slot(w, j0 == 0), lane);
+        if (a.alone) break;
+        const bool whole = j0 == 0 && j1 == c.n;
+        unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * kPartial<DV, 8 * NT>, lane);
         c.step(a, units, j1 - j0);
+    }
+    if (!a.alone) return;
+
+    // The block's own unit: its warps' parts meet in the rings' shared memory.
+    __syncthreads();
+    const int b = blockIdx.x / units, u = blockIdx.x - b * units, hk = u / a.n_rb, rb = u - hk * a.n_rb;
+    float *part = reinterpret_cast<float *>(smem);
+    if (warp < parts) unit.end(a, b, hk, rb, parts == 1, part + warp * kPartial<DV, 8 * NT>, lane);
+    if (parts == 1) return;
+    __syncthreads();
+    const int n_rows = min(8 * NT, a.R - rb * 8 * NT);
+    for (int i = threadIdx.x; i < n_rows * (DV / 4); i += G::WARPS * 32) {
+        const int local = i / (DV / 4), x = i - local * (DV / 4), row = rb * 8 * NT + local;
+        const float *m = part + 8 * NT * DV + local, *l = m + 8 * NT;
+        float top = -INFINITY, sum = 0.f;
+        for (int k = 0; k < parts; ++k) top = fmaxf(top, m[k * kPartial<DV, 8 * NT>]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; ++k) {
+            const float wt = exp2_approx((m[k * kPartial<DV, 8 * NT>] - base) * kLog2e);
+            const float4 v = reinterpret_cast<const float4 *>(part + k * kPartial<DV, 8 * NT> + local * DV)[x];
+            sum = fmaf(l[k * kPartial<DV, 8 * NT>], wt, sum);
+            y = make_float4(fmaf(v.x, wt, y.x), fmaf(v.y, wt, y.y), fmaf(v.z, wt, y.z), fmaf(v.w, wt, y.w));
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV + 4 * x;
+        store2(a.out, a.out_type, at, y.x * inv, y.y * inv);
+        store2(a.out, a.out_type, at + 2, y.z * inv, y.w * inv);
     }
 }
 
@@ -703,40 +750,31 @@ struct Join {
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-                const size_t i = at + column(c, e, lane);
-                const float u = x[c * V + e] * inv, v = x[c * V + e + 1] * inv;
-                if (a.out_type == GDN_DTYPE_F32)
-                    *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + i) = make_float2(u, v);
-                else if (a.out_type == GDN_DTYPE_BF16)
-                    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) =
-                        __floats2bfloat162_rn(u, v);
-                else
-                    *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(u, v);
+                store2(a.out, a.out_type, at + column(c, e, lane), x[c * V + e] * inv, x[c * V + e + 1] * inv);
             }
     }
 };
 
 template <int DV, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, long long n_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, int n_rows) {
     __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.c.Hkv * a.n_rb;
-    const long long T = total_tiles(a, units, lane);
-    const int W = (int)min((long long)a.W, T);
-    auto place = [&](long long r, int &local) {        // where a row's output goes
-        const int row = (int)(r % a.R), hk = (int)(r / a.R % a.c.Hkv), b = (int)(r / a.R / a.c.Hkv);
+    const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+    auto place = [&](int r, int &local) {              // where a row's output goes
+        const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         local = row % ROWS;
         return (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV;
     };
-    const long long r0 = (long long)blockIdx.x * rpb, r = r0 + warp;
+    const int r0 = blockIdx.x * rpb, r = r0 + warp;
     int w0 = 0, n = -1;                                // runs that share the row; -1: none of ours
     if (warp < rpb && r < n_rows) {
-        const int row = (int)(r % a.R), hk = (int)(r / a.R % a.c.Hkv), b = (int)(r / a.R / a.c.Hkv);
+        const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         const int tiles = tiles_of(length(a.c, b));
         n = 0;
         if (tiles > 0) {
-            const long long first = tiles_before(a, units, b, lane) + (long long)(hk * a.n_rb + row / ROWS) * tiles;
+            const int first = tiles_before(a, units, b, lane) + (hk * a.n_rb + row / ROWS) * tiles;
             w0 = run_of(T, W, first);
             n = run_of(T, W, first + tiles - 1) - w0 + 1;
         }
@@ -804,14 +842,15 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
-    attn_kernel<DK, DV, NT, QLO, PM><<<kGrid, G::WARPS * 32, G::SMEM, stream>>>(a);
+    const int grid = a.alone ? a.n_seqs * a.c.Hkv * a.n_rb : kGrid;
+    attn_kernel<DK, DV, NT, QLO, PM><<<grid, G::WARPS * 32, G::SMEM, stream>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.alone) return e;
     // few rows: a block each, so that long rows are shared out; many: a warp each
-    const long long n_rows = (long long)a.n_seqs * a.c.Hkv * a.R;
+    const int n_rows = a.n_seqs * a.c.Hkv * a.R;
     const int rpb = (int)(n_rows >= 2 * kGrid * kJoinWarps ? kJoinWarps : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((n_rows + rpb - 1) / rpb));
+    cfg.gridDim = dim3(((unsigned)n_rows + rpb - 1) / rpb);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
@@ -848,19 +887,25 @@ cudaError_t launch_k(const Attn &a, cudaStream_t stream) {
     }
 }
 
-// Runs and workspace of a call; false where there are more tiles than a run's
-// 32-bit count takes (2^40 of them would fill no memory yet made).
-bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, int *W, size_t *bytes) {
+// How a call is shared out.  False where the page tables have room for 2^31 tiles
+// (over all kv heads and row blocks): tiles are counted in 32 bits.
+struct Plan {
+    int W;                             // runs at most
+    bool alone;
+    size_t bytes;                      // of workspace
+};
+bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, Plan *p) {
     const long long R = (long long)(H / Hkv) * n_q;
-    const int rows = rows_of(R);
+    const int rows = rows_of(R), warps = warps_of(dk, dv, rows);
     const long long n_rb = (R + rows - 1) / rows;
     unsigned long long units, all;
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
-        !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (1ull << 40))
+        !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
         return false;
-    const int most = kGrid * warps_of(dk, dv, rows);
-    *W = (int)(all < (unsigned long long)most ? all : (unsigned long long)most);
-    *bytes = (size_t)*W * 2 * (size_t)rows * (dv + 2) * sizeof(float);
+    // few units of few tiles: a block each, whose warps meet in shared memory
+    p->alone = tiles <= kAloneTiles * warps && units <= kAloneUnits;
+    p->W = (int)(all < (unsigned long long)(kGrid * warps) ? all : (unsigned long long)(kGrid * warps));
+    p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)rows * (dv + 2) * sizeof(float);
     return true;
 }
 
@@ -877,15 +922,14 @@ extern "C" {
 size_t gdn_flash_attn_kv4_workspace_bytes(int n_seqs, int n_heads, int n_heads_kv, int n_q, int head_dim_k,
                                           int head_dim_v, int page_size, int max_pages) {
     using namespace gdn::kv4;
-    int W;
-    size_t bytes;
+    Plan p;
     if (!sizes_ok(n_seqs, n_heads, n_heads_kv, n_q) || n_seqs == 0 || n_heads == 0 || max_pages <= 0 ||
         page_size < kTile || page_size % kTile != 0 || !gdn_flash_attn_supports(n_q, head_dim_k, head_dim_v) ||
         (long long)max_pages * page_size > INT_MAX - 64 ||
         !plan(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v,
-              (long long)max_pages * (page_size / kTile), &W, &bytes))
+              (long long)max_pages * (page_size / kTile), &p))
         return 0;
-    return bytes;
+    return p.bytes;
 }
 
 int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, const int *seq_lens,
@@ -928,11 +972,10 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cap == 0)                                      // no room for a token: every row is zero
         return cudaMemsetAsync(out, 0, out_bytes, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-    int W;
-    size_t need;
-    if (!plan(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, cap / kTile, &W, &need))
-        return GDN_ERR_ARG;
-    if (workspace) {
+    Plan p;
+    if (!plan(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, cap / kTile, &p)) return GDN_ERR_ARG;
+    const size_t need = p.bytes;
+    if (workspace && need) {
         if (workspace_bytes < need || !aligned(workspace, 256)) return GDN_ERR_WORKSPACE;
         const Range rw = range_of(workspace, need);
         for (Range r : {ro, rc_, rt, rl, rq, rm})
@@ -941,7 +984,8 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
     int *status = gdn::status_word();
     if (!status) return GDN_ERR_CUDA;
     void *ws = workspace;
-    if (!ws) {
+    const bool owned = !ws && need;
+    if (owned) {
         cudaMemPool_t pool = gdn::workspace_pool();
         if (!pool) return GDN_ERR_CUDA;
         if (cudaMallocFromPoolAsync(&ws, need, pool, st) != cudaSuccess) return GDN_ERR_NOMEM;
@@ -950,14 +994,14 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
     const Attn a{{static_cast<uint8_t *>(const_cast<void *>(cache)), page_table, seq_lens, status, n_pages,
                   n_heads_kv, page_size / kTile, max_pages, head_dim_k, head_dim_v},
                  q, mask, out, static_cast<float *>(ws), n_seqs, n_heads, n_q, R,
-                 (R + rows_of(R) - 1) / rows_of(R), W, scale, dtype, out_dtype, causal != 0};
+                 (R + rows_of(R) - 1) / rows_of(R), p.W, scale, dtype, out_dtype, causal != 0, p.alone};
     cudaError_t e;
     switch (head_dim_k) {
         case 64: e = launch_k<64>(a, st); break;
         case 128: e = launch_k<128>(a, st); break;
         default: e = launch_k<256>(a, st); break;
     }
-    if (!workspace) {
+    if (owned) {
         const cudaError_t f = cudaFreeAsync(ws, st);
         if (e == cudaSuccess) e = f;
     }

@@ -24,8 +24,8 @@ void kv4_scale_bytes(const float *a, int n, int *out) {
     for (int i = 0; i < n; ++i) out[i] = gdn::kv4::scale_byte(a[i]);
 }
 
-long long kv4_run_begin(long long T, int W, int w) { return gdn::kv4::run_begin(T, W, w); }
-int kv4_run_of(long long T, int W, long long x) { return gdn::kv4::run_of(T, W, x); }
+int kv4_run_begin(int T, int W, int w) { return gdn::kv4::run_begin(T, W, w); }
+int kv4_run_of(int T, int W, int x) { return gdn::kv4::run_of(T, W, x); }
 int kv4_partial_slot(int w, int begins_here) { return gdn::kv4::partial_slot(w, begins_here != 0); }
 
 }  // extern "C"

@@ -33,9 +33,6 @@ def H(tmp_path_factory):
                                                           "-o", so, os.path.join(ROOT, "tests", "kv4_host.cu")])
     lib = ctypes.CDLL(so)
     lib.kv4_tile_offset.restype = ctypes.c_longlong
-    lib.kv4_run_begin.restype = ctypes.c_longlong
-    lib.kv4_run_begin.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
-    lib.kv4_run_of.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong]
     return lib
 
 
@@ -148,7 +145,7 @@ def test_runs_share_out_every_tile_and_their_parts_join(H, units, most):
 
 
 def test_runs_of_a_very_long_batch(H):
-    T, W = 1 << 48, 2432
+    T, W = 2 ** 31 - 1, 1824
     for w in (0, 1, 1000, W - 1):
         at = H.kv4_run_begin(T, W, w)
         assert at == T // W * w + min(w, T % W) and H.kv4_run_of(T, W, at) == w
@@ -271,9 +268,11 @@ def attend(L, **kw):
     (dict(mask=BASE + 300 * MB + 1), gdn.ERR_ALIGN), (dict(cache=BASE + 128 * MB + 4), gdn.ERR_ALIGN),
     (dict(out=BASE), gdn.ERR_ALIAS), (dict(out=BASE + 128 * MB + 64), gdn.ERR_ALIAS),
     (dict(out=BASE + 256 * MB), gdn.ERR_ALIAS), (dict(mask=BASE + 264 * MB), gdn.ERR_ALIAS),
-    (dict(ws=BASE + 512 * MB, ws_bytes=64), gdn.ERR_WORKSPACE),
-    (dict(ws=BASE + 512 * MB + 16, ws_bytes=1 << 30), gdn.ERR_WORKSPACE),
-    (dict(ws=BASE, ws_bytes=1 << 30), gdn.ERR_ALIAS), (dict(ws=BASE + 264 * MB, ws_bytes=1 << 30), gdn.ERR_ALIAS),
+    (dict(max_pages=100, ws=BASE + 512 * MB, ws_bytes=64), gdn.ERR_WORKSPACE),
+    (dict(max_pages=100, ws=BASE + 512 * MB + 16, ws_bytes=1 << 30), gdn.ERR_WORKSPACE),
+    (dict(max_pages=100, ws=BASE, ws_bytes=1 << 30), gdn.ERR_ALIAS),
+    (dict(max_pages=100, ws=BASE + 264 * MB, ws_bytes=1 << 30), gdn.ERR_ALIAS),
+    (dict(B=1 << 12, H=8, Hkv=8, page=16, max_pages=1 << 20, table=1 << 50), gdn.ERR_ARG),     # 2^35 tiles
     (dict(B=1 << 20, H=1 << 12, Hkv=1), gdn.ERR_ARG),                # more rows than the join has blocks
 ])
 def test_attention_refuses(L, kw, code):
@@ -288,10 +287,12 @@ def test_attention_with_nothing_to_do(L):
 
 
 def test_attention_workspace_sizes(L):
-    ok = (2, 8, 2, 1, 128, 128, 64, 4)
+    ok = (2, 8, 2, 1, 128, 128, 64, 40)
     assert L.gdn_flash_attn_kv4_workspace_bytes(*ok) > 0
+    # few short sequences: one kernel, no workspace
+    assert L.gdn_flash_attn_kv4_workspace_bytes(2, 8, 2, 1, 128, 128, 64, 4) == 0
     # never more than the grid's runs ask for, however long the cache
-    assert L.gdn_flash_attn_kv4_workspace_bytes(64, 32, 8, 1, 128, 128, 64, 1 << 20) < 64 << 20
+    assert L.gdn_flash_attn_kv4_workspace_bytes(64, 32, 8, 1, 128, 128, 64, 1 << 16) < 64 << 20
     for i, bad in ((0, 0), (0, -1), (1, 0), (2, 3), (3, 0), (3, 20), (4, 96), (5, 32), (6, 24), (7, 0), (7, 1 << 26)):
         a = list(ok)
         a[i] = bad
