@@ -16,6 +16,7 @@
 // sequence and one warp, so no other thread writes it meanwhile.
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
@@ -42,93 +43,131 @@ struct Run {
     bool wide;                         // rows are 32-byte aligned
 };
 
-template <typename T> __device__ __forceinline__ float to_f32(T x);
-template <> __device__ __forceinline__ float to_f32(float x) { return x; }
-template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <> __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+// N elements of a row in registers as they stand in memory: whole 32-byte words
+// where the rows are 32-byte aligned.
+template <typename T, int N>
+struct Raw {
+    static constexpr int W = N * (int)sizeof(T) / 4;
+    uint32_t w[W];
 
-struct Words8 {
-    uint32_t w[8];
+    __device__ __forceinline__ void load(const T *p, bool wide) {
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p) + i;
+            if (W >= 8 && wide) {
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]),
+                               "=r"(w[(i + 4) % W]), "=r"(w[(i + 5) % W]), "=r"(w[(i + 6) % W]),
+                               "=r"(w[(i + 7) % W]) : "l"(q));
+            } else {
+#pragma unroll
+                for (int j = i; j < i + 8 && j < W; j += 4) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(q + j - i);
+                    w[j] = a.x; w[j + 1] = a.y; w[j + 2] = a.z; w[j + 3] = a.w;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p, bool wide) const {
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            uint32_t *q = reinterpret_cast<uint32_t *>(p) + i;
+            if (W >= 8 && wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(w[i]),
+                             "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[(i + 4) % W]),
+                             "r"(w[(i + 5) % W]), "r"(w[(i + 6) % W]), "r"(w[(i + 7) % W]) : "memory");
+            } else {
+#pragma unroll
+                for (int j = i; j < i + 8 && j < W; j += 4)
+                    *reinterpret_cast<uint4 *>(q + j - i) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        else return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w[i / 2] >> 16 : w[i / 2])));
+    }
+    // Bits of the largest magnitude: of floats without sign, integer order is theirs,
+    // with infinities and then NaNs at the top.
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return max(m & 0xffffu, m >> 16);
+        }
+    }
+    static constexpr uint32_t INF = sizeof(T) == 4 ? 0x7f800000u
+                                                   : std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    // NaN to 0 and infinities to the largest number: the cache holds finite numbers
+    // only, so that a token that a mask hides cannot spoil a row.
+    __device__ __forceinline__ void finite() {
+        constexpr uint32_t MAG = sizeof(T) == 4 ? 0x7fffffffu : 0x7fffu;
+        constexpr int PER = 4 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            uint32_t x = 0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const uint32_t y = sizeof(T) == 4 ? w[i] : (w[i] >> (16 * e)) & 0xffffu, m = y & MAG;
+                x |= (m < INF ? y : (m == INF ? y - 1 : 0u)) << (16 * e);
+            }
+            w[i] = x;
+        }
+    }
+    __device__ __forceinline__ float top_value(uint32_t bits) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(bits << 16);
+        else return __half2float(__ushort_as_half((unsigned short)bits));
+    }
+    // The largest magnitude, after making every element finite.
+    __device__ __forceinline__ float amax() {
+        uint32_t m = top();
+        if (m >= INF) {
+            finite();
+            m = top();
+        }
+        return top_value(m);
+    }
 };
-__device__ __forceinline__ Words8 load32(const void *p, bool wide) {
-    Words8 x;
-    if (wide) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]),
-                       "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7]) : "l"(p));
-    } else {
-        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
-        x = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-    }
-    return x;
-}
-__device__ __forceinline__ void store32(void *p, const Words8 &x, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]),
-                     "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]),
-                     "r"(x.w[7]) : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(x.w[4], x.w[5], x.w[6], x.w[7]);
-    }
-}
 
-// N (8 or 16) consecutive elements of a row as fp32, a NaN as 0: the cache
-// holds finite numbers only, so a token that a mask hides cannot spoil a row.
+// A group's scale and what divides by it.
+struct Scale {
+    int byte;
+    float s, r;
+    __device__ __forceinline__ explicit Scale(float a) {
+        byte = scale_byte(a);
+        s = scale_value(byte);
+        r = byte ? __frcp_rn(s) : 0.f;
+    }
+    template <typename T>
+    __device__ __forceinline__ float ratio(float x) const {
+        return sizeof(T) == 4 ? ratio32(x, r, s) : ratio16(x, r);
+    }
+};
+
+// f16 pairs of values to a row's type, exact in each
 template <typename T, int N>
-__device__ __forceinline__ void load_row(const T *p, bool wide, float (&x)[N]) {
-    if constexpr (N * sizeof(T) == 16) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const T *e = reinterpret_cast<const T *>(&a);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+__device__ __forceinline__ void put(Raw<T, N> &x, int i, uint32_t pair) {   // elements i, i + 1 (i even)
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pair));
+    if constexpr (sizeof(T) == 4) {
+        x.w[i] = __float_as_uint(f.x);
+        x.w[i + 1] = __float_as_uint(f.y);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        x.w[i / 2] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
     } else {
-        constexpr int PER = 32 / (int)sizeof(T);
-#pragma unroll
-        for (int j = 0; j < N / PER; ++j) {
-            const Words8 a = load32(p + j * PER, wide);
-            const T *e = reinterpret_cast<const T *>(&a);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) x[j * PER + i] = to_f32(e[i]);
-        }
+        x.w[i / 2] = pair;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
-}
-
-template <typename T> __device__ __forceinline__ T from_f32(float x);
-template <> __device__ __forceinline__ float from_f32(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
-
-// N (8 or 16) consecutive elements of a row; every value is exact in T.
-template <typename T, int N>
-__device__ __forceinline__ void store_row(T *p, bool wide, const float (&x)[N]) {
-    if constexpr (N * sizeof(T) == 16) {
-        uint4 a;
-        T *e = reinterpret_cast<T *>(&a);
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = from_f32<T>(x[i]);
-        *reinterpret_cast<uint4 *>(p) = a;
-    } else {
-        constexpr int PER = 32 / (int)sizeof(T);
-#pragma unroll
-        for (int j = 0; j < N / PER; ++j) {
-            Words8 a;
-            T *e = reinterpret_cast<T *>(&a);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) e[i] = from_f32<T>(x[j * PER + i]);
-            store32(p + j * PER, a, wide);
-        }
-    }
-}
-
-template <int N>
-__device__ __forceinline__ float amax(const float (&x)[N]) {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) a = fmaxf(a, fabsf(x[i]));
-    return a;
 }
 
 // What a warp works on.
@@ -138,163 +177,177 @@ struct Part : Place {
     int chunk;                         // which 128 elements
 };
 
-// Parts are numbered with the tile's parts innermost (they share a tile), then
-// kv heads, then tiles.
-__device__ __forceinline__ bool part_of(const Run &r, Part &p) {
-    const int kc = r.c.dk > 128 ? 2 : 1, vc = r.c.dv > 128 ? 2 : 1, n = kc + vc;
-    long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int x = (int)(i % n);
-    i /= n;
+// blockIdx.y is the sequence (and those gridDim.y further on); the warps of the
+// blocks in x are numbered with a tile's parts innermost, then kv heads, then tiles.
+__device__ __forceinline__ bool part_of(const Run &r, int b, Part &p) {
+    const unsigned kc = r.c.dk > 128 ? 2 : 1, vc = r.c.dv > 128 ? 2 : 1, n = kc + vc;
+    const unsigned i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned unit = i / n, x = i - unit * n, j = unit / r.c.Hkv;
     p.value = x >= kc;
     p.chunk = p.value ? x - kc : x;
-    p.h = (int)(i % r.c.Hkv);
-    i /= r.c.Hkv;
-    const int j = (int)(i % r.n_tiles);
-    i /= r.n_tiles;
-    if (i >= r.n_seqs) return false;
-    p.b = (int)i;
-    const int raw = max(__ldg(r.c.lens + p.b), 0), cap = capacity(r.c);
+    p.h = unit - j * r.c.Hkv;
+    p.b = b;
+    if (j >= (unsigned)r.n_tiles) return false;
+    const int raw = max(__ldg(r.c.lens + b), 0), cap = capacity(r.c);
     if (raw > cap) *r.c.status = GDN_ERR_PAGE;
-    const int count = r.counts ? min(max(__ldg(r.counts + p.b), 0), r.T) : r.T;
+    const int count = r.counts ? min(max(__ldg(r.counts + b), 0), r.T) : r.T;
     static_cast<Place &>(p) = place_of(raw, cap, count, j);
     return true;
 }
 
-// One part of the write: W = 64 or 128 elements.
+// One part of the write: W = 64 or 128 elements of 16 tokens.  Row loads are issued
+// before the page table is looked at.
 template <typename T, int W>
-__device__ __forceinline__ void write_keys(const Run &r, const Part &p, uint8_t *tile, int lane) {
-    constexpr int G = W / 16;          // scale groups, one a lane
-    uint8_t *codes = tile + p.chunk * 16 * (W / 2), *scales = tile + 8 * r.c.dk + p.chunk * 16 * G;
+__device__ __forceinline__ void write_keys(const Run &r, const Part &p, int lane) {
+    constexpr int G = W / 16, M = G / 2;   // groups a row (one a lane), passes over the tokens
     const T *k = static_cast<const T *>(r.k) + p.b * r.ks.seq + p.h * r.ks.head + p.chunk * W;
+    const int g = lane % G;
+    Raw<T, 16> x[M];
+    bool in[M];
 #pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-        const int tok = (lane + 32 * i) / G, g = lane % G;
-        const int t = p.t0 + tok;
-        if (!p.present(t)) continue;
-        float x[16];
-        load_row<T, 16>(k + t * r.ks.token + g * 16, r.wide, x);
-        const int sb = scale_byte(amax(x));
-        const float s = scale_value(sb);
-        uint32_t w[2] = {0, 0};
+    for (int i = 0; i < M; ++i) {
+        const int t = p.t0 + (lane + 32 * i) / G;
+        in[i] = p.present(t);
+        if (in[i]) x[i].load(k + t * r.ks.token + g * 16, r.wide);
+    }
+    uint8_t *tile = tile_ptr(r.c, p.b, p.h, p.tile);
+    if (!tile) return;
+    uint8_t *codes = tile + p.chunk * 16 * (W / 2), *scales = tile + 8 * r.c.dk + p.chunk * 16 * G;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            w[e / 4] |= encode2(ratio(x[2 * e], s), ratio(x[2 * e + 1], s)) << (8 * (e % 4));
+    for (int i = 0; i < M; ++i) {
+        if (!in[i]) continue;
+        const int tok = (lane + 32 * i) / G;
+        const Scale s(x[i].amax());
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = s.ratio<T>(x[i].get(8 * h + e));
+            w[h] = encode8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+        }
         *reinterpret_cast<uint2 *>(codes + tok * (W / 2) + g * 8) = make_uint2(w[0], w[1]);
-        scales[tok * G + g] = (uint8_t)sb;
+        scales[tok * G + g] = (uint8_t)s.byte;
     }
 }
 
 template <typename T, int W>
-__device__ __forceinline__ void write_values(const Run &r, const Part &p, uint8_t *tile, int lane) {
+__device__ __forceinline__ void write_values(const Run &r, const Part &p, int lane) {
     constexpr int N = W / 8;           // elements of a lane
     const int g = lane >> 2, t4 = lane & 3;
     const T *v = static_cast<const T *>(r.v) + p.b * r.vs.seq + p.h * r.vs.head + p.chunk * W + g * N;
-    float x[4][N];
-    int sb[4];
+    Raw<T, N> x[4];
     uint32_t keep = 0, keep_s = 0;     // what the tile already has: nibbles of a word, scale bytes
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = p.t0 + 4 * t4 + i;
         if (p.present(t)) {
-            load_row<T, N>(v + t * r.vs.token, r.wide, x[i]);
+            x[i].load(v + t * r.vs.token, r.wide);
         } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[i][e] = 0.f;
+            x[i].zero();
             keep |= 0x0f0fu << (4 * (i & 1) + 16 * (i >> 1));
             keep_s |= 0xffu << (8 * i);
         }
     }
-    // width 64: a group of 16 spans two lanes, g and g ^ 1, which hold the same tokens
-    float s[4];
+    uint8_t *tile = tile_ptr(r.c, p.b, p.h, p.tile);
+    if (!tile) return;                 // (the whole warp's)
+    uint4 *codes = reinterpret_cast<uint4 *>(tile + 9 * r.c.dk + p.chunk * 1024) + g * 4 + t4;
+    const int group = W == 64 ? g >> 1 : p.chunk * 8 + g;
+    uint32_t *scales = reinterpret_cast<uint32_t *>(tile + 9 * r.c.dk + 8 * r.c.dv + group * 16 + 4 * t4);
+    uint4 had[W / 64];
+    uint32_t had_s = 0;
+    if (keep) {
+#pragma unroll
+        for (int q = 0; q < W / 64; ++q) had[q] = codes[q * 32];
+        had_s = *scales;
+    }
+    float a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float a = amax(x[i]);
-        if constexpr (W == 64) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
-        sb[i] = scale_byte(a);
-        s[i] = scale_value(sb[i]);
+        a[i] = x[i].amax();
+        // width 64: a group of 16 spans two lanes, g and g ^ 1, which hold the same tokens
+        if constexpr (W == 64) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], 4));
     }
     if (keep_s == 0xffffffffu) return;
-    uint32_t w[W / 16];                // word i: elements 2i, 2i + 1 of the four tokens
-#pragma unroll
-    for (int i = 0; i < W / 16; ++i) {
-        w[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int el = 2 * i + (e & 1), k0 = 2 * (e >> 1);
-            w[i] |= encode2(ratio(x[k0][el], s[k0]), ratio(x[k0 + 1][el], s[k0 + 1])) << (8 * e);
-        }
-    }
-    uint8_t *part = tile + 9 * r.c.dk + p.chunk * 1024;
+    const Scale s[4] = {Scale(a[0]), Scale(a[1]), Scale(a[2]), Scale(a[3])};
 #pragma unroll
     for (int q = 0; q < W / 64; ++q) {
-        uint4 *dst = reinterpret_cast<uint4 *>(part + ((q * 8 + g) * 4 + t4) * 16);
-        uint4 a = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-        if (keep) {
-            const uint4 o = *dst;
-            a.x |= o.x & keep; a.y |= o.y & keep; a.z |= o.z & keep; a.w |= o.w & keep;
+        uint32_t w[4];                 // a word: elements e, e + 1 of the four tokens
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 8 * q + 2 * i;
+            float y[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[k][0] = s[k].template ratio<T>(x[k].get(e));
+                y[k][1] = s[k].template ratio<T>(x[k].get(e + 1));
+            }
+            w[i] = encode8(y[0][0], y[1][0], y[0][1], y[1][1], y[2][0], y[3][0], y[2][1], y[3][1]);
         }
-        *dst = a;
+        if (keep) {
+            w[0] = (w[0] & ~keep) | (had[q].x & keep);
+            w[1] = (w[1] & ~keep) | (had[q].y & keep);
+            w[2] = (w[2] & ~keep) | (had[q].z & keep);
+            w[3] = (w[3] & ~keep) | (had[q].w & keep);
+        }
+        codes[q * 32] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (W == 128 || !(g & 1)) {
-        const int group = W == 64 ? g >> 1 : p.chunk * 8 + g;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(tile + 9 * r.c.dk + 8 * r.c.dv + group * 16 + 4 * t4);
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (!(keep_s >> (8 * i) & 1)) a |= (uint32_t)sb[i] << (8 * i);
-        if (keep_s) a |= *dst & keep_s;
-        *dst = a;
+        const uint32_t b = (uint32_t)s[0].byte | (uint32_t)s[1].byte << 8 | (uint32_t)s[2].byte << 16 |
+                           (uint32_t)s[3].byte << 24;
+        *scales = (b & ~keep_s) | (had_s & keep_s);
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) write_kernel(const Run r) {
-    Part p;
-    if (!part_of(r, p)) return;
-    if (!p.held()) return;
-    uint8_t *tile = tile_ptr(r.c, p.b, p.h, p.tile);
-    if (!tile) return;
     const int lane = threadIdx.x & 31;
-    if (p.value) {
-        if (r.c.dv == 64) write_values<T, 64>(r, p, tile, lane);
-        else write_values<T, 128>(r, p, tile, lane);
-    } else {
-        if (r.c.dk == 64) write_keys<T, 64>(r, p, tile, lane);
-        else write_keys<T, 128>(r, p, tile, lane);
+    for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
+        Part p;
+        if (!part_of(r, b, p) || !p.held()) continue;
+        if (p.value) {
+            if (r.c.dv == 64) write_values<T, 64>(r, p, lane);
+            else write_values<T, 128>(r, p, lane);
+        } else {
+            if (r.c.dk == 64) write_keys<T, 64>(r, p, lane);
+            else write_keys<T, 128>(r, p, lane);
+        }
     }
 }
 
 // One part of the read: rows of tokens that are not there are zeros.
 template <typename T, int W>
 __device__ __forceinline__ void read_keys(const Run &r, const Part &p, const uint8_t *tile, int lane) {
-    constexpr int G = W / 16;
+    constexpr int G = W / 16, M = G / 2;
     const uint8_t *codes = tile + p.chunk * 16 * (W / 2), *scales = tile + 8 * r.c.dk + p.chunk * 16 * G;
     T *k = static_cast<T *>(r.k) + p.b * r.ks.seq + p.h * r.ks.head + p.chunk * W;
+    const int g = lane % G;
+    uint2 w[M];
+    uint32_t s[M];
 #pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-        const int tok = (lane + 32 * i) / G, g = lane % G;
-        const int t = p.t0 + tok;
-        if (t < 0 || t >= r.T) continue;
-        float x[16];
-        if (tile && p.present(t)) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(codes + tok * (W / 2) + g * 8);
-            const float s = scale_value(scales[tok * G + g]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t h[4];
-                decode4(j ? w.y : w.x, h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-                    x[8 * j + 2 * e] = f.x * s;
-                    x[8 * j + 2 * e + 1] = f.y * s;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    for (int i = 0; i < M; ++i) {
+        const int tok = (lane + 32 * i) / G;
+        w[i] = make_uint2(0, 0);
+        s[i] = 0;
+        if (tile && p.present(p.t0 + tok)) {
+            w[i] = *reinterpret_cast<const uint2 *>(codes + tok * (W / 2) + g * 8);
+            s[i] = scales[tok * G + g];
         }
-        store_row<T, 16>(k + t * r.ks.token + g * 16, r.wide, x);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const int t = p.t0 + (lane + 32 * i) / G;
+        if (t < 0 || t >= r.T) continue;
+        const uint32_t sc = s[i] << 7 | s[i] << 23;
+        Raw<T, 16> x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t h[4];
+            decode4(j ? w[i].y : w[i].x, h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put<T, 16>(x, 8 * j + 2 * e, mul2(h[e], sc));
+        }
+        x.store(k + t * r.ks.token + g * 16, r.wide);
     }
 }
 
@@ -303,56 +356,60 @@ __device__ __forceinline__ void read_values(const Run &r, const Part &p, const u
     constexpr int N = W / 8;
     const int g = lane >> 2, t4 = lane & 3;
     T *v = static_cast<T *>(r.v) + p.b * r.vs.seq + p.h * r.vs.head + p.chunk * W + g * N;
-    float x[4][N];
+    const uint8_t *part = tile + 9 * r.c.dk + p.chunk * 1024;
+    uint4 w4[W / 64];
     uint32_t sw = 0;
+#pragma unroll
+    for (int q = 0; q < W / 64; ++q) {
+        w4[q] = make_uint4(0, 0, 0, 0);
+        if (tile) w4[q] = *reinterpret_cast<const uint4 *>(part + ((q * 8 + g) * 4 + t4) * 16);
+    }
     if (tile) {
         const int group = W == 64 ? g >> 1 : p.chunk * 8 + g;
         sw = *reinterpret_cast<const uint32_t *>(tile + 9 * r.c.dk + 8 * r.c.dv + group * 16 + 4 * t4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)    // absent tokens: zeros, whatever their bytes say
+            if (!p.present(p.t0 + 4 * t4 + i)) sw &= ~(0xffu << (8 * i));
     }
-    const uint8_t *part = tile + 9 * r.c.dk + p.chunk * 1024;
+    // pairs of tokens to pairs of elements
+    Raw<T, N> x[4];
 #pragma unroll
     for (int q = 0; q < W / 64; ++q) {
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (tile) a = *reinterpret_cast<const uint4 *>(part + ((q * 8 + g) * 4 + t4) * 16);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        const uint32_t w[4] = {w4[q].x, w4[q].y, w4[q].z, w4[q].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
             decode4(w[i], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-                x[2 * (e >> 1)][8 * q + 2 * i + (e & 1)] = f.x;
-                x[2 * (e >> 1) + 1][8 * q + 2 * i + (e & 1)] = f.y;
-            }
+            const uint32_t s01 = scales01(sw), s23 = scales23(sw);
+            const uint32_t a0 = mul2(h[0], s01), a1 = mul2(h[1], s01), b0 = mul2(h[2], s23), b1 = mul2(h[3], s23);
+            const int e = 8 * q + 2 * i;
+            put<T, N>(x[0], e, __byte_perm(a0, a1, 0x5410));
+            put<T, N>(x[1], e, __byte_perm(a0, a1, 0x7632));
+            put<T, N>(x[2], e, __byte_perm(b0, b1, 0x5410));
+            put<T, N>(x[3], e, __byte_perm(b0, b1, 0x7632));
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = p.t0 + 4 * t4 + i;
-        if (t < 0 || t >= r.T) continue;
-        const bool in = tile && p.present(t);
-        const float s = in ? scale_value((sw >> (8 * i)) & 0xff) : 0.f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[i][e] = in ? x[i][e] * s : 0.f;
-        store_row<T, N>(v + t * r.vs.token, r.wide, x[i]);
+        if (t >= 0 && t < r.T) x[i].store(v + t * r.vs.token, r.wide);
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) read_kernel(const Run r) {
-    Part p;
-    if (!part_of(r, p)) return;
-    if (p.t0 >= r.T) return;
-    const uint8_t *tile = nullptr;
-    if (p.held()) tile = tile_ptr(r.c, p.b, p.h, p.tile);
     const int lane = threadIdx.x & 31;
-    if (p.value) {
-        if (r.c.dv == 64) read_values<T, 64>(r, p, tile, lane);
-        else read_values<T, 128>(r, p, tile, lane);
-    } else {
-        if (r.c.dk == 64) read_keys<T, 64>(r, p, tile, lane);
-        else read_keys<T, 128>(r, p, tile, lane);
+    for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
+        Part p;
+        if (!part_of(r, b, p) || p.t0 >= r.T) continue;
+        const uint8_t *tile = p.held() ? tile_ptr(r.c, p.b, p.h, p.tile) : nullptr;
+        if (p.value) {
+            if (r.c.dv == 64) read_values<T, 64>(r, p, tile, lane);
+            else read_values<T, 128>(r, p, tile, lane);
+        } else {
+            if (r.c.dk == 64) read_keys<T, 64>(r, p, tile, lane);
+            else read_keys<T, 128>(r, p, tile, lane);
+        }
     }
 }
 
@@ -401,7 +458,7 @@ bool strided_bytes(const Strides &s, int n_seqs, int Hkv, int T, int d, unsigned
 }
 
 template <typename T>
-cudaError_t launch(bool write, const Run &r, unsigned blocks, cudaStream_t stream) {
+cudaError_t launch(bool write, const Run &r, dim3 blocks, cudaStream_t stream) {
     if (write) write_kernel<T><<<blocks, kWarps * 32, 0, stream>>>(r);
     else read_kernel<T><<<blocks, kWarps * 32, 0, stream>>>(r);
     return cudaGetLastError();
@@ -451,17 +508,14 @@ int run(bool write, void *k, void *v, const long long *strides, uint8_t *cache, 
     }
     const int n_tiles = (int)(((long long)T + 2 * kTile - 2) / kTile);
     const long long parts = (dk > 128 ? 2 : 1) + (dv > 128 ? 2 : 1);
-    unsigned long long items;
-    if (!mul_ok((unsigned long long)n_seqs * (unsigned long long)Hkv,
-                (unsigned long long)n_tiles * (unsigned long long)parts, &items) ||
-        items > (unsigned long long)INT_MAX * kWarps)
-        return GDN_ERR_ARG;
+    const long long items = (long long)n_tiles * Hkv * parts;      // of a sequence
+    if (items > INT_MAX) return GDN_ERR_ARG;
     int *status = status_word();
     if (!status) return GDN_ERR_CUDA;
     const bool wide = all % 32 == 0 && aligned(k, 32) && aligned(v, 32);
     const Run r{{cache, table, lens, status, n_pages, Hkv, page_size / kTile, max_pages, dk, dv},
                 counts, k, v, ks, vs, n_seqs, T, n_tiles, wide};
-    const unsigned blocks = (unsigned)((items + kWarps - 1) / kWarps);
+    const dim3 blocks((unsigned)((items + kWarps - 1) / kWarps), (unsigned)(n_seqs < 65535 ? n_seqs : 65535));
     cudaError_t e;
     if (dtype == GDN_DTYPE_BF16) e = launch<__nv_bfloat16>(write, r, blocks, stream);
     else if (dtype == GDN_DTYPE_F16) e = launch<__half>(write, r, blocks, stream);

@@ -141,18 +141,34 @@ __host__ __device__ inline int scale_byte(float a) {
     return c;
 }
 
-// x / s as the conversion to 4 bits takes it.  The quotient is correctly
-// rounded, so it is a border between two codes only where x / s itself is one
-// (a border times s is exact in fp32), and ties go to the even code.
-__device__ __forceinline__ float ratio(float x, float s) { return s > 0.f ? __fdiv_rn(x, s) : x * 0.f; }
-
-// Two codes in a byte (lo in the low nibble), rounded to nearest even, at most 6.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
-        : "=r"(r) : "f"(lo), "f"(hi));
-    return r;
+// x / s as the conversion to 4 bits takes it, with r = 1 / s rounded (0 for s = 0).
+// All that counts is on which side of the seven borders between codes it falls, or
+// that it is one of them (ties go to the even code; a border times s is exact).
+// 16-bit x: a quotient off a border is off by 2^-13 or more, and x r is within 2^-20
+// of the quotient (at most 7 of interest), so rounding x r to multiples of 2^-13,
+// by adding and subtracting 1.5 * 2^10, leaves it on its side and borders exact.
+__host__ __device__ inline float ratio16(float x, float r) { return fmaf(x, r, 1536.f) - 1536.f; }
+// fp32 x: the correctly rounded quotient (the last step of P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990, for a
+// correctly rounded reciprocal), which is a border only where x / s is.
+__host__ __device__ inline float ratio32(float x, float r, float s) {
+    const float y = x * r;
+    return fmaf(fmaf(-y, s, x), r, y);
 }
+
+#ifdef __CUDACC__
+// Eight codes, the first in the lowest nibble: rounded to nearest even, at most 6.
+__device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                            float x7) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w) : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
+    return w;
+}
+#endif
 
 // How the attention's work is shared out: all tiles of all units (sequence, kv
 // head, row block), one after another, cut into equal runs, one a warp.

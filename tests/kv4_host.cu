@@ -24,6 +24,11 @@ void kv4_scale_bytes(const float *a, int n, int *out) {
     for (int i = 0; i < n; ++i) out[i] = gdn::kv4::scale_byte(a[i]);
 }
 
+// quotients by scale `byte` as the conversion to 4 bits takes them
+void kv4_ratios(const float *x, int n, int byte, int wide, float *out) {
+    const float s = gdn::kv4::scale_value(byte), r = 1.f / s;
+    for (int i = 0; i < n; ++i) out[i] = wide ? gdn::kv4::ratio32(x[i], r, s) : gdn::kv4::ratio16(x[i], r);
+}
 int kv4_run_begin(int T, int W, int w) { return gdn::kv4::run_begin(T, W, w); }
 int kv4_run_of(int T, int W, int x) { return gdn::kv4::run_of(T, W, x); }
 int kv4_partial_slot(int w, int begins_here) { return gdn::kv4::partial_slot(w, begins_here != 0); }

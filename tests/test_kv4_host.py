@@ -85,6 +85,29 @@ def test_scale_bytes_round_as_the_oracle(H):
     assert np.array_equal(out, want)
 
 
+def fall(y, m, s):
+    """On which side of the borders m (times s) the values y (or rows y * s) fall, as -1, 0, 1."""
+    return np.sign(y[:, None].astype(np.float64) - np.asarray(m, dtype=np.float64) * s)
+
+
+def test_quotients_fall_where_the_values_do(H):
+    """Every f16 and bf16 value under every scale, and fp32 values around each border: the quotient is on the side of
+    each border between codes where the value is of the border times the scale, and on it where it is."""
+    borders = (kv4.LEVELS[1:] + kv4.LEVELS[:-1]) / 2
+    x16 = np.concatenate([np.arange(1, 0x7c00, dtype=np.uint16).view(np.float16).astype(np.float32),
+                          (np.arange(1, 0x7f80, dtype=np.uint32) << 16).view(np.float32)])
+    for byte, s in enumerate(kv4.SCALES):
+        if byte == 0:
+            continue
+        near = (borders * s).astype(np.float32)
+        x32 = (near.view(np.int32)[:, None] + np.arange(-40, 41)).astype(np.int32).view(np.float32).ravel()
+        for wide, x in ((0, x16[x16 < 7 * s]), (1, x32)):
+            x = np.ascontiguousarray(x)
+            y = np.zeros_like(x)
+            H.kv4_ratios(ctypes.c_void_p(x.ctypes.data), x.size, byte, wide, ctypes.c_void_p(y.ctypes.data))
+            assert np.array_equal(fall(y, borders, 1), fall(x, borders, s))
+
+
 def test_pages_outside_the_cache_have_no_offset(H):
     assert H.kv4_tile_offset(0, 5, 3, 2, 4, 1, 2304) == (2 * 4 + 1) * 2304
     assert H.kv4_tile_offset(4, 5, 3, 2, 4, 3, 2304) == ((4 * 3 + 2) * 4 + 3) * 2304
