@@ -3,7 +3,8 @@
 //
 // Both are streams: a write reads e bytes an element (2 or 4) and writes 9/16,
 // a read the other way round, so HBM bounds them.  One warp takes one part of
-// up to 128 elements of one tile (16 tokens of one kv head), keys or values:
+// one tile (16 tokens of one kv head), up to 128 elements of the tokens' keys or
+// values (a write: of 8 tokens' keys):
 //   * a key lane takes one scale group (16 elements) of a token: it reads and
 //     writes whole 32-byte sectors of the rows, 8 code bytes and a scale byte,
 //     and finds its scale without a shuffle;
@@ -13,7 +14,7 @@
 // A tile that a write covers in part (the first and last of a run; every tile
 // of a decode step) keeps its other tokens: key lanes of those tokens do not
 // store, value lanes merge nibbles with what is there.  A tile belongs to one
-// sequence and one warp, so no other thread writes it meanwhile.
+// sequence and each of its bytes to one lane, so no other thread writes it meanwhile.
 #include <climits>
 #include <cstdint>
 #include <type_traits>
@@ -26,7 +27,9 @@ namespace gdn {
 namespace kv4 {
 namespace {
 
-constexpr int kWarps = 4;              // warps of a block, each with a part of its own
+constexpr int kWarps = 4;              // warps of a block, each with parts of its own
+constexpr int kGroup = 4;              // tiles of a warp in a call of kManyParts parts or more
+constexpr long long kManyParts = 4 * 152 * 32;
 
 struct Strides {
     long long seq, head, token;        // in elements; the row itself is contiguous
@@ -40,6 +43,7 @@ struct Run {
     void *k, *v;                       // rows: read by a write, written by a read
     Strides ks, vs;
     int n_seqs, T, n_tiles;            // n_tiles: tiles that T tokens can touch
+    int group;                         // tiles of a warp
     bool wide;                         // rows are 32-byte aligned
 };
 
@@ -93,18 +97,21 @@ struct Raw {
             return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
         else return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w[i / 2] >> 16 : w[i / 2])));
     }
-    // Bits of the largest magnitude: of floats without sign, integer order is theirs,
-    // with infinities and then NaNs at the top.
+    // Bits of the largest magnitude: infinity's, or above for a NaN, where there is one.
     __device__ __forceinline__ uint32_t top() const {
-        uint32_t m = 0;
         if constexpr (sizeof(T) == 4) {
+            uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7fffffffu);
             return m;
         } else {
+            using T2 = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+            const T2 *x = reinterpret_cast<const T2 *>(w);
+            T2 m = __habs2(x[0]);
 #pragma unroll
-            for (int i = 0; i < W; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-            return max(m & 0xffffu, m >> 16);
+            for (int i = 1; i < W; ++i) m = __hmax2_nan(m, __habs2(x[i]));
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(&m);
+            return max(u & 0xffffu, u >> 16);
         }
     }
     static constexpr uint32_t INF = sizeof(T) == 4 ? 0x7f800000u
@@ -141,20 +148,30 @@ struct Raw {
     }
 };
 
-// A group's scale and what divides by it.
+// A group's scale and what divides by it, for elements of type T.
+template <typename T>
 struct Scale {
     int byte;
     float s, r;
     __device__ __forceinline__ explicit Scale(float a) {
-        byte = scale_byte(a);
+        byte = sizeof(T) == 4 ? scale_byte(a) : scale_byte16(a);
         s = scale_value(byte);
-        r = byte ? __frcp_rn(s) : 0.f;
-    }
-    template <typename T>
-    __device__ __forceinline__ float ratio(float x) const {
-        return sizeof(T) == 4 ? ratio32(x, r, s) : ratio16(x, r);
+        if (sizeof(T) == 4) r = __frcp_rn(s);
+        else asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        if (byte == 0) r = 0.f;
     }
 };
+template <typename T>
+__device__ __forceinline__ void ratios(float &x, float &y, const Scale<T> &sx, const Scale<T> &sy) {
+    if constexpr (sizeof(T) == 4) {
+        x = ratio32(x, sx.r, sx.s);
+        y = ratio32(y, sy.r, sy.s);
+    } else {
+        // (the packed forms of these two instructions were slower: register pairs, spills)
+        x = ratio16(x, sx.r);
+        y = ratio16(y, sy.r);
+    }
+}
 
 // f16 pairs of values to a row's type, exact in each
 template <typename T, int N>
@@ -170,28 +187,42 @@ __device__ __forceinline__ void put(Raw<T, N> &x, int i, uint32_t pair) {   // e
     }
 }
 
-// What a warp works on.
+// Parts of a tile, each of up to 128 elements: values of 16 tokens, keys of 16 (read)
+// or 8 (write: more loads in flight for the registers they take).
+__host__ __device__ constexpr unsigned key_parts(int dk, bool write) { return (dk > 128 ? 2 : 1) * (write ? 2 : 1); }
+__host__ __device__ constexpr unsigned parts_of(int dk, int dv, bool write) {
+    return key_parts(dk, write) + (dv > 128 ? 2 : 1);
+}
+
+// What a warp works on: a part of r.group tiles in a row.
 struct Part : Place {
     int b, h;                          // sequence, kv head
     bool value;                        // values (else keys)
     int chunk;                         // which 128 elements
+    int half;                          // of a written tile's keys: 0 or 8, the first of the tokens
+    __device__ __forceinline__ void next() {
+        ++tile;
+        t0 += kTile;
+    }
 };
 
 // blockIdx.y is the sequence (and those gridDim.y further on); the warps of the
 // blocks in x are numbered with a tile's parts innermost, then kv heads, then tiles.
+template <bool WRITE>
 __device__ __forceinline__ bool part_of(const Run &r, int b, Part &p) {
-    const unsigned kc = r.c.dk > 128 ? 2 : 1, vc = r.c.dv > 128 ? 2 : 1, n = kc + vc;
+    const unsigned kc = key_parts(r.c.dk, WRITE), n = parts_of(r.c.dk, r.c.dv, WRITE);
     const unsigned i = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const unsigned unit = i / n, x = i - unit * n, j = unit / r.c.Hkv;
     p.value = x >= kc;
-    p.chunk = p.value ? x - kc : x;
+    p.chunk = p.value ? x - kc : WRITE ? x >> 1 : x;
+    p.half = WRITE ? 8 * (x & 1) : 0;
     p.h = unit - j * r.c.Hkv;
     p.b = b;
-    if (j >= (unsigned)r.n_tiles) return false;
+    if (j * r.group >= (unsigned)r.n_tiles) return false;
     const int raw = max(__ldg(r.c.lens + b), 0), cap = capacity(r.c);
     if (raw > cap) *r.c.status = GDN_ERR_PAGE;
     const int count = r.counts ? min(max(__ldg(r.counts + b), 0), r.T) : r.T;
-    static_cast<Place &>(p) = place_of(raw, cap, count, j);
+    static_cast<Place &>(p) = place_of(raw, cap, count, j * r.group);
     return true;
 }
 
@@ -199,14 +230,14 @@ __device__ __forceinline__ bool part_of(const Run &r, int b, Part &p) {
 // before the page table is looked at.
 template <typename T, int W>
 __device__ __forceinline__ void write_keys(const Run &r, const Part &p, int lane) {
-    constexpr int G = W / 16, M = G / 2;   // groups a row (one a lane), passes over the tokens
+    constexpr int G = W / 16, M = G / 4;   // groups a row (one a lane), passes over 8 tokens
     const T *k = static_cast<const T *>(r.k) + p.b * r.ks.seq + p.h * r.ks.head + p.chunk * W;
     const int g = lane % G;
     Raw<T, 16> x[M];
     bool in[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        const int t = p.t0 + (lane + 32 * i) / G;
+        const int t = p.t0 + p.half + (lane + 32 * i) / G;
         in[i] = p.present(t);
         if (in[i]) x[i].load(k + t * r.ks.token + g * 16, r.wide);
     }
@@ -216,14 +247,18 @@ __device__ __forceinline__ void write_keys(const Run &r, const Part &p, int lane
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         if (!in[i]) continue;
-        const int tok = (lane + 32 * i) / G;
-        const Scale s(x[i].amax());
+        const int tok = p.half + (lane + 32 * i) / G;
+        const Scale<T> s(x[i].amax());
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = s.ratio<T>(x[i].get(8 * h + e));
+            for (int e = 0; e < 8; e += 2) {
+                y[e] = x[i].get(8 * h + e);
+                y[e + 1] = x[i].get(8 * h + e + 1);
+                ratios(y[e], y[e + 1], s, s);
+            }
             w[h] = encode8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
         }
         *reinterpret_cast<uint2 *>(codes + tok * (W / 2) + g * 8) = make_uint2(w[0], w[1]);
@@ -254,13 +289,7 @@ __device__ __forceinline__ void write_values(const Run &r, const Part &p, int la
     uint4 *codes = reinterpret_cast<uint4 *>(tile + 9 * r.c.dk + p.chunk * 1024) + g * 4 + t4;
     const int group = W == 64 ? g >> 1 : p.chunk * 8 + g;
     uint32_t *scales = reinterpret_cast<uint32_t *>(tile + 9 * r.c.dk + 8 * r.c.dv + group * 16 + 4 * t4);
-    uint4 had[W / 64];
-    uint32_t had_s = 0;
-    if (keep) {
-#pragma unroll
-        for (int q = 0; q < W / 64; ++q) had[q] = codes[q * 32];
-        had_s = *scales;
-    }
+    const uint32_t had_s = keep ? *scales : 0;
     float a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -269,28 +298,38 @@ __device__ __forceinline__ void write_values(const Run &r, const Part &p, int la
         if constexpr (W == 64) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], 4));
     }
     if (keep_s == 0xffffffffu) return;
-    const Scale s[4] = {Scale(a[0]), Scale(a[1]), Scale(a[2]), Scale(a[3])};
-#pragma unroll
+    const Scale<T> s[4] = {Scale<T>(a[0]), Scale<T>(a[1]), Scale<T>(a[2]), Scale<T>(a[3])};
+    // (not unrolled: registers decide how many warps keep loads in flight)
+#pragma unroll 1
     for (int q = 0; q < W / 64; ++q) {
         uint32_t w[4];                 // a word: elements e, e + 1 of the four tokens
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = 8 * q + 2 * i;
             float y[4][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[k][0] = s[k].template ratio<T>(x[k].get(e));
-                y[k][1] = s[k].template ratio<T>(x[k].get(e + 1));
-            }
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) y[k][e] = x[k].get(2 * i + e);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ratios(y[k][e], y[k + 1][e], s[k], s[k + 1]);
             w[i] = encode8(y[0][0], y[1][0], y[0][1], y[1][1], y[2][0], y[3][0], y[2][1], y[3][1]);
         }
         if (keep) {
-            w[0] = (w[0] & ~keep) | (had[q].x & keep);
-            w[1] = (w[1] & ~keep) | (had[q].y & keep);
-            w[2] = (w[2] & ~keep) | (had[q].z & keep);
-            w[3] = (w[3] & ~keep) | (had[q].w & keep);
+            const uint4 had = codes[q * 32];
+            w[0] = (w[0] & ~keep) | (had.x & keep);
+            w[1] = (w[1] & ~keep) | (had.y & keep);
+            w[2] = (w[2] & ~keep) | (had.z & keep);
+            w[3] = (w[3] & ~keep) | (had.w & keep);
         }
         codes[q * 32] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (W == 128) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < Raw<T, N>::W / 2; ++i) x[k].w[i] = x[k].w[i + Raw<T, N>::W / 2];
+        }
     }
     if (W == 128 || !(g & 1)) {
         const uint32_t b = (uint32_t)s[0].byte | (uint32_t)s[1].byte << 8 | (uint32_t)s[2].byte << 16 |
@@ -300,17 +339,21 @@ __device__ __forceinline__ void write_values(const Run &r, const Part &p, int la
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) write_kernel(const Run r) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 8) write_kernel(const Run r) {
     const int lane = threadIdx.x & 31;
     for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
         Part p;
-        if (!part_of(r, b, p) || !p.held()) continue;
-        if (p.value) {
-            if (r.c.dv == 64) write_values<T, 64>(r, p, lane);
-            else write_values<T, 128>(r, p, lane);
-        } else {
-            if (r.c.dk == 64) write_keys<T, 64>(r, p, lane);
-            else write_keys<T, 128>(r, p, lane);
+        if (!part_of<true>(r, b, p)) continue;
+#pragma unroll 1
+        for (int n = 0; n < r.group; ++n, p.next()) {
+            if (!p.held()) continue;
+            if (p.value) {
+                if (r.c.dv == 64) write_values<T, 64>(r, p, lane);
+                else write_values<T, 128>(r, p, lane);
+            } else {
+                if (r.c.dk == 64) write_keys<T, 64>(r, p, lane);
+                else write_keys<T, 128>(r, p, lane);
+            }
         }
     }
 }
@@ -397,18 +440,21 @@ __device__ __forceinline__ void read_values(const Run &r, const Part &p, const u
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(const Run r) {
+__global__ void __launch_bounds__(kWarps * 32, 8) read_kernel(const Run r) {
     const int lane = threadIdx.x & 31;
     for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
         Part p;
-        if (!part_of(r, b, p) || p.t0 >= r.T) continue;
-        const uint8_t *tile = p.held() ? tile_ptr(r.c, p.b, p.h, p.tile) : nullptr;
-        if (p.value) {
-            if (r.c.dv == 64) read_values<T, 64>(r, p, tile, lane);
-            else read_values<T, 128>(r, p, tile, lane);
-        } else {
-            if (r.c.dk == 64) read_keys<T, 64>(r, p, tile, lane);
-            else read_keys<T, 128>(r, p, tile, lane);
+        if (!part_of<false>(r, b, p)) continue;
+#pragma unroll 1
+        for (int n = 0; n < r.group && p.t0 < r.T; ++n, p.next()) {
+            const uint8_t *tile = p.held() ? tile_ptr(r.c, p.b, p.h, p.tile) : nullptr;
+            if (p.value) {
+                if (r.c.dv == 64) read_values<T, 64>(r, p, tile, lane);
+                else read_values<T, 128>(r, p, tile, lane);
+            } else {
+                if (r.c.dk == 64) read_keys<T, 64>(r, p, tile, lane);
+                else read_keys<T, 128>(r, p, tile, lane);
+            }
         }
     }
 }
@@ -507,14 +553,16 @@ int run(bool write, void *k, void *v, const long long *strides, uint8_t *cache, 
         if (overlap(rk, rv)) return GDN_ERR_ALIAS;
     }
     const int n_tiles = (int)(((long long)T + 2 * kTile - 2) / kTile);
-    const long long parts = (dk > 128 ? 2 : 1) + (dv > 128 ? 2 : 1);
-    const long long items = (long long)n_tiles * Hkv * parts;      // of a sequence
+    // one tile a warp while that leaves the GPU short of warps, else several in a row
+    const long long each = (long long)Hkv * parts_of(dk, dv, write);
+    const int group = (long long)n_seqs * n_tiles * each >= kManyParts ? kGroup : 1;
+    const long long items = (n_tiles + group - 1) / group * each;  // of a sequence
     if (items > INT_MAX) return GDN_ERR_ARG;
     int *status = status_word();
     if (!status) return GDN_ERR_CUDA;
     const bool wide = all % 32 == 0 && aligned(k, 32) && aligned(v, 32);
     const Run r{{cache, table, lens, status, n_pages, Hkv, page_size / kTile, max_pages, dk, dv},
-                counts, k, v, ks, vs, n_seqs, T, n_tiles, wide};
+                counts, k, v, ks, vs, n_seqs, T, n_tiles, group, wide};
     const dim3 blocks((unsigned)((items + kWarps - 1) / kWarps), (unsigned)(n_seqs < 65535 ? n_seqs : 65535));
     cudaError_t e;
     if (dtype == GDN_DTYPE_BF16) e = launch<__nv_bfloat16>(write, r, blocks, stream);

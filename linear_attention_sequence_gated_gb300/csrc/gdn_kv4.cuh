@@ -25,6 +25,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -141,11 +142,28 @@ __host__ __device__ inline int scale_byte(float a) {
     return c;
 }
 
+// The same for the largest magnitude of f16 or bf16 elements, whose sixth is a border
+// or off it by 2^-13 of itself (2^-27 below 2^-14): the product with 2^-112 / 6 has a
+// 16-bit float's exponent, so its bits from 20 on are the byte before rounding, and
+// rounding them to multiples of 16 first makes borders exact (the product is within 2
+// of them, and others are hundreds off).
+__host__ __device__ inline int scale_byte16(float a) {
+    const float t = fminf(a, kMaxValue) * 0x1.555556p-115f;
+#ifdef __CUDA_ARCH__
+    uint32_t u = __float_as_uint(t);
+#else
+    uint32_t u;
+    memcpy(&u, &t, 4);
+#endif
+    u = (u + 8u) & ~15u;
+    return (int)((u + 0x7ffffu + (u >> 20 & 1u)) >> 20);
+}
+
 // x / s as the conversion to 4 bits takes it, with r = 1 / s rounded (0 for s = 0).
 // All that counts is on which side of the seven borders between codes it falls, or
 // that it is one of them (ties go to the even code; a border times s is exact).
-// 16-bit x: a quotient off a border is off by 2^-13 or more, and x r is within 2^-20
-// of the quotient (at most 7 of interest), so rounding x r to multiples of 2^-13,
+// 16-bit x: a quotient off a border is off by 2^-13 or more, and x r is within 2^-19
+// of the quotient (at most 7 of interest; r may be 2 units off), so rounding x r to multiples of 2^-13,
 // by adding and subtracting 1.5 * 2^10, leaves it on its side and borders exact.
 __host__ __device__ inline float ratio16(float x, float r) { return fmaf(x, r, 1536.f) - 1536.f; }
 // fp32 x: the correctly rounded quotient (the last step of P. Markstein, "Computation

@@ -20,13 +20,14 @@ void kv4_place(int raw, int cap, int count, int j, int *out) {
     for (int i = 0; i < 16; ++i) out[3 + i] = p.present(p.t0 + i);
 }
 
-void kv4_scale_bytes(const float *a, int n, int *out) {
-    for (int i = 0; i < n; ++i) out[i] = gdn::kv4::scale_byte(a[i]);
+void kv4_scale_bytes(const float *a, int n, int wide, int *out) {
+    for (int i = 0; i < n; ++i) out[i] = wide ? gdn::kv4::scale_byte(a[i]) : gdn::kv4::scale_byte16(a[i]);
 }
 
 // quotients by scale `byte` as the conversion to 4 bits takes them
 void kv4_ratios(const float *x, int n, int byte, int wide, float *out) {
-    const float s = gdn::kv4::scale_value(byte), r = 1.f / s;
+    // 16-bit elements: an approximate reciprocal will do, here one that is 2 units off
+    const float s = gdn::kv4::scale_value(byte), r = wide ? 1.f / s : 1.f / s * (1.f + 3e-7f);
     for (int i = 0; i < n; ++i) out[i] = wide ? gdn::kv4::ratio32(x[i], r, s) : gdn::kv4::ratio16(x[i], r);
 }
 int kv4_run_begin(int T, int W, int w) { return gdn::kv4::run_begin(T, W, w); }

@@ -75,14 +75,14 @@ def test_scale_bytes_round_as_the_oracle(H):
     rng = np.random.default_rng(2)
     border = (6 * (kv4.SCALES[1:] + kv4.SCALES[:-1]) / 2).astype(np.float32)
     near = (border.view(np.int32)[:, None] + np.arange(-30, 31)).astype(np.int32).view(np.float32).ravel()
-    a = np.concatenate([near[near >= 0], np.arange(0x7c01, dtype=np.uint16).view(np.float16).astype(np.float32),
-                        (np.arange(0x7f81, dtype=np.uint32) << 16).view(np.float32),
-                        np.exp(rng.uniform(-14, 12, 100000)).astype(np.float32)])
-    a = np.ascontiguousarray(a)
-    out = np.zeros(a.size, dtype=np.int32)
-    H.kv4_scale_bytes(ctypes.c_void_p(a.ctypes.data), a.size, ctypes.c_void_p(out.ctypes.data))
-    want = kv4.nearest(np.minimum(a.astype(np.float64), 61440) / 6, kv4.SCALES)
-    assert np.array_equal(out, want)
+    x16 = np.concatenate([np.arange(0x7c01, dtype=np.uint16).view(np.float16).astype(np.float32),
+                          (np.arange(0x7f81, dtype=np.uint32) << 16).view(np.float32)])
+    x32 = np.concatenate([near[near >= 0], x16, np.exp(rng.uniform(-14, 12, 100000)).astype(np.float32)])
+    for wide, a in ((0, x16), (1, x32)):
+        out = np.zeros(a.size, dtype=np.int32)
+        H.kv4_scale_bytes(ctypes.c_void_p(a.ctypes.data), a.size, wide, ctypes.c_void_p(out.ctypes.data))
+        want = kv4.nearest(np.minimum(a.astype(np.float64), 61440) / 6, kv4.SCALES)
+        assert np.array_equal(out, want)
 
 
 def fall(y, m, s):
