@@ -367,8 +367,8 @@ int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, 
  * bits), the softmax weights with 22 bits.  Results do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), the cache's widths and page
  * sizes, n_heads_kv dividing n_heads, page tables with room for fewer than 2^31
- * tiles of 16 tokens over all kv heads (and blocks of 8 or 16 of a kv head's
- * (n_heads / n_heads_kv) * n_q rows).  q and out 16-byte aligned; out must not
+ * tiles of 16 tokens over all kv heads (and blocks of 8 of a kv head's (n_heads /
+ * n_heads_kv) * n_q rows).  q and out 16-byte aligned; out must not
  * overlap an input.
  * workspace: caller's device buffer of gdn_flash_attn_kv4_workspace_bytes (0 where
  *   the call needs none, and for sizes that are not supported), 256-byte aligned, its contents ignored on entry and garbage on return, for one

@@ -51,18 +51,21 @@ constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is wr
 constexpr int kAloneTiles = 4;         // up to so many tiles a warp, and so many units, a unit has
 constexpr int kAloneUnits = 2 * kGrid; // a CTA to itself
 
-// Rows of a unit's block: 8 per MMA column tile.
-constexpr int rows_of(long long R) { return R > 8 ? 16 : 8; }
+// Rows of a unit: one MMA column tile.  More rows of a kv head are more units, which
+// decode the tiles again (from L2): blocks of 16 rows decode half as often, but took
+// twice the registers and so half the warps, and 16 x 5 queries x 32/8 x 5001 x 128 took
+// 57 us so and 49 us with blocks of 8.
+constexpr int kRows = 8;
 
-// Shape of the kernel for widths DK, DV and NT column tiles of rows.  Each warp
-// streams its run through a ring of its own in shared memory: stages of U tiles,
-// each tile one bulk copy.  12 warps and steps of 4 tiles where 168 registers a
-// thread hold the output tile and two steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x
-// 128: 68 us; 16 warps with steps of 2 tiles 72, 8 warps with steps of 4 82.)
-constexpr int warps_of(int dk, int dv, int rows) { return rows == 8 && dk <= 128 && dv <= 128 ? 12 : 8; }
-template <int DK, int DV, int NT>
+// Shape of the kernel for widths DK and DV.  Each warp streams its run through a ring
+// of its own in shared memory: stages of U tiles, each tile one bulk copy.  12 warps
+// and steps of 4 tiles where 168 registers a thread hold the output tile and two
+// steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x 128: 68 us; 16 warps with steps of 2
+// tiles 72, 8 warps with steps of 4 82.)
+constexpr int warps_of(int dk, int dv) { return dk <= 128 && dv <= 128 ? 12 : 8; }
+template <int DK, int DV>
 struct Geo {
-    static constexpr int WARPS = warps_of(DK, DV, 8 * NT);
+    static constexpr int WARPS = warps_of(DK, DV);
     static constexpr int U = WARPS == 12 ? 4 : 2;
     static constexpr int TB = tile_bytes(DK, DV);
     static constexpr int BUDGET = 216 * 1024;
@@ -166,14 +169,6 @@ __device__ __forceinline__ void store2(void *out, int type, size_t i, float x, f
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-__device__ __forceinline__ long long warp_scan(long long n, int lane) {
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, n, off);
-        if (lane >= off) n += o;
-    }
-    return n;
-}
 // Tiles of all units of sequence b.  Whole-warp: their total over the sequences
 // before `end`, and the sequence that tile x lies in with the tiles before it.
 __device__ __forceinline__ int tiles_at(const Attn &a, int b, int units) {
@@ -206,21 +201,21 @@ __device__ __forceinline__ int find_tile(const Attn &a, int units, int x, int la
 }
 
 // A partial result: [rows][DV] outputs, [rows] maxima, [rows] sums.
-template <int DV, int ROWS> constexpr size_t kPartial = (size_t)ROWS * (DV + 2);
+template <int DV> constexpr size_t kPartial = (size_t)kRows * (DV + 2);
 
 // One warp's share of one unit: an online softmax over tiles.
-template <int DK, int DV, int NT, bool QLO, int PM>
+template <int DK, int DV, bool QLO, int PM>
 struct Unit {
-    static constexpr int U = Geo<DK, DV, NT>::U, TB = tile_bytes(DK, DV);
+    static constexpr int U = Geo<DK, DV>::U, TB = tile_bytes(DK, DV);
     static constexpr int CK = DK > 128 ? 2 : 1;        // key parts
     static constexpr int ST = DK >= 128 ? 8 : 4;       // MMA steps of a part
     static constexpr int VB = DV / 64;                 // value blocks, four M tiles each
-    uint32_t qh[NT][CK * ST][2], ql[QLO ? NT : 1][CK * ST][2];
-    float f[NT][2];                                    // row factors of the scores (not negative)
-    int qi[NT][2];                                     // the row's query; -1: no such row
+    uint32_t qh[CK * ST][2], ql[QLO ? CK * ST : 1][2];
+    float f[2];                                    // row factors of the scores (not negative)
+    int qi[2];                                     // the row's query; -1: no such row
     int all;                                           // tokens that every row sees and no mask changes
-    float m[NT][2], l[NT][2];                          // running maximum, sum of the weights
-    float o[NT][VB * 4][4];
+    float m[2], l[2];                          // running maximum, sum of the weights
+    float o[VB * 4][4];
 
     __device__ __forceinline__ void begin(const Attn &a, int b, int hk, int rb, int lane) {
         const int g = lane >> 2, t = lane & 3;
@@ -229,74 +224,68 @@ struct Unit {
         all = a.mask ? 0 : (a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len);
         // all loads first: a lane's elements are whole 16-byte words
         constexpr int QE = QLO ? 4 : 8, QW = ST * 4 / QE;   // elements a word, words a part
-        uint4 raw_q[NT][CK][QW];
+        uint4 raw_q[CK][QW];
+        const int row = PM == kColumns ? g & 3 : rb * kRows + g;
+        const size_t q0 = ((size_t)(b * (size_t)a.H + hk * rep) * a.n_q + row) * DK;
+        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
+                                                          (q0 + t * ST * 4) * (16 / QE));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = PM == kColumns ? g & 3 : rb * 8 * NT + nt * 8 + g;
-            const size_t q0 = ((size_t)(b * (size_t)a.H + hk * rep) * a.n_q + row) * DK;
-            const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
-                                                              (q0 + t * ST * 4) * (16 / QE));
+        for (int c = 0; c < CK; ++c)
 #pragma unroll
-            for (int c = 0; c < CK; ++c)
+            for (int i = 0; i < QW; ++i)
+                raw_q[c][i] = row < a.R ? __ldg(at + c * (128 / QE) + i) : make_uint4(0, 0, 0, 0);
+        float x[CK * ST * 4];
+        float big = 0.f;
 #pragma unroll
-                for (int i = 0; i < QW; ++i)
-                    raw_q[nt][c][i] = row < a.R ? __ldg(at + c * (128 / QE) + i) : make_uint4(0, 0, 0, 0);
-        }
+        for (int c = 0; c < CK; ++c)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[CK * ST * 4];
-            float big = 0.f;
+            for (int i = 0; i < QW; ++i) {
+                const uint32_t w[4] = {raw_q[c][i].x, raw_q[c][i].y, raw_q[c][i].z,
+                                       raw_q[c][i].w};
+                float *y = x + (c * QW + i) * QE;
 #pragma unroll
-            for (int c = 0; c < CK; ++c)
-#pragma unroll
-                for (int i = 0; i < QW; ++i) {
-                    const uint32_t w[4] = {raw_q[nt][c][i].x, raw_q[nt][c][i].y, raw_q[nt][c][i].z,
-                                           raw_q[nt][c][i].w};
-                    float *y = x + (c * QW + i) * QE;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (QLO) {
-                            y[e] = __uint_as_float(w[e]);
-                        } else if (a.q_type == GDN_DTYPE_BF16) {
-                            y[2 * e] = __uint_as_float(w[e] << 16);
-                            y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                        } else {
-                            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-                            y[2 * e] = h.x;
-                            y[2 * e + 1] = h.y;
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (QLO) {
+                        y[e] = __uint_as_float(w[e]);
+                    } else if (a.q_type == GDN_DTYPE_BF16) {
+                        y[2 * e] = __uint_as_float(w[e] << 16);
+                        y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                    } else {
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                        y[2 * e] = h.x;
+                        y[2 * e + 1] = h.y;
                     }
                 }
-#pragma unroll
-            for (int e = 0; e < CK * ST * 4; ++e) big = fmaxf(big, fabsf(x[e]));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^14 / (the power of two at or below the row's largest element)
-            const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 126);
-            const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-            const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(a.scale);
-            const float sup = a.scale < 0.f ? -up : up;   // q takes the scale's sign
-#pragma unroll
-            for (int s = 0; s < CK * ST; ++s)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float x0 = x[s * 4 + 2 * p] * sup, x1 = x[s * 4 + 2 * p + 1] * sup;
-                    if constexpr (QLO) split2(x0, x1, qh[nt][s][p], ql[nt][s][p]);
-                    else qh[nt][s][p] = half2_bits(__floats2half2_rn(x0, x1));
-                }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                f[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
-                const int mine = PM == kColumns ? (2 * t + r) & 3 : rb * 8 * NT + nt * 8 + 2 * t + r;
-                qi[nt][r] = mine < a.R ? mine % a.n_q : -1;
-                m[nt][r] = -INFINITY;
-                l[nt][r] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < VB * 4; ++i)
+        for (int e = 0; e < CK * ST * 4; ++e) big = fmaxf(big, fabsf(x[e]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^14 / (the power of two at or below the row's largest element)
+        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 126);
+        const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+        const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(a.scale);
+        const float sup = a.scale < 0.f ? -up : up;   // q takes the scale's sign
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+        for (int s = 0; s < CK * ST; ++s)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float x0 = x[s * 4 + 2 * p] * sup, x1 = x[s * 4 + 2 * p + 1] * sup;
+                if constexpr (QLO) split2(x0, x1, qh[s][p], ql[s][p]);
+                else qh[s][p] = half2_bits(__floats2half2_rn(x0, x1));
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            f[r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
+            const int mine = PM == kColumns ? (2 * t + r) & 3 : rb * kRows + 2 * t + r;
+            qi[r] = mine < a.R ? mine % a.n_q : -1;
+            m[r] = -INFINITY;
+            l[r] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < VB * 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     }
 
     // U tiles at `p`, tokens pos .. of a sequence; from `stop` on they are not this
@@ -305,7 +294,7 @@ struct Unit {
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int ka = 4 * (g >> 1) + (g & 1), kb = ka + 2;   // tokens of C rows g, g + 8
-        float s[U][NT][4];
+        float s[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint8_t *k = p + u * TB;
@@ -342,96 +331,88 @@ struct Unit {
                         const uint32_t A[4] = {mul2(x[2 * i], da), mul2(y[2 * i], db), mul2(x[2 * i + 1], da),
                                                mul2(y[2 * i + 1], db)};
                         const int st = c * ST + 2 * h + i;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (st == 0) mma0(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
-                            else mma(s[u][nt], A, qh[nt][st][0], qh[nt][st][1]);
-                            if constexpr (QLO) mma(s[u][nt], A, ql[nt][st][0], ql[nt][st][1]);
-                        }
+                        if (st == 0) mma0(s[u], A, qh[st][0], qh[st][1]);
+                        else mma(s[u], A, qh[st][0], qh[st][1]);
+                        if constexpr (QLO) mma(s[u], A, ql[st][0], ql[st][1]);
                     }
                 }
             }
         }
         const bool plain = pos + U * kTile <= min(all, stop) && good == (1u << U) - 1u;
-        uint32_t ph[U][NT][2], pl[PM == kHiLo ? U : 1][NT][2];
-        float cf[NT][2];
+        uint32_t ph[U][2], pl[PM == kHiLo ? U : 1][2];
+        float cf[2];
         if (!plain) {
             const int raw = max(__ldg(a.c.lens + b), 0);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int r = 0; r < 2; ++r) {
+                // (a length past the table counts in full for the causal limit)
+                const int i = qi[r];
+                const int lim = a.causal ? (int)min((long long)stop, (long long)raw - a.n_q + 1 + i) : stop;
+                const size_t row = ((size_t)b * a.n_q + i) * (size_t)capacity(a.c);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    // (a length past the table counts in full for the causal limit)
-                    const int i = qi[nt][r];
-                    const int lim = a.causal ? (int)min((long long)stop, (long long)raw - a.n_q + 1 + i) : stop;
-                    const size_t row = ((size_t)b * a.n_q + i) * (size_t)capacity(a.c);
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-#pragma unroll
-                        for (int e = r; e < 4; e += 2) {
-                            const int key = pos + u * kTile + (e < 2 ? ka : kb);
-                            float x = s[u][nt][e] * f[nt][r];
-                            if (i < 0 || key >= lim || !(good >> u & 1)) x = -INFINITY;
-                            else if (a.mask) x += element(a.mask, a.q_type, row + key);
-                            s[u][nt][e] = x;
-                        }
-                }
+                    for (int e = r; e < 4; e += 2) {
+                        const int key = pos + u * kTile + (e < 2 ? ka : kb);
+                        float x = s[u][e] * f[r];
+                        if (i < 0 || key >= lim || !(good >> u & 1)) x = -INFINITY;
+                        else if (a.mask) x += element(a.mask, a.q_type, row + key);
+                        s[u][e] = x;
+                    }
+            }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int r = 0; r < 2; ++r) {
+            float mx = fmaxf(s[0][r], s[0][r + 2]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float mx = fmaxf(s[0][nt][r], s[0][nt][r + 2]);
+            for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(s[u][r], s[u][r + 2]));
 #pragma unroll
-                for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][r], s[u][nt][r + 2]));
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            // The weight of a score x is 2^((x - maximum) log2 e + 12).  Without a
+            // mask that is one FMA on the MMAs' result, with the maximum's product
+            // rounded the same way wherever it is used.  Scores that took a mask
+            // are differences in natural units first: masks of the type's lowest
+            // value would overflow.
+            const float old = m[r], mn = fmaxf(old, plain ? mx * f[r] : mx);
+            m[r] = mn;
+            const float base = mn == -INFINITY ? 0.f : mn;
+            cf[r] = exp2_approx(a.mask ? (old - base) * kLog2e : old * kLog2e - __fmul_rn(base, kLog2e));
+            float sum = 0.f;
+            if (plain) {
+                const float k = f[r] * kLog2e, z = kPBits - __fmul_rn(base, kLog2e);
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                // The weight of a score x is 2^((x - maximum) log2 e + 12).  Without a
-                // mask that is one FMA on the MMAs' result, with the maximum's product
-                // rounded the same way wherever it is used.  Scores that took a mask
-                // are differences in natural units first: masks of the type's lowest
-                // value would overflow.
-                const float old = m[nt][r], mn = fmaxf(old, plain ? mx * f[nt][r] : mx);
-                m[nt][r] = mn;
-                const float base = mn == -INFINITY ? 0.f : mn;
-                cf[nt][r] = exp2_approx(a.mask ? (old - base) * kLog2e : old * kLog2e - __fmul_rn(base, kLog2e));
-                float sum = 0.f;
-                if (plain) {
-                    const float k = f[nt][r] * kLog2e, z = kPBits - __fmul_rn(base, kLog2e);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r], k, z));
-                        s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2], k, z));
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        s[u][nt][r] = exp2_approx(fmaf(s[u][nt][r] - base, kLog2e, kPBits));
-                        s[u][nt][r + 2] = exp2_approx(fmaf(s[u][nt][r + 2] - base, kLog2e, kPBits));
-                    }
+                for (int u = 0; u < U; ++u) {
+                    s[u][r] = exp2_approx(fmaf(s[u][r], k, z));
+                    s[u][r + 2] = exp2_approx(fmaf(s[u][r + 2], k, z));
                 }
+            } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u) sum += s[u][nt][r] + s[u][nt][r + 2];
-                l[nt][r] = fmaf(l[nt][r], cf[nt][r], sum);
+                for (int u = 0; u < U; ++u) {
+                    s[u][r] = exp2_approx(fmaf(s[u][r] - base, kLog2e, kPBits));
+                    s[u][r + 2] = exp2_approx(fmaf(s[u][r + 2] - base, kLog2e, kPBits));
+                }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x = s[u][nt][2 * k], y = s[u][nt][2 * k + 1];
-                    if constexpr (PM == kHi) {
-                        ph[u][nt][k] = half2_bits(__floats2half2_rn(x, y));
-                    } else if constexpr (PM == kHiLo) {
-                        split2(x, y, ph[u][nt][k], pl[u][nt][k]);
-                        pl[u][nt][k] = transpose8(pl[u][nt][k]);
-                    } else {
-                        uint32_t lo;
-                        split2(x, y, ph[u][nt][k], lo);
-                        if (t >= 2) ph[u][nt][k] = lo;
-                    }
-                    ph[u][nt][k] = transpose8(ph[u][nt][k]);
-                }
+            for (int u = 0; u < U; ++u) sum += s[u][r] + s[u][r + 2];
+            l[r] = fmaf(l[r], cf[r], sum);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float x = s[u][2 * k], y = s[u][2 * k + 1];
+                if constexpr (PM == kHi) {
+                    ph[u][k] = half2_bits(__floats2half2_rn(x, y));
+                } else if constexpr (PM == kHiLo) {
+                    split2(x, y, ph[u][k], pl[u][k]);
+                    pl[u][k] = transpose8(pl[u][k]);
+                } else {
+                    uint32_t lo;
+                    split2(x, y, ph[u][k], lo);
+                    if (t >= 2) ph[u][k] = lo;
+                }
+                ph[u][k] = transpose8(ph[u][k]);
+            }
         // The products of U tiles add up in the MMAs, small terms first, and reach
         // the output by one fp32 FMA that also rescales it: the MMAs' accumulation
         // truncates, and over thousands of tokens that would show.
@@ -464,23 +445,20 @@ struct Unit {
                     A[u][0] = mul2(x[0], s01[u]); A[u][1] = mul2(x[1], s01[u]);
                     A[u][2] = mul2(x[2], s23[u]); A[u][3] = mul2(x[3], s23[u]);
                 }
+                float d[4];
+                if constexpr (PM == kHiLo) {
+                    mma0(d, A[0], pl[0][0], pl[0][1]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float d[4];
-                    if constexpr (PM == kHiLo) {
-                        mma0(d, A[0], pl[0][nt][0], pl[0][nt][1]);
-#pragma unroll
-                        for (int u = 1; u < U; ++u) mma(d, A[u], pl[u][nt][0], pl[u][nt][1]);
-                        mma(d, A[0], ph[0][nt][0], ph[0][nt][1]);
-                    } else {
-                        mma0(d, A[0], ph[0][nt][0], ph[0][nt][1]);
-                    }
-#pragma unroll
-                    for (int u = 1; u < U; ++u) mma(d, A[u], ph[u][nt][0], ph[u][nt][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[nt][r * 4 + i][e] = fmaf(o[nt][r * 4 + i][e], cf[nt][e & 1], d[e]);
+                    for (int u = 1; u < U; ++u) mma(d, A[u], pl[u][0], pl[u][1]);
+                    mma(d, A[0], ph[0][0], ph[0][1]);
+                } else {
+                    mma0(d, A[0], ph[0][0], ph[0][1]);
                 }
+#pragma unroll
+                for (int u = 1; u < U; ++u) mma(d, A[u], ph[u][0], ph[u][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[r * 4 + i][e] = fmaf(o[r * 4 + i][e], cf[e & 1], d[e]);
             }
         }
     }
@@ -489,37 +467,35 @@ struct Unit {
     __device__ __forceinline__ void end(const Attn &a, int b, int hk, int rb, bool whole, float *part, int lane) {
         const int g = lane >> 2, t = lane & 3, rep = a.H / a.c.Hkv;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float sum = l[nt][r];
+            for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const int local = 2 * t + r, row = rb * kRows + local;
+            if constexpr (PM == kColumns) {
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                const int local = nt * 8 + 2 * t + r, row = rb * 8 * NT + local;
-                if constexpr (PM == kColumns) {
-#pragma unroll
-                    for (int i = 0; i < VB * 4; ++i) {
-                        o[nt][i][r] += __shfl_xor_sync(0xffffffffu, o[nt][i][r], 2);
-                        o[nt][i][r + 2] += __shfl_xor_sync(0xffffffffu, o[nt][i][r + 2], 2);
-                    }
-                }
-                if (row >= a.R) continue;
-                const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * rep + row / a.n_q) * DV;
-#pragma unroll
-                for (int blk = 0; blk < VB; ++blk) {
-                    const int el = 128 * (blk >> 1) + (DV == 64 ? 8 : 16) * g + 8 * (blk & 1);
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = o[nt][blk * 4 + e / 2][2 * (e & 1) + r] * inv;
-                    if (whole) store8(a.out, a.out_type, at + el, x);
-                    else store8(part, GDN_DTYPE_F32, (size_t)local * DV + el, x);
-                }
-                if (!whole && g == 0) {
-                    part[8 * NT * DV + local] = m[nt][r];
-                    part[8 * NT * (DV + 1) + local] = sum;
+                for (int i = 0; i < VB * 4; ++i) {
+                    o[i][r] += __shfl_xor_sync(0xffffffffu, o[i][r], 2);
+                    o[i][r + 2] += __shfl_xor_sync(0xffffffffu, o[i][r + 2], 2);
                 }
             }
+            if (row >= a.R) continue;
+            const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * rep + row / a.n_q) * DV;
+#pragma unroll
+            for (int blk = 0; blk < VB; ++blk) {
+                const int el = 128 * (blk >> 1) + (DV == 64 ? 8 : 16) * g + 8 * (blk & 1);
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = o[blk * 4 + e / 2][2 * (e & 1) + r] * inv;
+                if (whole) store8(a.out, a.out_type, at + el, x);
+                else store8(part, GDN_DTYPE_F32, (size_t)local * DV + el, x);
+            }
+            if (!whole && g == 0) {
+                part[kRows * DV + local] = m[r];
+                part[kRows * (DV + 1) + local] = sum;
+            }
+        }
     }
 };
 
@@ -545,9 +521,9 @@ struct Cursor {
     }
 };
 
-template <int DK, int DV, int NT, bool QLO, int PM>
-__global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(const Attn a) {
-    using G = Geo<DK, DV, NT>;
+template <int DK, int DV, bool QLO, int PM>
+__global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const Attn a) {
+    using G = Geo<DK, DV>;
     constexpr int U = G::U, ST = G::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[G::WARPS][ST];
@@ -616,7 +592,7 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) copy();
 
-    Unit<DK, DV, NT, QLO, PM> unit;
+    Unit<DK, DV, QLO, PM> unit;
     int get = 0;                                       // stage to read, and its barrier's phase
     uint32_t phase = 0;
     while (c.left > 0) {
@@ -645,7 +621,7 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
         }
         if (a.alone) break;
         const bool whole = j0 == 0 && j1 == c.n;
-        unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * kPartial<DV, 8 * NT>, lane);
+        unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * kPartial<DV>, lane);
         c.step(a, units, j1 - j0);
     }
     if (!a.alone) return;
@@ -654,21 +630,21 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
     __syncthreads();
     const int b = blockIdx.x / units, u = blockIdx.x - b * units, hk = u / a.n_rb, rb = u - hk * a.n_rb;
     float *part = reinterpret_cast<float *>(smem);
-    if (warp < parts) unit.end(a, b, hk, rb, parts == 1, part + warp * kPartial<DV, 8 * NT>, lane);
+    if (warp < parts) unit.end(a, b, hk, rb, parts == 1, part + warp * kPartial<DV>, lane);
     if (parts == 1) return;
     __syncthreads();
-    const int n_rows = min(8 * NT, a.R - rb * 8 * NT);
+    const int n_rows = min(kRows, a.R - rb * kRows);
     for (int i = threadIdx.x; i < n_rows * (DV / 4); i += G::WARPS * 32) {
-        const int local = i / (DV / 4), x = i - local * (DV / 4), row = rb * 8 * NT + local;
-        const float *m = part + 8 * NT * DV + local, *l = m + 8 * NT;
+        const int local = i / (DV / 4), x = i - local * (DV / 4), row = rb * kRows + local;
+        const float *m = part + kRows * DV + local, *l = m + kRows;
         float top = -INFINITY, sum = 0.f;
-        for (int k = 0; k < parts; ++k) top = fmaxf(top, m[k * kPartial<DV, 8 * NT>]);
+        for (int k = 0; k < parts; ++k) top = fmaxf(top, m[k * kPartial<DV>]);
         const float base = top == -INFINITY ? 0.f : top;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < parts; ++k) {
-            const float wt = exp2_approx((m[k * kPartial<DV, 8 * NT>] - base) * kLog2e);
-            const float4 v = reinterpret_cast<const float4 *>(part + k * kPartial<DV, 8 * NT> + local * DV)[x];
-            sum = fmaf(l[k * kPartial<DV, 8 * NT>], wt, sum);
+            const float wt = exp2_approx((m[k * kPartial<DV>] - base) * kLog2e);
+            const float4 v = reinterpret_cast<const float4 *>(part + k * kPartial<DV> + local * DV)[x];
+            sum = fmaf(l[k * kPartial<DV>], wt, sum);
             y = make_float4(fmaf(v.x, wt, y.x), fmaf(v.y, wt, y.y), fmaf(v.z, wt, y.z), fmaf(v.w, wt, y.w));
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -683,7 +659,7 @@ __global__ void __launch_bounds__(Geo<DK, DV, NT>::WARPS * 32, 1) attn_kernel(co
 // once, so their weights are known before the outputs are read, and those loads
 // do not wait for one another.  A row of more parts is left to the whole block.
 constexpr int kJoinWarps = 8;
-template <int DV, int ROWS>
+template <int DV>
 struct Join {
     static constexpr int V = DV == 64 ? 2 : 4, C = DV == 256 ? 2 : 1;   // columns of a lane: C times V
     float x[C * V];
@@ -696,11 +672,11 @@ struct Join {
         for (int e = 0; e < C * V; ++e) x[e] = 0.f;
         for (int p0 = first; p0 < n; p0 += 32 * step) {
             const int mine = p0 + lane * step, cnt = min(32, (n - p0 + step - 1) / step);
-            const float *at = ws + (size_t)partial_slot(w0 + mine, mine == 0) * kPartial<DV, ROWS>;
+            const float *at = ws + (size_t)partial_slot(w0 + mine, mine == 0) * kPartial<DV>;
             float m = -INFINITY, l = 0.f;
             if (mine < n) {
-                m = __ldcg(at + ROWS * DV + local);
-                l = __ldcg(at + ROWS * (DV + 1) + local);
+                m = __ldcg(at + kRows * DV + local);
+                l = __ldcg(at + kRows * (DV + 1) + local);
             }
             float top = m;
 #pragma unroll
@@ -721,7 +697,7 @@ struct Join {
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
                     const int p = p0 + min(i0 + i, cnt - 1) * step;
-                    const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV, ROWS> + local * DV;
+                    const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV> + local * DV;
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         if constexpr (V == 2) {
@@ -755,7 +731,7 @@ struct Join {
     }
 };
 
-template <int DV, int ROWS>
+template <int DV>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, int n_rows) {
     __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
@@ -764,7 +740,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
     auto place = [&](int r, int &local) {              // where a row's output goes
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
-        local = row % ROWS;
+        local = row % kRows;
         return (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV;
     };
     const int r0 = blockIdx.x * rpb, r = r0 + warp;
@@ -774,7 +750,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
         const int tiles = tiles_of(length(a.c, b));
         n = 0;
         if (tiles > 0) {
-            const int first = tiles_before(a, units, b, lane) + (hk * a.n_rb + row / ROWS) * tiles;
+            const int first = tiles_before(a, units, b, lane) + (hk * a.n_rb + row / kRows) * tiles;
             w0 = run_of(T, W, first);
             n = run_of(T, W, first + tiles - 1) - w0 + 1;
         }
@@ -786,7 +762,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     // the attention kernel's results; every block waits, so that this grid never
     // ends before that one
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Join<DV, ROWS> join;
+    Join<DV> join;
     int local;
     if (n >= 0 && n != 1 && n <= 32) {                 // (one run had it all: written; none: zeros)
         const size_t at = place(r, local);
@@ -833,17 +809,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
 
 // ------------------------------------------------------------------ host
 
-template <int DK, int DV, int NT, bool QLO, int PM>
+template <int DK, int DV, bool QLO, int PM>
 cudaError_t launch(const Attn &a, cudaStream_t stream) {
-    using G = Geo<DK, DV, NT>;
+    using G = Geo<DK, DV>;
     static PerDeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(attn_kernel<DK, DV, NT, QLO, PM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_kernel<DK, DV, QLO, PM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
     const int grid = a.alone ? a.n_seqs * a.c.Hkv * a.n_rb : kGrid;
-    attn_kernel<DK, DV, NT, QLO, PM><<<grid, G::WARPS * 32, G::SMEM, stream>>>(a);
+    attn_kernel<DK, DV, QLO, PM><<<grid, G::WARPS * 32, G::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.alone) return e;
     // few rows: a block each, so that long rows are shared out; many: a warp each
@@ -862,20 +838,16 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<DV, 8 * NT>, a, rpb, n_rows);
+    return cudaLaunchKernelEx(&cfg, join_kernel<DV>, a, rpb, n_rows);
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
 // queries are exact in one f16, and 16-bit outputs need 11 bits of the weights.
 template <int DK, int DV>
 cudaError_t launch_d(const Attn &a, cudaStream_t stream) {
-    const bool two = rows_of(a.R) > 8;
-    if (a.q_type == GDN_DTYPE_F32)
-        return two ? launch<DK, DV, 2, true, kHiLo>(a, stream) : launch<DK, DV, 1, true, kHiLo>(a, stream);
-    if (a.out_type != GDN_DTYPE_F32)
-        return two ? launch<DK, DV, 2, false, kHi>(a, stream) : launch<DK, DV, 1, false, kHi>(a, stream);
-    if (a.R <= 4) return launch<DK, DV, 1, false, kColumns>(a, stream);
-    return two ? launch<DK, DV, 2, false, kHiLo>(a, stream) : launch<DK, DV, 1, false, kHiLo>(a, stream);
+    if (a.q_type == GDN_DTYPE_F32) return launch<DK, DV, true, kHiLo>(a, stream);
+    if (a.out_type != GDN_DTYPE_F32) return launch<DK, DV, false, kHi>(a, stream);
+    return a.R <= 4 ? launch<DK, DV, false, kColumns>(a, stream) : launch<DK, DV, false, kHiLo>(a, stream);
 }
 
 template <int DK>
@@ -896,8 +868,8 @@ struct Plan {
 };
 bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, Plan *p) {
     const long long R = (long long)(H / Hkv) * n_q;
-    const int rows = rows_of(R), warps = warps_of(dk, dv, rows);
-    const long long n_rb = (R + rows - 1) / rows;
+    const int warps = warps_of(dk, dv);
+    const long long n_rb = (R + kRows - 1) / kRows;
     unsigned long long units, all;
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
         !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
@@ -905,7 +877,7 @@ bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, 
     // few units of few tiles: a block each, whose warps meet in shared memory
     p->alone = tiles <= kAloneTiles * warps && units <= kAloneUnits;
     p->W = (int)(all < (unsigned long long)(kGrid * warps) ? all : (unsigned long long)(kGrid * warps));
-    p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)rows * (dv + 2) * sizeof(float);
+    p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)kRows * (dv + 2) * sizeof(float);
     return true;
 }
 
@@ -994,7 +966,7 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
     const Attn a{{static_cast<uint8_t *>(const_cast<void *>(cache)), page_table, seq_lens, status, n_pages,
                   n_heads_kv, page_size / kTile, max_pages, head_dim_k, head_dim_v},
                  q, mask, out, static_cast<float *>(ws), n_seqs, n_heads, n_q, R,
-                 (R + rows_of(R) - 1) / rows_of(R), p.W, scale, dtype, out_dtype, causal != 0, p.alone};
+                 (R + kRows - 1) / kRows, p.W, scale, dtype, out_dtype, causal != 0, p.alone};
     cudaError_t e;
     switch (head_dim_k) {
         case 64: e = launch_k<64>(a, st); break;
