@@ -15,10 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_recurrent.cu", "gdn_chunked.cu", "gdn_attn.cu",
-           "gdn_kv4.cu", "gdn_kv4_attn.cu", "gdn_kv4_rows.cu"]
+           "gdn_kv4.cu", "gdn_kv4_attn.cu"]
 HEADERS = [os.path.join(CSRC, "gdn_internal.h"), os.path.join(CSRC, "gdn_ptx.cuh"),
            os.path.join(CSRC, "gdn_kv4.cuh"),
-           os.path.join(CSRC, "gdn_kv4_attn.cuh"),
            os.path.join(os.path.dirname(PKG), "include", "gdn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -40,13 +40,14 @@
 
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
-#include "gdn_kv4_attn.cuh"
+#include "gdn_kv4.cuh"
 #include "gdn_ptx.cuh"
 
 namespace gdn {
 namespace kv4 {
 namespace {
 
+constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for
 constexpr int kAloneTiles = 4;         // up to so many tiles a warp, and so many units, a unit has
 constexpr int kAloneUnits = 2 * kGrid; // a CTA to itself
 
@@ -75,7 +76,17 @@ struct Geo {
     static_assert(STAGES >= 2 && TB % 16 == 0, "ring");
 };
 
-constexpr float kPBits = 12.f;         // probabilities are scaled by 2^12
+struct Attn {
+    View c;
+    const void *q, *mask;
+    void *out;
+    float *ws;
+    int n_seqs, H, n_q, R, n_rb, W;    // R rows a kv head in n_rb blocks; W runs at most
+    float scale;
+    int q_type, out_type;
+    bool causal;
+    bool alone;                        // a block a unit, and no partial results
+};
 
 // How the weights enter the MMAs.  kHi: 11 bits, for 16-bit outputs.  kHiLo: the
 // remainder's 11 bits in a second MMA.  kColumns: of at most 4 rows, the remainder
@@ -83,6 +94,13 @@ constexpr float kPBits = 12.f;         // probabilities are scaled by 2^12
 // column r + 4; the two columns' outputs are added at the end.
 enum Weights { kHi = 0, kHiLo = 1, kColumns = 2 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPBits = 12.f;         // probabilities are scaled by 2^12
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -103,6 +121,88 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// (x, y) as f16 pairs hi + lo
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = half2_bits(h);
+    lo = half2_bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+__device__ __forceinline__ float element(const void *p, int type, size_t i) {
+    if (type == GDN_DTYPE_F32) return __ldg(static_cast<const float *>(p) + i);
+    const unsigned short u = __ldg(static_cast<const unsigned short *>(p) + i);
+    return type == GDN_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+// 8 consecutive outputs
+__device__ __forceinline__ void store8(void *out, int type, size_t i, const float (&x)[8]) {
+    if (type == GDN_DTYPE_F32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(out) + i);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (type == GDN_DTYPE_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            w[e] = half2_bits(__floats2half2_rn(x[2 * e], x[2 * e + 1]));
+        }
+    }
+    *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 2 consecutive outputs
+__device__ __forceinline__ void store2(void *out, int type, size_t i, float x, float y) {
+    if (type == GDN_DTYPE_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(out) + i) = make_float2(x, y);
+    else if (type == GDN_DTYPE_BF16)
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(out) + i) = __floats2bfloat162_rn(x, y);
+    else
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(out) + i) = __floats2half2_rn(x, y);
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Tiles of all units of sequence b.  Whole-warp: their total over the sequences
+// before `end`, and the sequence that tile x lies in with the tiles before it.
+__device__ __forceinline__ int tiles_at(const Attn &a, int b, int units) {
+    return b < a.n_seqs ? tiles_of(length(a.c, b)) * units : 0;
+}
+__device__ __forceinline__ int tiles_before(const Attn &a, int units, int end, int lane) {
+    int n = 0;
+    for (int b = lane; b < end; b += 32) n += tiles_at(a, b, units);
+    return __reduce_add_sync(0xffffffffu, n);
+}
+__device__ __forceinline__ int find_tile(const Attn &a, int units, int x, int lane, int *before) {
+    int done = 0;
+    for (int base = 0;; base += 32) {
+        const int n = tiles_at(a, base + lane, units);
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        incl += done;
+        const unsigned hit = __ballot_sync(0xffffffffu, incl > x);
+        if (hit || base + 32 >= a.n_seqs) {            // (x is below the total, so there is one)
+            const int src = hit ? __ffs(hit) - 1 : 31;
+            *before = __shfl_sync(0xffffffffu, incl - n, src);
+            return min(base + src, a.n_seqs - 1);
+        }
+        done = __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// A partial result: [rows][DV] outputs, [rows] maxima, [rows] sums.
+template <int DV> constexpr size_t kPartial = (size_t)kRows * (DV + 2);
+
 // One warp's share of one unit: an online softmax over tiles.
 template <int DK, int DV, bool QLO, int PM>
 struct Unit {
@@ -399,6 +499,28 @@ struct Unit {
     }
 };
 
+// A walk over a run: the unit and the tile that it has reached.
+struct Cursor {
+    int left;                          // tiles of the run from here on
+    int b, u, j, n, len;               // sequence, unit of it, tile of the unit, tiles of a unit, tokens
+    __device__ __forceinline__ int batch(int U) const { return min(min(U, n - j), left); }
+    __device__ __forceinline__ void step(const Attn &a, int units, int k) {
+        left -= k;
+        j += k;
+        if (j < n) return;
+        j = 0;
+        if (++u == units) {
+            u = 0;
+            if (left > 0) {            // the next sequence that holds anything
+                do {
+                    len = length(a.c, ++b);
+                    n = tiles_of(len);
+                } while (n == 0);
+            }
+        }
+    }
+};
+
 template <int DK, int DV, bool QLO, int PM>
 __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const Attn a) {
     using G = Geo<DK, DV>;
@@ -419,16 +541,23 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         c.b = blockIdx.x / units;
         c.u = blockIdx.x - c.b * units;
         c.len = length(a.c, c.b);
-        c.n = steps_of(a, c.len);
+        c.n = tiles_of(c.len);
         parts = min(G::WARPS, c.n);
         c.j = warp < parts ? run_begin(c.n, parts, warp) : 0;
         c.left = warp < parts ? run_begin(c.n, parts, warp + 1) - c.j : 0;
     } else {
-        const int T = steps_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+        const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
         // neighbouring runs on different SMs: few tiles spread over the GPU
         w = warp * gridDim.x + blockIdx.x;
         if (w >= W) return;
-        c = run_of_call(a, units, T, W, w, lane);
+        const int at = run_begin(T, W, w);
+        int before;
+        c.left = run_begin(T, W, w + 1) - at;
+        c.b = find_tile(a, units, at, lane, &before);
+        c.len = length(a.c, c.b);
+        c.n = tiles_of(c.len);
+        c.u = (at - before) / c.n;
+        c.j = at - before - c.u * c.n;
     }
     if (c.left > 0 && lane == 0 && __ldg(a.c.lens + c.b) > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
 
@@ -472,8 +601,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         unit.begin(a, b, hk, rb, lane);
         for (int j = j0; j < j1; j += U) {
             copy();                                    // into the stage that the last step left
-            // (one answer for the warp: its lanes stay together whatever happens)
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&full[warp][get], phase, &gave_up))) {
+            if (!ptx::mbar_wait(&full[warp][get], phase, &gave_up)) {
                 *a.c.status = GDN_ERR_TIMEOUT;
                 gave_up = 1;
                 // the copies in flight still write this block's shared memory
@@ -493,7 +621,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         }
         if (a.alone) break;
         const bool whole = j0 == 0 && j1 == c.n;
-        unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * partial<DV>(kRows), lane);
+        unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * kPartial<DV>, lane);
         c.step(a, units, j1 - j0);
     }
     if (!a.alone) return;
@@ -502,7 +630,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     __syncthreads();
     const int b = blockIdx.x / units, u = blockIdx.x - b * units, hk = u / a.n_rb, rb = u - hk * a.n_rb;
     float *part = reinterpret_cast<float *>(smem);
-    if (warp < parts) unit.end(a, b, hk, rb, parts == 1, part + warp * partial<DV>(kRows), lane);
+    if (warp < parts) unit.end(a, b, hk, rb, parts == 1, part + warp * kPartial<DV>, lane);
     if (parts == 1) return;
     __syncthreads();
     const int n_rows = min(kRows, a.R - rb * kRows);
@@ -510,19 +638,172 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         const int local = i / (DV / 4), x = i - local * (DV / 4), row = rb * kRows + local;
         const float *m = part + kRows * DV + local, *l = m + kRows;
         float top = -INFINITY, sum = 0.f;
-        for (int k = 0; k < parts; ++k) top = fmaxf(top, m[k * partial<DV>(kRows)]);
+        for (int k = 0; k < parts; ++k) top = fmaxf(top, m[k * kPartial<DV>]);
         const float base = top == -INFINITY ? 0.f : top;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < parts; ++k) {
-            const float wt = exp2_approx((m[k * partial<DV>(kRows)] - base) * kLog2e);
-            const float4 v = reinterpret_cast<const float4 *>(part + k * partial<DV>(kRows) + local * DV)[x];
-            sum = fmaf(l[k * partial<DV>(kRows)], wt, sum);
+            const float wt = exp2_approx((m[k * kPartial<DV>] - base) * kLog2e);
+            const float4 v = reinterpret_cast<const float4 *>(part + k * kPartial<DV> + local * DV)[x];
+            sum = fmaf(l[k * kPartial<DV>], wt, sum);
             y = make_float4(fmaf(v.x, wt, y.x), fmaf(v.y, wt, y.y), fmaf(v.z, wt, y.z), fmaf(v.w, wt, y.w));
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const size_t at = (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV + 4 * x;
         store2(a.out, a.out_type, at, y.x * inv, y.y * inv);
         store2(a.out, a.out_type, at + 2, y.z * inv, y.w * inv);
+    }
+}
+
+// Joins the partial results of the rows that several runs share.  A block has
+// `rpb` rows, a warp each.  A warp reads the maxima and sums of up to 32 parts at
+// once, so their weights are known before the outputs are read, and those loads
+// do not wait for one another.  A row of more parts is left to the whole block.
+constexpr int kJoinWarps = 8;
+template <int DV>
+struct Join {
+    static constexpr int V = DV == 64 ? 2 : 4, C = DV == 256 ? 2 : 1;   // columns of a lane: C times V
+    float x[C * V];
+    float M, L;
+    // parts first, first + step, ... below n of a row; part 0 is in its run's slot 1
+    __device__ __forceinline__ void parts(const float *ws, int w0, int n, int local, int first, int step, int lane) {
+        M = -INFINITY;
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < C * V; ++e) x[e] = 0.f;
+        for (int p0 = first; p0 < n; p0 += 32 * step) {
+            const int mine = p0 + lane * step, cnt = min(32, (n - p0 + step - 1) / step);
+            const float *at = ws + (size_t)partial_slot(w0 + mine, mine == 0) * kPartial<DV>;
+            float m = -INFINITY, l = 0.f;
+            if (mine < n) {
+                m = __ldcg(at + kRows * DV + local);
+                l = __ldcg(at + kRows * (DV + 1) + local);
+            }
+            float top = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, M);
+            const float base = top == -INFINITY ? 0.f : top;
+            const float old = exp2_approx((M - base) * kLog2e), wt = exp2_approx((m - base) * kLog2e);
+            M = top;
+            float sum = l * wt;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            L = fmaf(L, old, sum);
+#pragma unroll
+            for (int e = 0; e < C * V; ++e) x[e] *= old;
+            constexpr int B = 8;                       // loads in flight (they do not pass the shuffles)
+            for (int i0 = 0; i0 < cnt; i0 += B) {
+                float v[B][C * V];
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const int p = p0 + min(i0 + i, cnt - 1) * step;
+                    const float *row = ws + (size_t)partial_slot(w0 + p, p == 0) * kPartial<DV> + local * DV;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        if constexpr (V == 2) {
+                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(row) + lane);
+                            v[i][0] = y.x; v[i][1] = y.y;
+                        } else {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(row + 128 * c) + lane);
+                            v[i][4 * c] = y.x; v[i][4 * c + 1] = y.y; v[i][4 * c + 2] = y.z; v[i][4 * c + 3] = y.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const float k = __shfl_sync(0xffffffffu, wt, min(i0 + i, 31));
+#pragma unroll
+                    for (int e = 0; e < C * V; ++e)
+                        if (i0 + i < cnt) x[e] = fmaf(v[i][e], k, x[e]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ int column(int c, int e, int lane) const { return c * 128 + lane * V + e; }
+    __device__ __forceinline__ void store(const Attn &a, size_t at, int lane) const {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                store2(a.out, a.out_type, at + column(c, e, lane), x[c * V + e] * inv, x[c * V + e + 1] * inv);
+            }
+    }
+};
+
+template <int DV>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, int n_rows) {
+    __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = a.c.Hkv * a.n_rb;
+    const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+    auto place = [&](int r, int &local) {              // where a row's output goes
+        const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
+        local = row % kRows;
+        return (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV;
+    };
+    const int r0 = blockIdx.x * rpb, r = r0 + warp;
+    int w0 = 0, n = -1;                                // runs that share the row; -1: none of ours
+    if (warp < rpb && r < n_rows) {
+        const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
+        const int tiles = tiles_of(length(a.c, b));
+        n = 0;
+        if (tiles > 0) {
+            const int first = tiles_before(a, units, b, lane) + (hk * a.n_rb + row / kRows) * tiles;
+            w0 = run_of(T, W, first);
+            n = run_of(T, W, first + tiles - 1) - w0 + 1;
+        }
+    }
+    if (lane == 0) {
+        s_w0[warp] = w0;
+        s_n[warp] = n;
+    }
+    // the attention kernel's results; every block waits, so that this grid never
+    // ends before that one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Join<DV> join;
+    int local;
+    if (n >= 0 && n != 1 && n <= 32) {                 // (one run had it all: written; none: zeros)
+        const size_t at = place(r, local);
+        join.parts(a.ws, w0, n, local, 0, 1, lane);
+        join.store(a, at, lane);
+    }
+    __syncthreads();
+    for (int i = 0; i < rpb; ++i) {
+        if (s_n[i] <= 32) continue;
+        const size_t at = place(r0 + i, local);
+        join.parts(a.ws, s_w0[i], s_n[i], local, warp, kJoinWarps, lane);
+#pragma unroll
+        for (int c = 0; c < join.C; ++c)
+#pragma unroll
+            for (int e = 0; e < join.V; ++e) s_x[warp][join.column(c, e, lane)] = join.x[c * join.V + e];
+        if (lane == 0) {
+            s_m[warp] = join.M;
+            s_l[warp] = join.L;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int e = 0; e < join.C * join.V; ++e) join.x[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                const float wt = exp2_approx((s_m[k] - base) * kLog2e);
+                sum = fmaf(s_l[k], wt, sum);
+#pragma unroll
+                for (int c = 0; c < join.C; ++c)
+#pragma unroll
+                    for (int e = 0; e < join.V; ++e)
+                        join.x[c * join.V + e] = fmaf(s_x[k][join.column(c, e, lane)], wt, join.x[c * join.V + e]);
+            }
+            join.L = sum;
+            join.store(a, at, lane);
+        }
+        __syncthreads();
     }
 }
 
@@ -541,7 +822,23 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     attn_kernel<DK, DV, QLO, PM><<<grid, G::WARPS * 32, G::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.alone) return e;
-    return launch_join<DV>(a, stream);
+    // few rows: a block each, so that long rows are shared out; many: a warp each
+    const int n_rows = a.n_seqs * a.c.Hkv * a.R;
+    const int rpb = (int)(n_rows >= 2 * kGrid * kJoinWarps ? kJoinWarps : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(((unsigned)n_rows + rpb - 1) / rpb);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
+    // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
+    // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
+    // as a plain launch.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<DV>, a, rpb, n_rows);
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
@@ -566,23 +863,21 @@ cudaError_t launch_k(const Attn &a, cudaStream_t stream) {
 // (over all kv heads and row blocks): tiles are counted in 32 bits.
 struct Plan {
     int W;                             // runs at most
-    bool alone, many;                  // (steps are of one tile, with many rows of 8)
+    bool alone;
     size_t bytes;                      // of workspace
 };
 bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, Plan *p) {
     const long long R = (long long)(H / Hkv) * n_q;
-    p->many = R > kRows && many_rows_ok(dk, dv);
-    const int warps = p->many ? 1 : warps_of(dk, dv), rows = p->many ? kManyRows : kRows;
-    const long long n_rb = (R + rows - 1) / rows;
-    if (p->many) tiles = (tiles + 7) / 8;
+    const int warps = warps_of(dk, dv);
+    const long long n_rb = (R + kRows - 1) / kRows;
     unsigned long long units, all;
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
         !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
         return false;
     // few units of few tiles: a block each, whose warps meet in shared memory
-    p->alone = !p->many && tiles <= kAloneTiles * warps && units <= kAloneUnits;
+    p->alone = tiles <= kAloneTiles * warps && units <= kAloneUnits;
     p->W = (int)(all < (unsigned long long)(kGrid * warps) ? all : (unsigned long long)(kGrid * warps));
-    p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)rows * (dv + 2) * sizeof(float);
+    p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)kRows * (dv + 2) * sizeof(float);
     return true;
 }
 
@@ -667,14 +962,13 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
         if (!pool) return GDN_ERR_CUDA;
         if (cudaMallocFromPoolAsync(&ws, need, pool, st) != cudaSuccess) return GDN_ERR_NOMEM;
     }
-    const int R = n_heads / n_heads_kv * n_q, block = p.many ? kManyRows : kRows;
+    const int R = n_heads / n_heads_kv * n_q;
     const Attn a{{static_cast<uint8_t *>(const_cast<void *>(cache)), page_table, seq_lens, status, n_pages,
                   n_heads_kv, page_size / kTile, max_pages, head_dim_k, head_dim_v},
                  q, mask, out, static_cast<float *>(ws), n_seqs, n_heads, n_q, R,
-                 (R + block - 1) / block, p.W, block, p.many ? 7 : 4, scale, dtype, out_dtype, causal != 0, p.alone};
+                 (R + kRows - 1) / kRows, p.W, scale, dtype, out_dtype, causal != 0, p.alone};
     cudaError_t e;
-    switch (p.many ? 0 : head_dim_k) {
-        case 0: e = launch_many_rows(a, st); break;
+    switch (head_dim_k) {
         case 64: e = launch_k<64>(a, st); break;
         case 128: e = launch_k<128>(a, st); break;
         default: e = launch_k<256>(a, st); break;
