@@ -16,6 +16,14 @@ head_dim) fp32 [value][key] or None (zeros).  out is fp32 and already carries
 "Ops" and its shape table.)  q and k may carry fewer heads n_k (dividing
 n_heads): value head i then reads key head i % n_k, the tiled mapping of the
 model card's contract notes.
+
+Beside it, for a hybrid's attention layers: ``flash_attn`` over dense keys and
+values, and a paged 4-bit cache (``kv4_cache``, ``kv4_write``, ``kv4_read``,
+``flash_attn_kv4``).  A decode step of a layer over that cache:
+
+    lens += 1
+    kv4_write(k, v, cache, page_table, lens)
+    out = flash_attn_kv4(q, cache, page_table, lens)
 """
 from __future__ import annotations
 

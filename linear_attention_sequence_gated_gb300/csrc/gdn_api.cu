@@ -308,7 +308,7 @@ const char *gdn_status_string(int status) {
         case GDN_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
         case GDN_ERR_NOMEM: return "stream-ordered workspace allocation failed";
         case GDN_ERR_DTYPE: return "dtype not supported on the requested path (chunked: bf16 only)";
-        case GDN_ERR_SHAPE: return "shape outside the op's scope (flash_attn: 20 or more queries)";
+        case GDN_ERR_SHAPE: return "shape outside the op's scope (attention: 20 or more queries; cache: page size)";
         case GDN_ERR_SCRATCH:
             return "the call needs more scratch than gdn_forward_noalloc's fixed 64 MiB array";
         case GDN_ERR_PAGE: return "a page table entry or a length outside the cache (seen on the device)";
@@ -316,7 +316,7 @@ const char *gdn_status_string(int status) {
     }
 }
 
-int gdn_version(void) { return 100; }
+int gdn_version(void) { return 200; }
 
 int gdn_selftest_wait_timeout(gdn_stream_t stream) {
     int *status = status_word_for_current_device();

@@ -54,7 +54,9 @@ constexpr int kAloneUnits = 2 * kGrid; // a CTA to itself
 // Rows of a unit: one MMA column tile.  More rows of a kv head are more units, which
 // decode the tiles again (from L2): blocks of 16 rows decode half as often, but took
 // twice the registers and so half the warps, and 16 x 5 queries x 32/8 x 5001 x 128 took
-// 57 us so and 49 us with blocks of 8.
+// 57 us so and 49 us with blocks of 8.  (Steps of 128 tokens decoded once for 32 rows
+// into operand tiles of tcgen05.mma took 99 us: the chain of copy, decoding, product,
+// softmax and product across warps is 2.4 us a step and 8 us a unit.)
 constexpr int kRows = 8;
 
 // Shape of the kernel for widths DK and DV.  Each warp streams its run through a ring
@@ -601,7 +603,8 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         unit.begin(a, b, hk, rb, lane);
         for (int j = j0; j < j1; j += U) {
             copy();                                    // into the stage that the last step left
-            if (!ptx::mbar_wait(&full[warp][get], phase, &gave_up)) {
+            // (one answer for the warp: its lanes stay together whatever happens)
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&full[warp][get], phase, &gave_up))) {
                 *a.c.status = GDN_ERR_TIMEOUT;
                 gave_up = 1;
                 // the copies in flight still write this block's shared memory
