@@ -302,7 +302,7 @@ int gdn_flash_attn_supports(int n_q, int head_dim_k, int head_dim_v);
  * touched, and tokens of such a page, or from position max_pages * page_size
  * on, count as absent (not written, read as zeros, not attended to).
  * Pages may be shared by sequences for reading; a call that writes a page must
- * have it through one sequence only.
+ * have it through one entry of one sequence's table only.
  *
  * Supported: head_dim_k and head_dim_v each 64, 128 or 256 (gdn_kv4_supports,
  * else GDN_ERR_HEADDIM), page_size a multiple of 16 (else GDN_ERR_SHAPE), cache

@@ -48,8 +48,6 @@ namespace kv4 {
 namespace {
 
 constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for
-constexpr int kAloneTiles = 4;         // up to so many tiles a warp, and so many units, a unit has
-constexpr int kAloneUnits = 2 * kGrid; // a CTA to itself
 
 // Rows of a unit: one MMA column tile.  More rows of a kv head are more units, which
 // decode the tiles again (from L2): blocks of 16 rows decode half as often, but took
@@ -171,13 +169,22 @@ __device__ __forceinline__ void store2(void *out, int type, size_t i, float x, f
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
+// Runs of a call of T tiles: of at least 4 tiles, which a warp decodes in about the time
+// that it waits for one, and the fewer parts there are to join (1 sequence x 20000 tokens:
+// 24.6 us with runs of 1 tile and more, 16.9 of 2, 12.9 of 4).
+__device__ __forceinline__ int runs_of(const Attn &a, int T) { return min(a.W, (T + 3) / 4); }
+
 // Tiles of all units of sequence b.  Whole-warp: their total over the sequences
 // before `end`, and the sequence that tile x lies in with the tiles before it.
 __device__ __forceinline__ int tiles_at(const Attn &a, int b, int units) {
-    return b < a.n_seqs ? tiles_of(length(a.c, b)) * units : 0;
+    if (b >= a.n_seqs) return 0;
+    const int raw = __ldg(a.c.lens + b);
+    if (raw > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
+    return tiles_of(min(max(raw, 0), capacity(a.c))) * units;
 }
 __device__ __forceinline__ int tiles_before(const Attn &a, int units, int end, int lane) {
     int n = 0;
+#pragma unroll 4
     for (int b = lane; b < end; b += 32) n += tiles_at(a, b, units);
     return __reduce_add_sync(0xffffffffu, n);
 }
@@ -213,10 +220,10 @@ struct Unit {
     static constexpr int ST = DK >= 128 ? 8 : 4;       // MMA steps of a part
     static constexpr int VB = DV / 64;                 // value blocks, four M tiles each
     uint32_t qh[CK * ST][2], ql[QLO ? CK * ST : 1][2];
-    float f[2];                                    // row factors of the scores (not negative)
-    int qi[2];                                     // the row's query; -1: no such row
-    int all;                                           // tokens that every row sees and no mask changes
-    float m[2], l[2];                          // running maximum, sum of the weights
+    float f[2];                        // row factors of the scores (not negative)
+    int qi[2];                         // the row's query; -1: no such row
+    int all;                           // tokens that every row sees and no mask changes
+    float m[2], l[2];                  // running maximum, sum of the weights
     float o[VB * 4][4];
 
     __device__ __forceinline__ void begin(const Attn &a, int b, int hk, int rb, int lane) {
@@ -542,13 +549,13 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     if (a.alone) {
         c.b = blockIdx.x / units;
         c.u = blockIdx.x - c.b * units;
+        c.n = tiles_at(a, c.b, 1);
         c.len = length(a.c, c.b);
-        c.n = tiles_of(c.len);
         parts = min(G::WARPS, c.n);
         c.j = warp < parts ? run_begin(c.n, parts, warp) : 0;
         c.left = warp < parts ? run_begin(c.n, parts, warp + 1) - c.j : 0;
     } else {
-        const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+        const int T = tiles_before(a, units, a.n_seqs, lane), W = runs_of(a, T);
         // neighbouring runs on different SMs: few tiles spread over the GPU
         w = warp * gridDim.x + blockIdx.x;
         if (w >= W) return;
@@ -561,7 +568,6 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         c.u = (at - before) / c.n;
         c.j = at - before - c.u * c.n;
     }
-    if (c.left > 0 && lane == 0 && __ldg(a.c.lens + c.b) > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
 
     uint8_t *ring = smem + warp * G::RING;
     // Copies run ST - 1 stages ahead.  The tiles' addresses are looked up for a
@@ -660,7 +666,8 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
 // Joins the partial results of the rows that several runs share.  A block has
 // `rpb` rows, a warp each.  A warp reads the maxima and sums of up to 32 parts at
 // once, so their weights are known before the outputs are read, and those loads
-// do not wait for one another.  A row of more parts is left to the whole block.
+// do not wait for one another.  A row of more parts than a warp should take is left
+// to the whole block.
 constexpr int kJoinWarps = 8;
 template <int DV>
 struct Join {
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.c.Hkv * a.n_rb;
-    const int T = tiles_before(a, units, a.n_seqs, lane), W = min(a.W, T);
+    const int T = tiles_before(a, units, a.n_seqs, lane), W = runs_of(a, T);
     auto place = [&](int r, int &local) {              // where a row's output goes
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         local = row % kRows;
@@ -767,14 +774,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Join<DV> join;
     int local;
-    if (n >= 0 && n != 1 && n <= 32) {                 // (one run had it all: written; none: zeros)
+    // (one run had it all: written; none: zeros; many parts: the whole block's)
+    const int many = rpb == 1 ? 8 : 32;
+    if (n >= 0 && n != 1 && n <= many) {
         const size_t at = place(r, local);
         join.parts(a.ws, w0, n, local, 0, 1, lane);
         join.store(a, at, lane);
     }
     __syncthreads();
     for (int i = 0; i < rpb; ++i) {
-        if (s_n[i] <= 32) continue;
+        if (s_n[i] <= many) continue;
         const size_t at = place(r0 + i, local);
         join.parts(a.ws, s_w0[i], s_n[i], local, warp, kJoinWarps, lane);
 #pragma unroll
@@ -877,8 +886,12 @@ bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, 
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
         !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
         return false;
-    // few units of few tiles: a block each, whose warps meet in shared memory
-    p->alone = tiles <= kAloneTiles * warps && units <= kAloneUnits;
+    // Up to a unit an SM, of few tiles: a CTA each, whose warps meet in shared memory.
+    // The more units, the more tiles that takes to be slower than runs over the whole
+    // GPU and a join.  n tokens a sequence at 128 + 128, us so and joined: 1 unit, 700: 9.1
+    // and 11.0, 1500: 11.7 and 11.6; 64 units, 1500: 11.8 and 18.3, 3000: 17.3 and 21.2; 256
+    // units, 16: 12.6 and 9.9.
+    p->alone = units <= (unsigned long long)kGrid && tiles <= (4 + (long long)units / 8) * warps;
     p->W = (int)(all < (unsigned long long)(kGrid * warps) ? all : (unsigned long long)(kGrid * warps));
     p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)kRows * (dv + 2) * sizeof(float);
     return true;

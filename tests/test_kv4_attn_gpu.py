@@ -247,6 +247,39 @@ def test_bad_pages_are_reported_and_left_out():
     assert not c.run()[0].any() and gdn.device_status() == gdn.OK
 
 
+def test_a_length_past_the_table_is_reported_wherever_it_stands():
+    """In the middle of a run over several short sequences, and as a CTA's own."""
+    for B, at in ((200, 101), (200, 0), (9, 4)):
+        c = Case([16] * B, 2, 2, 1, 64, page=16, seed=B)
+        want = c.run()
+        assert gdn.device_status() == gdn.OK
+        c.lens[at] = 17
+        got = c.run()
+        assert gdn.device_status() == gdn.ERR_PAGE and torch.equal(got, want)
+
+
+def test_more_sequences_than_a_grid_has_rows():
+    """70000 sequences of up to 3 tokens: written, read back, attended to."""
+    B, d = 70000, 64
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 4, B)
+    k, v = (torch.randn((B, 1, 3, d), device="cuda") for _ in range(2))
+    cache = gdn.kv4_cache(B, 1, 16, d)
+    table = torch.randperm(B, device="cuda").to(torch.int32).reshape(B, 1)
+    n = i32(lens.tolist())
+    gdn.kv4_write(k, v, cache, table, n, n)
+    rk, rv = gdn.kv4_read(cache, table, n, 3, d, lens=n, dtype=torch.float32)
+    there = np.arange(3)[None] < lens[:, None]
+    kk, vk = (kv4.kept(np64(x)) * there[:, None, :, None] for x in (k, v))
+    assert np.array_equal(np64(rk), kk) and np.array_equal(np64(rv), vk)
+    q = torch.randn((B, 2, 1, d), device="cuda").to(torch.bfloat16)
+    got = np64(gdn.flash_attn_kv4(q, cache, table, n))[:, 0]                   # (B, H, d)
+    s = np.einsum("bhd,bnd->bhn", np64(q)[:, :, 0], kk[:, 0]) * float(np.float32(d ** -0.5))
+    p = np.exp(s) * there[:, None]
+    ref = np.einsum("bhn,bnd->bhd", p / np.maximum(p.sum(-1, keepdims=True), 1e-300), vk[:, 0])
+    assert oracle.parity_error(got, ref) <= TOL and gdn.device_status() == gdn.OK
+
+
 def test_shared_pages():
     """Two sequences that begin with the same pages."""
     c = Case([64, 64], 4, 2, 1, 128, page=32, seed=15)
