@@ -302,7 +302,8 @@ int gdn_flash_attn_supports(int n_q, int head_dim_k, int head_dim_v);
  * touched, and tokens of such a page, or from position max_pages * page_size
  * on, count as absent (not written, read as zeros, not attended to).
  * Pages may be shared by sequences for reading; a call that writes a page must
- * have it through one entry of one sequence's table only.
+ * have it through one entry of one sequence's table only, and is to be ordered
+ * (one stream, or events) with other calls that read or write that page.
  *
  * Supported: head_dim_k and head_dim_v each 64, 128 or 256 (gdn_kv4_supports,
  * else GDN_ERR_HEADDIM), page_size a multiple of 16 (else GDN_ERR_SHAPE), cache
@@ -364,16 +365,17 @@ int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, 
  * sequence's start, every token hidden by -inf) is zeros.  A mask of the type's
  * lowest finite value takes part in the softmax as the number it is.
  * Accumulation is fp32; the cache's values enter exactly, q exactly (fp32 as 22
- * bits), the softmax weights with 22 bits.  Results do not depend on timing.
+ * bits), the softmax weights with 22 bits (11 where q and out are both 16-bit).
+ * Results do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), the cache's widths and page
  * sizes, n_heads_kv dividing n_heads, page tables with room for fewer than 2^31
  * tiles of 16 tokens over all kv heads (and blocks of 8 of a kv head's (n_heads /
  * n_heads_kv) * n_q rows).  q and out 16-byte aligned; out must not
  * overlap an input.
  * workspace: caller's device buffer of gdn_flash_attn_kv4_workspace_bytes (0 where
- *   the call needs none, and for sizes that are not supported), 256-byte aligned, its contents ignored on entry and garbage on return, for one
- *   call at a time; or NULL: allocated and freed in stream order as by
- *   gdn_forward_ex.
+ *   the call needs none, and for sizes that are not supported), 256-byte aligned,
+ *   its contents ignored on entry and garbage on return, for one call at a time; or
+ *   NULL: allocated and freed in stream order as by gdn_forward_ex.
  */
 int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, const int *seq_lens,
                        const void *mask, void *out, int n_seqs, int n_heads, int n_heads_kv, int n_q,

@@ -1,7 +1,8 @@
 // C-ABI front end of libgdn.so: argument validation, path selection,
 // workspace handling and the device status word.  Every compute step runs in
 // the kernels of gdn_recurrent.cu and gdn_chunked.cu; this file launches
-// nothing else (the attention and cache entry points are beside their kernels).  Declarations and the full contract are in include/gdn.h.
+// nothing else (the attention and cache entry points are beside their kernels).
+// Declarations and the full contract are in include/gdn.h.
 #include <climits>
 #include <cmath>
 #include <cstdint>

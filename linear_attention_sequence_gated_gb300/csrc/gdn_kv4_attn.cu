@@ -958,8 +958,6 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
     for (Range in : {rc_, rt, rl, rq, rm})
         if (overlap(ro, in)) return GDN_ERR_ALIAS;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cap == 0)                                      // no room for a token: every row is zero
-        return cudaMemsetAsync(out, 0, out_bytes, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
     Plan p;
     if (!plan(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, cap / kTile, &p)) return GDN_ERR_ARG;
     const size_t need = p.bytes;

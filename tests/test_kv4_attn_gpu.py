@@ -258,6 +258,17 @@ def test_a_length_past_the_table_is_reported_wherever_it_stands():
         assert gdn.device_status() == gdn.ERR_PAGE and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("B", [3, 200])
+def test_a_table_without_pages(B):
+    """Rows are zeros; a length above its room is reported."""
+    cache, q = gdn.kv4_cache(0, 2, 16, 64), torch.randn((B, 4, 2, 64), device="cuda")
+    table, lens = i32([[]] * B), i32([0] * B)
+    for n, status in ((0, gdn.OK), (5, gdn.ERR_PAGE)):
+        lens[B - 1] = n
+        out = gdn.flash_attn_kv4(q, cache, table, lens, out=torch.ones((B, 2, 4, 64), device="cuda"))
+        assert not out.any() and gdn.device_status() == status
+
+
 def test_more_sequences_than_a_grid_has_rows():
     """70000 sequences of up to 3 tokens: written, read back, attended to."""
     B, d = 70000, 64
