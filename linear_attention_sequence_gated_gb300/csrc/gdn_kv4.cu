@@ -340,6 +340,7 @@ __device__ __forceinline__ void write_values(const Run &r, const Part &p, int la
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 8) write_kernel(const Run r) {
+    after_the_kernel_before();
     const int lane = threadIdx.x & 31;
     for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
         Part p;
@@ -441,6 +442,7 @@ __device__ __forceinline__ void read_values(const Run &r, const Part &p, const u
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, 8) read_kernel(const Run r) {
+    after_the_kernel_before();
     const int lane = threadIdx.x & 31;
     for (int b = blockIdx.y; b < r.n_seqs; b += gridDim.y) {
         Part p;
@@ -505,9 +507,7 @@ bool strided_bytes(const Strides &s, int n_seqs, int Hkv, int T, int d, unsigned
 
 template <typename T>
 cudaError_t launch(bool write, const Run &r, dim3 blocks, cudaStream_t stream) {
-    if (write) write_kernel<T><<<blocks, kWarps * 32, 0, stream>>>(r);
-    else read_kernel<T><<<blocks, kWarps * 32, 0, stream>>>(r);
-    return cudaGetLastError();
+    return launch_early(write ? write_kernel<T> : read_kernel<T>, blocks, kWarps * 32, 0, stream, r);
 }
 
 int run(bool write, void *k, void *v, const long long *strides, uint8_t *cache, const int *table,

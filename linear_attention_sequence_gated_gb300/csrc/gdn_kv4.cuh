@@ -28,6 +28,7 @@
 #include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 namespace gdn {
 namespace kv4 {
@@ -186,6 +187,32 @@ __device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float 
         : "=r"(w) : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
     return w;
 }
+#endif
+
+// The cache's kernels are launched as programmatic dependents, so that their blocks are
+// set up while the kernel before them in the stream ends.  Every thread waits for that
+// kernel's end before it reads or writes what a kernel before may write or read, so
+// when this kernel has ended, so have those before it.  Calls in a row, us: attention over
+// 64 x 32/8 x 4096 x 128: 68.4 -> 65.0, one token at 64: 8.2 -> 5.5; in captured steps,
+// 16 x 4 kv heads x 3000 x 128: 17.2 -> 16.6, a token's write and attention over 8 x 8 kv
+// heads x 500 x 128: 12.0 -> 11.4.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const A &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void after_the_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 #endif
 
 // How the attention's work is shared out: all tiles of all units (sequence, kv

@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     if (lane < ST) ptx::mbar_init(&full[warp][lane], 1);
     if (lane == 0) ptx::fence_mbar_init();
     __syncthreads();
+    after_the_kernel_before();
     const int units = a.c.Hkv * a.n_rb;
     Cursor c;
     int w = 0, parts = 0;                              // this run's number; runs of the block's own unit
@@ -769,9 +770,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
         s_w0[warp] = w0;
         s_n[warp] = n;
     }
-    // the attention kernel's results; every block waits, so that this grid never
-    // ends before that one
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_the_kernel_before();                         // the parts (lengths are older: the attention waited for them)
     Join<DV> join;
     int local;
     // (one run had it all: written; none: zeros; many parts: the whole block's)
@@ -831,26 +830,17 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     });
     if (e != cudaSuccess) return e;
     const int grid = a.alone ? a.n_seqs * a.c.Hkv * a.n_rb : kGrid;
-    attn_kernel<DK, DV, QLO, PM><<<grid, G::WARPS * 32, G::SMEM, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(attn_kernel<DK, DV, QLO, PM>, dim3(grid), G::WARPS * 32, G::SMEM, stream, a);
     if (e != cudaSuccess || a.alone) return e;
     // few rows: a block each, so that long rows are shared out; many: a warp each
     const int n_rows = a.n_seqs * a.c.Hkv * a.R;
     const int rpb = (int)(n_rows >= 2 * kGrid * kJoinWarps ? kJoinWarps : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(((unsigned)n_rows + rpb - 1) / rpb);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
     // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
     // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
     // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
     // as a plain launch.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<DV>, a, rpb, n_rows);
+    return launch_early(join_kernel<DV>, dim3(((unsigned)n_rows + rpb - 1) / rpb), kJoinWarps * 32, 0, stream, a, rpb,
+                        n_rows);
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit

@@ -360,6 +360,56 @@ def test_a_decode_loop_captured_once():
     assert gdn.device_status() == gdn.OK
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("lens", [[40, 7], [3000, 900, 0, 2100]])
+def test_inputs_made_just_before_and_overwritten_just_after(lens, captured):
+    """By kernels, copies and another stream, eagerly and in a graph: one CTA a unit, and joined."""
+    c = Case(lens, 8, 2, 2, 128, page=16, seed=7)
+    want = c.run()
+    busy = torch.randn((3000, 3000), device="cuda")
+    cache, q, n = torch.zeros_like(c.cache), torch.zeros_like(c.q), torch.zeros_like(c.lens)
+    k, v, out = torch.zeros_like(c.k), torch.zeros_like(c.v), torch.zeros_like(want)
+    side = torch.cuda.Stream()
+
+    def step(main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            busy @ busy
+            k.copy_(c.k)
+            v.copy_(c.v)
+        n.copy_(c.lens)
+        main.wait_stream(side)
+        gdn.kv4_write(k, v, cache, c.table, n, n)
+        for x in (k, v):
+            x.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            busy @ busy
+            q.copy_(c.q)
+        main.wait_stream(side)
+        gdn.flash_attn_kv4(q, cache, c.table, n, out=out)
+        for x in (q, n, cache):
+            x.zero_()
+
+    main = torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step(main)
+        torch.cuda.synchronize()
+        run = lambda: step(main)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                step(main)
+            run = graph.replay
+        for _ in range(5):
+            out.fill_(float("nan"))
+            run()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    assert gdn.device_status() == gdn.OK
+
+
 def test_against_flash_attn_on_the_rows_read_back():
     """The path that it replaces: read back dense in f16 (exact), then dense attention."""
     c = Case([500, 500], 16, 4, 3, 256, dtype="f16", seed=18)
