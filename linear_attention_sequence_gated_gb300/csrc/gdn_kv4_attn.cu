@@ -63,10 +63,11 @@ constexpr int kRows = 8;
 // steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x 128: 68 us; 16 warps with steps of 2
 // tiles 72, 8 warps with steps of 4 82.)
 constexpr int warps_of(int dk, int dv) { return dk <= 128 && dv <= 128 ? 12 : 8; }
+constexpr int step_of(int dk, int dv) { return warps_of(dk, dv) == 12 ? 4 : 2; }
 template <int DK, int DV>
 struct Geo {
     static constexpr int WARPS = warps_of(DK, DV);
-    static constexpr int U = WARPS == 12 ? 4 : 2;
+    static constexpr int U = step_of(DK, DV);          // tiles of a step
     static constexpr int TB = tile_bytes(DK, DV);
     static constexpr int BUDGET = 216 * 1024;
     static constexpr int FIT = BUDGET / (WARPS * U * TB);
@@ -169,29 +170,34 @@ __device__ __forceinline__ void store2(void *out, int type, size_t i, float x, f
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// Runs of a call of T tiles: of at least 4 tiles, which a warp decodes in about the time
+// Work is shared out in steps of U tiles, counted from each unit's start: a step of fewer
+// tiles takes as long.
+__device__ __forceinline__ int steps_of(int tiles, int U) { return (tiles + U - 1) / U; }
+
+// Runs of a call of T steps: of at least 4 tiles, which a warp decodes in about the time
 // that it waits for one, and the fewer parts there are to join (1 sequence x 20000 tokens:
 // 24.6 us with runs of 1 tile and more, 16.9 of 2, 12.9 of 4).
-__device__ __forceinline__ int runs_of(const Attn &a, int T) { return min(a.W, (T + 3) / 4); }
+__device__ __forceinline__ int runs_of(const Attn &a, int T, int U) { return min(a.W, steps_of(T, 4 / U)); }
 
-// Tiles of all units of sequence b.  Whole-warp: their total over the sequences
-// before `end`, and the sequence that tile x lies in with the tiles before it.
-__device__ __forceinline__ int tiles_at(const Attn &a, int b, int units) {
+// Tiles of a unit of sequence b.
+__device__ __forceinline__ int tiles_at(const Attn &a, int b) {
     if (b >= a.n_seqs) return 0;
     const int raw = __ldg(a.c.lens + b);
     if (raw > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
-    return tiles_of(min(max(raw, 0), capacity(a.c))) * units;
+    return tiles_of(min(max(raw, 0), capacity(a.c)));
 }
-__device__ __forceinline__ int tiles_before(const Attn &a, int units, int end, int lane) {
+// Whole-warp: the steps of all units of the sequences before `end`, and the sequence
+// that step x lies in with the steps before it.
+__device__ __forceinline__ int steps_before(const Attn &a, int U, int units, int end, int lane) {
     int n = 0;
 #pragma unroll 4
-    for (int b = lane; b < end; b += 32) n += tiles_at(a, b, units);
+    for (int b = lane; b < end; b += 32) n += steps_of(tiles_at(a, b), U) * units;
     return __reduce_add_sync(0xffffffffu, n);
 }
-__device__ __forceinline__ int find_tile(const Attn &a, int units, int x, int lane, int *before) {
+__device__ __forceinline__ int find_step(const Attn &a, int U, int units, int x, int lane, int *before) {
     int done = 0;
     for (int base = 0;; base += 32) {
-        const int n = tiles_at(a, base + lane, units);
+        const int n = steps_of(tiles_at(a, base + lane), U) * units;
         int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -509,12 +515,15 @@ struct Unit {
 };
 
 // A walk over a run: the unit and the tile that it has reached.
+template <int U>
 struct Cursor {
-    int left;                          // tiles of the run from here on
+    int left;                          // steps of the run from here on
     int b, u, j, n, len;               // sequence, unit of it, tile of the unit, tiles of a unit, tokens
-    __device__ __forceinline__ int batch(int U) const { return min(min(U, n - j), left); }
-    __device__ __forceinline__ void step(const Attn &a, int units, int k) {
-        left -= k;
+    // the run's tiles of this unit
+    __device__ __forceinline__ int tiles() const { return min(n - j, left * U); }
+    // k tiles on (whole steps, or to the unit's end)
+    __device__ __forceinline__ void next(const Attn &a, int units, int k) {
+        left -= steps_of(k, U);
         j += k;
         if (j < n) return;
         j = 0;
@@ -545,35 +554,37 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     __syncthreads();
     after_the_kernel_before();
     const int units = a.c.Hkv * a.n_rb;
-    Cursor c;
+    Cursor<U> c;
     int w = 0, parts = 0;                              // this run's number; runs of the block's own unit
     if (a.alone) {
         c.b = blockIdx.x / units;
         c.u = blockIdx.x - c.b * units;
-        c.n = tiles_at(a, c.b, 1);
         c.len = length(a.c, c.b);
-        parts = min(G::WARPS, c.n);
-        c.j = warp < parts ? run_begin(c.n, parts, warp) : 0;
-        c.left = warp < parts ? run_begin(c.n, parts, warp + 1) - c.j : 0;
+        const int n = tiles_at(a, c.b);
+        parts = min(G::WARPS, n);
+        c.j = warp < parts ? run_begin(n, parts, warp) : 0;
+        c.n = warp < parts ? run_begin(n, parts, warp + 1) : 0;
+        c.left = steps_of(c.n - c.j, U);
     } else {
-        const int T = tiles_before(a, units, a.n_seqs, lane), W = runs_of(a, T);
+        const int T = steps_before(a, U, units, a.n_seqs, lane), W = runs_of(a, T, U);
         // neighbouring runs on different SMs: few tiles spread over the GPU
         w = warp * gridDim.x + blockIdx.x;
         if (w >= W) return;
         const int at = run_begin(T, W, w);
         int before;
         c.left = run_begin(T, W, w + 1) - at;
-        c.b = find_tile(a, units, at, lane, &before);
+        c.b = find_step(a, U, units, at, lane, &before);
         c.len = length(a.c, c.b);
         c.n = tiles_of(c.len);
-        c.u = (at - before) / c.n;
-        c.j = at - before - c.u * c.n;
+        const int each = steps_of(c.n, U);
+        c.u = (at - before) / each;
+        c.j = (at - before - c.u * each) * U;
     }
 
     uint8_t *ring = smem + warp * G::RING;
     // Copies run ST - 1 stages ahead.  The tiles' addresses are looked up for a
     // window of up to 32 tiles of a unit at once, one a lane.
-    Cursor ahead = c;
+    Cursor<U> ahead = c;
     const uint8_t *src = nullptr;
     unsigned have = 0;                                 // tiles of the window whose pages exist
     int off = 0, count = 0, put = 0;                   // window's tiles copied, its tiles; next stage
@@ -581,10 +592,10 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         if (off == count) {
             if (ahead.left <= 0) return;
             off = 0;
-            count = ahead.batch(32);
+            count = min(32, ahead.tiles());
             src = lane < count ? tile_ptr(a.c, ahead.b, ahead.u / a.n_rb, ahead.j + lane) : nullptr;
             have = __ballot_sync(0xffffffffu, src != nullptr);
-            ahead.step(a, units, count);
+            ahead.next(a, units, count);
         }
         const int k = min(U, count - off);
         const unsigned mine = have >> off & ((1u << k) - 1u);
@@ -606,7 +617,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     uint32_t phase = 0;
     while (c.left > 0) {
         const int b = c.b, hk = c.u / a.n_rb, rb = c.u - hk * a.n_rb, j0 = c.j;
-        const int j1 = min(c.n, c.j + c.left), stop = min(c.len, j1 * kTile);
+        const int j1 = c.j + c.tiles(), stop = min(c.len, j1 * kTile);
         unit.begin(a, b, hk, rb, lane);
         for (int j = j0; j < j1; j += U) {
             copy();                                    // into the stage that the last step left
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         if (a.alone) break;
         const bool whole = j0 == 0 && j1 == c.n;
         unit.end(a, b, hk, rb, whole, a.ws + (size_t)partial_slot(w, j0 == 0) * kPartial<DV>, lane);
-        c.step(a, units, j1 - j0);
+        c.next(a, units, j1 - j0);
     }
     if (!a.alone) return;
 
@@ -743,12 +754,12 @@ struct Join {
 };
 
 template <int DV>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int rpb, int n_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int U, int rpb, int n_rows) {
     __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.c.Hkv * a.n_rb;
-    const int T = tiles_before(a, units, a.n_seqs, lane), W = runs_of(a, T);
+    const int T = steps_before(a, U, units, a.n_seqs, lane), W = runs_of(a, T, U);
     auto place = [&](int r, int &local) {              // where a row's output goes
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         local = row % kRows;
@@ -758,12 +769,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     int w0 = 0, n = -1;                                // runs that share the row; -1: none of ours
     if (warp < rpb && r < n_rows) {
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
-        const int tiles = tiles_of(length(a.c, b));
+        const int steps = steps_of(tiles_of(length(a.c, b)), U);
         n = 0;
-        if (tiles > 0) {
-            const int first = tiles_before(a, units, b, lane) + (hk * a.n_rb + row / kRows) * tiles;
+        if (steps > 0) {
+            const int first = steps_before(a, U, units, b, lane) + (hk * a.n_rb + row / kRows) * steps;
             w0 = run_of(T, W, first);
-            n = run_of(T, W, first + tiles - 1) - w0 + 1;
+            n = run_of(T, W, first + steps - 1) - w0 + 1;
         }
     }
     if (lane == 0) {
@@ -839,8 +850,8 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
     // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
     // as a plain launch.
-    return launch_early(join_kernel<DV>, dim3(((unsigned)n_rows + rpb - 1) / rpb), kJoinWarps * 32, 0, stream, a, rpb,
-                        n_rows);
+    return launch_early(join_kernel<DV>, dim3(((unsigned)n_rows + rpb - 1) / rpb), kJoinWarps * 32, 0, stream, a, G::U,
+                        rpb, n_rows);
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
