@@ -60,8 +60,9 @@ constexpr int kRows = 8;
 // Shape of the kernel for widths DK and DV.  Each warp streams its run through a ring
 // of its own in shared memory: stages of U tiles, each tile one bulk copy.  12 warps
 // and steps of 4 tiles where 168 registers a thread hold the output tile and two
-// steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x 128: 68 us; 16 warps with steps of 2
-// tiles 72, 8 warps with steps of 4 82.)
+// steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x 128: 64 us; 12 warps with steps of 2
+// tiles 72, with steps of 3 68; 8 warps with steps of 4 82, 16 with steps of 2 72, both
+// when it took 68.)
 constexpr int warps_of(int dk, int dv) { return dk <= 128 && dv <= 128 ? 12 : 8; }
 constexpr int step_of(int dk, int dv) { return warps_of(dk, dv) == 12 ? 4 : 2; }
 template <int DK, int DV>
@@ -679,8 +680,9 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
 // `rpb` rows, a warp each.  A warp reads the maxima and sums of up to 32 parts at
 // once, so their weights are known before the outputs are read, and those loads
 // do not wait for one another.  A row of more parts than a warp should take is left
-// to the whole block.
-constexpr int kJoinWarps = 8;
+// to the whole block, of JW warps: 16 where units have 128 parts and more (60000 tokens
+// over one kv head: 15.7 us, and 19.2 with 8 warps; 63 parts of 3 x 2 kv heads at
+// (64, 256): 14.1 and 13.4).
 template <int DV>
 struct Join {
     static constexpr int V = DV == 64 ? 2 : 4, C = DV == 256 ? 2 : 1;   // columns of a lane: C times V
@@ -753,10 +755,10 @@ struct Join {
     }
 };
 
-template <int DV>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int U, int rpb, int n_rows) {
-    __shared__ int s_w0[kJoinWarps], s_n[kJoinWarps];
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps][DV];
+template <int DV, int JW>
+__global__ void __launch_bounds__(JW * 32) join_kernel(const Attn a, int U, int rpb, int n_rows) {
+    __shared__ int s_w0[JW], s_n[JW];
+    __shared__ float s_m[JW], s_l[JW], s_x[JW][DV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.c.Hkv * a.n_rb;
     const int T = steps_before(a, U, units, a.n_seqs, lane), W = runs_of(a, T, U);
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
     for (int i = 0; i < rpb; ++i) {
         if (s_n[i] <= many) continue;
         const size_t at = place(r0 + i, local);
-        join.parts(a.ws, s_w0[i], s_n[i], local, warp, kJoinWarps, lane);
+        join.parts(a.ws, s_w0[i], s_n[i], local, warp, JW, lane);
 #pragma unroll
         for (int c = 0; c < join.C; ++c)
 #pragma unroll
@@ -808,12 +810,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
         if (warp == 0) {
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
+            for (int k = 0; k < JW; ++k) top = fmaxf(top, s_m[k]);
             const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
             for (int e = 0; e < join.C * join.V; ++e) join.x[e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) {
+            for (int k = 0; k < JW; ++k) {
                 const float wt = exp2_approx((s_m[k] - base) * kLog2e);
                 sum = fmaf(s_l[k], wt, sum);
 #pragma unroll
@@ -831,6 +833,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attn a, int
 
 // ------------------------------------------------------------------ host
 
+template <int DV, int JW>
+cudaError_t launch_join(const Attn &a, int U, cudaStream_t stream) {
+    // few rows: a block each, so that long rows are shared out; many: a warp each
+    const int n_rows = a.n_seqs * a.c.Hkv * a.R;
+    const int rpb = (int)(n_rows >= 2 * kGrid * JW ? JW : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
+    // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
+    // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
+    // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
+    // as a plain launch.
+    return launch_early(join_kernel<DV, JW>, dim3(((unsigned)n_rows + rpb - 1) / rpb), JW * 32, 0, stream, a, U, rpb,
+                        n_rows);
+}
+
 template <int DK, int DV, bool QLO, int PM>
 cudaError_t launch(const Attn &a, cudaStream_t stream) {
     using G = Geo<DK, DV>;
@@ -843,15 +858,8 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
     const int grid = a.alone ? a.n_seqs * a.c.Hkv * a.n_rb : kGrid;
     e = launch_early(attn_kernel<DK, DV, QLO, PM>, dim3(grid), G::WARPS * 32, G::SMEM, stream, a);
     if (e != cudaSuccess || a.alone) return e;
-    // few rows: a block each, so that long rows are shared out; many: a warp each
-    const int n_rows = a.n_seqs * a.c.Hkv * a.R;
-    const int rpb = (int)(n_rows >= 2 * kGrid * kJoinWarps ? kJoinWarps : (n_rows + 2 * kGrid - 1) / (2 * kGrid));
-    // Its blocks start as the attention kernel's end (no earlier trigger: blocks that
-    // only wait would gather on the first SM that has room, and stay there).  2 x 16/4
-    // x (100003, 50001) x 128: 52 us triggered at the kernel's start, 42 at its end, 44
-    // as a plain launch.
-    return launch_early(join_kernel<DV>, dim3(((unsigned)n_rows + rpb - 1) / rpb), kJoinWarps * 32, 0, stream, a, G::U,
-                        rpb, n_rows);
+    const bool many = a.W >= 128ll * a.n_seqs * a.c.Hkv * a.n_rb;
+    return many ? launch_join<DV, 16>(a, G::U, stream) : launch_join<DV, 8>(a, G::U, stream);
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
@@ -887,12 +895,14 @@ bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, 
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
         !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
         return false;
-    // Up to a unit an SM, of few tiles: a CTA each, whose warps meet in shared memory.
-    // The more units, the more tiles that takes to be slower than runs over the whole
-    // GPU and a join.  n tokens a sequence at 128 + 128, us so and joined: 1 unit, 700: 9.1
-    // and 11.0, 1500: 11.7 and 11.6; 64 units, 1500: 11.8 and 18.3, 3000: 17.3 and 21.2; 256
-    // units, 16: 12.6 and 9.9.
-    p->alone = units <= (unsigned long long)kGrid && tiles <= (4 + (long long)units / 8) * warps;
+    // Up to a unit an SM, of few tiles: a CTA each, whose warps meet in shared memory.  It
+    // takes as long as 4 tiles a warp do, times how many of those the unit has; the more
+    // units, the later runs over the whole GPU and a join are faster.  n tokens a sequence
+    // at 128 + 128, us so and joined: 1 unit, 700: 8.5 and 9.7, 1000: 11.3 and 9.5; 32
+    // units, 1000: 11.5 and 10.2; 64 units, 2200: 14.2 and 15.7, 3000: 16.9 and 16.3; 128
+    // units, 4500: 22.9 and 25.2; 256 units, 16: 12.6 and 9.9.
+    const long long rounds = units < 40 ? 1 : (long long)units / 20;
+    p->alone = units <= (unsigned long long)kGrid && tiles <= 4 * rounds * warps;
     p->W = (int)(all < (unsigned long long)(kGrid * warps) ? all : (unsigned long long)(kGrid * warps));
     p->bytes = p->alone ? 0 : (size_t)p->W * 2 * (size_t)kRows * (dv + 2) * sizeof(float);
     return true;
