@@ -303,24 +303,25 @@ def _kv4_dtype(dtype, what):
 
 
 def _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, lens=None):
-    """Shapes, types and devices of a cache and what goes with it; its device's index."""
-    if cache.dim() != 4 or cache.dtype != torch.uint8 or cache.shape[1] != Hkv \
-            or cache.shape[3] != 9 * (dk + dv):
-        raise ValueError(f"cache: expected (n_pages, {Hkv}, page_size / 16, {9 * (dk + dv)}) uint8, got "
-                         f"{tuple(cache.shape)} {cache.dtype}")
-    int32 = torch.int32
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != int32:
-        raise ValueError(f"page_table: expected ({B}, max_pages) int32, got {tuple(page_table.shape)} "
+    """Shapes, types and devices of a cache and what goes with it; its device's
+    index, pages, tokens of a page and pages of a sequence's table."""
+    shape, width, int32 = cache.shape, 9 * (dk + dv), torch.int32
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != width or cache.dtype != torch.uint8:
+        raise ValueError(f"cache: expected (n_pages, {Hkv}, page_size / 16, {width}) uint8, got "
+                         f"{tuple(shape)} {cache.dtype}")
+    pages = page_table.shape
+    if len(pages) != 2 or pages[0] != B or page_table.dtype != int32:
+        raise ValueError(f"page_table: expected ({B}, max_pages) int32, got {tuple(pages)} "
                          f"{page_table.dtype}")
     dev = cache.get_device()
     for t in (seq_lens,) if lens is None else (seq_lens, lens):
-        if t.dim() != 1 or t.shape[0] != B or t.dtype != int32:
+        if t.shape != (B,) or t.dtype != int32:
             raise ValueError(f"lengths: expected ({B},) int32, got {tuple(t.shape)} {t.dtype}")
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError("lengths must be contiguous and on the cache's device")
     if dev < 0 or page_table.get_device() != dev or not cache.is_contiguous() or not page_table.is_contiguous():
         raise ValueError("cache and page_table must be contiguous CUDA tensors on one device")
-    return dev
+    return dev, shape[0], shape[2] * 16, pages[1]
 
 
 def _kv4_call(torch, dev, stream, call):
@@ -331,7 +332,7 @@ def _kv4_call(torch, dev, stream, call):
             raise ValueError("stream must be on the tensors' device")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return call(torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         return call(torch._C._cuda_getCurrentRawStream(dev))
@@ -371,12 +372,13 @@ def kv4_write(k, v, cache, page_table, seq_lens, new_lens=None, *, stream=None):
     include/gdn.h."""
     L, torch = lib(), _kv4_torch()
     dt = _kv4_dtype(k.dtype, "k/v")
-    if k.dim() != 4 or v.dim() != 4 or v.shape[:3] != k.shape[:3] or v.dtype != k.dtype:
+    kn, vn = k.shape, v.shape
+    if len(kn) != 4 or len(vn) != 4 or vn[:3] != kn[:3] or v.dtype != k.dtype:
         raise ValueError("k, v: expected (n_seqs, n_heads_kv, n_new, dk / dv) of one dtype, got "
-                         f"{tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
-    B, Hkv, T, dk = k.shape
-    dv = v.shape[3]
-    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, new_lens)
+                         f"{tuple(kn)} {k.dtype}, {tuple(vn)} {v.dtype}")
+    B, Hkv, T, dk = kn
+    dv = vn[3]
+    dev, n_pages, page, max_pages = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, new_lens)
     ks, vs = k.stride(), v.stride()
     if k.get_device() != dev or v.get_device() != dev:
         raise ValueError("all tensors must be on one CUDA device")
@@ -388,7 +390,7 @@ def kv4_write(k, v, cache, page_table, seq_lens, new_lens=None, *, stream=None):
     def call(handle):
         return L.gdn_kv4_write(k.data_ptr(), v.data_ptr(), strides, cache.data_ptr(), page_table.data_ptr(),
                                seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, T,
-                               Hkv, dk, dv, cache.shape[0], cache.shape[2] * 16, page_table.shape[1], dt, handle)
+                               Hkv, dk, dv, n_pages, page, max_pages, dt, handle)
 
     rc = _kv4_call(torch, dev, stream, call)
     if rc != OK:
@@ -414,7 +416,7 @@ def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_d
     if cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("cache must be 4-D and page_table 2-D")
     B, Hkv = page_table.shape[0], cache.shape[1]
-    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, lens)
+    dev, n_pages, page, max_pages = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv, lens)
     for name, t, d in (("k_out", k_out, dk), ("v_out", v_out, dv)):
         if t is not None and (tuple(t.shape) != (B, Hkv, n_tokens, d) or t.dtype != dtype
                               or not t.is_contiguous() or t.get_device() != dev):
@@ -425,7 +427,7 @@ def kv4_read(cache, page_table, seq_lens, n_tokens: int, head_dim_k: int, head_d
         v = torch.empty((B, Hkv, n_tokens, dv), dtype=dtype, device=cache.device) if v_out is None else v_out
         rc = L.gdn_kv4_read(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
                             None if lens is None else lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, n_tokens,
-                            Hkv, dk, dv, cache.shape[0], cache.shape[2] * 16, page_table.shape[1], dt, handle)
+                            Hkv, dk, dv, n_pages, page, max_pages, dt, handle)
         if rc != OK:
             raise GdnError(rc, "gdn_kv4_read")
         return k, v
@@ -457,12 +459,12 @@ def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, s
     the library allocates in stream order."""
     L, torch = lib(), _kv4_torch()
     dt = _kv4_dtype(q.dtype, "q")
-    if q.dim() != 4 or cache.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("q and cache must be 4-D and page_table 2-D")
+    if q.dim() != 4 or cache.dim() != 4:
+        raise ValueError("q and cache must be 4-D")
     B, H, n_q, dk = q.shape
     dv = int(dk if head_dim_v is None else head_dim_v)
-    Hkv, page, max_pages = cache.shape[1], cache.shape[2] * 16, page_table.shape[1]
-    dev = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv)
+    Hkv = cache.shape[1]
+    dev, n_pages, page, max_pages = _kv4_check(torch, cache, page_table, seq_lens, B, Hkv, dk, dv)
     if mask is not None and (tuple(mask.shape) != (B, 1, n_q, max_pages * page) or mask.dtype != q.dtype):
         raise ValueError(f"mask: expected {(B, 1, n_q, max_pages * page)} {q.dtype}, got "
                          f"{tuple(mask.shape)} {mask.dtype}")
@@ -485,7 +487,7 @@ def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, s
         o = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=cache.device) if out is None else out
         rc = L.gdn_flash_attn_kv4(
             q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-            None if mask is None else mask.data_ptr(), o.data_ptr(), B, H, Hkv, n_q, dk, dv, cache.shape[0],
+            None if mask is None else mask.data_ptr(), o.data_ptr(), B, H, Hkv, n_q, dk, dv, n_pages,
             page, max_pages, scale, 1 if causal else 0, dt, odt,
             None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
