@@ -215,10 +215,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 __device__ __forceinline__ void after_the_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 #endif
 
-// How the attention's work is shared out: all tiles of all units (sequence, kv
+// How the attention's work is shared out: all steps of all units (sequence, kv
 // head, row block), one after another, cut into equal runs, one a warp.
-// Run w of W over T tiles (W <= T, so none is empty): T / W of them, one more in the
-// first T % W runs; and the run of tile x.
+// Run w of W over T steps (W <= T, so none is empty): T / W of them, one more in the
+// first T % W runs; and the run of step x.
 __host__ __device__ inline int run_begin(int T, int W, int w) {
     const int each = T / W, more = T - each * W;
     return each * w + (w < more ? w : more);

@@ -26,9 +26,9 @@
 //     P^T of row g and tokens 2t, 2t + 1.
 // Scores, maxima, sums and the output accumulate in fp32.
 //
-// Work is shared out in tiles, not in sequences: the tiles of all (sequence, kv
-// head, row block) units in a row are cut into equal runs, one a warp, so ragged
-// batches and single long sequences load the GPU evenly.  A warp that has a unit
+// Work is shared out in steps of 2 or 4 tiles, not in sequences: the steps of all
+// (sequence, kv head, row block) units in a row are cut into equal runs, one a warp, so
+// ragged batches and single long sequences load the GPU evenly.  A warp that has a unit
 // to itself writes its output; otherwise it leaves (max, sum, output) in the
 // workspace and a second kernel, launched as a programmatic dependent, joins the
 // parts in a fixed order (results do not depend on timing).  It also writes the
@@ -171,8 +171,9 @@ __device__ __forceinline__ void store2(void *out, int type, size_t i, float x, f
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// Work is shared out in steps of U tiles, counted from each unit's start: a step of fewer
-// tiles takes as long.
+// Steps of U tiles are counted from each unit's start and never cut, since a step of
+// fewer tiles takes as long (8 x 8 kv heads x 3000 x 128: 16.0 us, and 19.1 with runs of
+// equal tiles).
 __device__ __forceinline__ int steps_of(int tiles, int U) { return (tiles + U - 1) / U; }
 
 // Runs of a call of T steps: of at least 4 tiles, which a warp decodes in about the time
