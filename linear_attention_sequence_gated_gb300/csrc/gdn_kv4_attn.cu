@@ -188,12 +188,12 @@ __device__ __forceinline__ int tiles_at(const Attn &a, int b) {
     if (raw > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
     return tiles_of(min(max(raw, 0), capacity(a.c)));
 }
-// Whole-warp: the steps of all units of the sequences before `end`, and the sequence
-// that step x lies in with the steps before it.
-__device__ __forceinline__ int steps_before(const Attn &a, int U, int units, int end, int lane) {
+// Whole-warp: the steps of all units of the sequences from `b0` to before `end`, and the
+// sequence that step x lies in with the steps before it.
+__device__ __forceinline__ int steps_between(const Attn &a, int U, int units, int b0, int end, int lane) {
     int n = 0;
 #pragma unroll 4
-    for (int b = lane; b < end; b += 32) n += steps_of(tiles_at(a, b), U) * units;
+    for (int b = b0 + lane; b < end; b += 32) n += steps_of(tiles_at(a, b), U) * units;
     return __reduce_add_sync(0xffffffffu, n);
 }
 __device__ __forceinline__ int find_step(const Attn &a, int U, int units, int x, int lane, int *before) {
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         c.n = warp < parts ? run_begin(n, parts, warp + 1) : 0;
         c.left = steps_of(c.n - c.j, U);
     } else {
-        const int T = steps_before(a, U, units, a.n_seqs, lane), W = runs_of(a, T, U);
+        const int T = steps_between(a, U, units, 0, a.n_seqs, lane), W = runs_of(a, T, U);
         // neighbouring runs on different SMs: few tiles spread over the GPU
         w = warp * gridDim.x + blockIdx.x;
         if (w >= W) return;
@@ -762,20 +762,42 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const Attn a, int U, int 
     __shared__ float s_m[JW], s_l[JW], s_x[JW][DV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.c.Hkv * a.n_rb;
-    const int T = steps_before(a, U, units, a.n_seqs, lane), W = runs_of(a, T, U);
+    // the call's steps, and those before the block's first row's sequence: the block scans
+    // the lengths together
+    const int r0 = blockIdx.x * rpb, r = r0 + warp, b0 = r0 / a.R / a.c.Hkv;
+    int all = 0, pre = 0;
+    for (int b = threadIdx.x; b < a.n_seqs; b += JW * 32) {
+        const int n = steps_of(tiles_at(a, b), U) * units;
+        all += n;
+        if (b < b0) pre += n;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    pre = __reduce_add_sync(0xffffffffu, pre);
+    if (lane == 0) {
+        s_w0[warp] = all;
+        s_n[warp] = pre;
+    }
+    __syncthreads();
+    int T = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < JW; ++k) {
+        T += s_w0[k];
+        before += s_n[k];
+    }
+    __syncthreads();
+    const int W = runs_of(a, T, U);
     auto place = [&](int r, int &local) {              // where a row's output goes
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         local = row % kRows;
         return (((size_t)b * a.n_q + row % a.n_q) * a.H + hk * (a.H / a.c.Hkv) + row / a.n_q) * DV;
     };
-    const int r0 = blockIdx.x * rpb, r = r0 + warp;
     int w0 = 0, n = -1;                                // runs that share the row; -1: none of ours
     if (warp < rpb && r < n_rows) {
         const int unit = r / a.R, row = r - unit * a.R, b = unit / a.c.Hkv, hk = unit - b * a.c.Hkv;
         const int steps = steps_of(tiles_of(length(a.c, b)), U);
         n = 0;
         if (steps > 0) {
-            const int first = steps_before(a, U, units, b, lane) + (hk * a.n_rb + row / kRows) * steps;
+            const int first = before + steps_between(a, U, units, b0, b, lane) + (hk * a.n_rb + row / kRows) * steps;
             w0 = run_of(T, W, first);
             n = run_of(T, W, first + steps - 1) - w0 + 1;
         }
