@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[G::WARPS][ST];
     __shared__ unsigned good[G::WARPS][ST];            // tiles of the stage whose pages exist
+    __shared__ int steps[G::WARPS];
     __shared__ int gave_up;                            // (a hint only: other waits need not run out too)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) gave_up = 0;
@@ -568,7 +569,16 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
         c.n = warp < parts ? run_begin(n, parts, warp + 1) : 0;
         c.left = steps_of(c.n - c.j, U);
     } else {
-        const int T = steps_between(a, U, units, 0, a.n_seqs, lane), W = runs_of(a, T, U);
+        // the call's steps: the block scans the lengths together
+        int T = 0;
+        for (int b = threadIdx.x; b < a.n_seqs; b += G::WARPS * 32) T += steps_of(tiles_at(a, b), U) * units;
+        T = __reduce_add_sync(0xffffffffu, T);
+        if (lane == 0) steps[warp] = T;
+        __syncthreads();
+        T = 0;
+#pragma unroll
+        for (int k = 0; k < G::WARPS; ++k) T += steps[k];
+        const int W = runs_of(a, T, U);
         // neighbouring runs on different SMs: few tiles spread over the GPU
         w = warp * gridDim.x + blockIdx.x;
         if (w >= W) return;
