@@ -219,9 +219,9 @@ __device__ __forceinline__ bool part_of(const Run &r, int b, Part &p) {
     p.h = unit - j * r.c.Hkv;
     p.b = b;
     if (j * r.group >= (unsigned)r.n_tiles) return false;
-    const int raw = max(__ldg(r.c.lens + b), 0), cap = capacity(r.c);
+    const int raw = max(r.c.lens[b], 0), cap = capacity(r.c);
     if (raw > cap) *r.c.status = GDN_ERR_PAGE;
-    const int count = r.counts ? min(max(__ldg(r.counts + b), 0), r.T) : r.T;
+    const int count = r.counts ? min(max(r.counts[b], 0), r.T) : r.T;
     static_cast<Place &>(p) = place_of(raw, cap, count, j * r.group);
     return true;
 }

@@ -53,7 +53,7 @@ __device__ __forceinline__ int capacity(const View &c) { return c.max_pages * c.
 
 // Tokens of sequence b: what the table has room for at most, none if negative.
 __device__ __forceinline__ int length(const View &c, int b) {
-    return min(max(__ldg(c.lens + b), 0), capacity(c));
+    return min(max(c.lens[b], 0), capacity(c));
 }
 
 // Byte offset of tile `in_page` of (page, kv head h), or -1 for a page that the
@@ -68,7 +68,7 @@ __host__ __device__ inline long long tile_offset(int page, int n_pages, int Hkv,
 // word) where the table names a page that the cache does not have.
 __device__ __forceinline__ uint8_t *tile_ptr(const View &c, int b, int h, int tile) {
     const int slot = tile / c.tpp;
-    const int page = __ldg(c.table + (size_t)b * c.max_pages + slot);
+    const int page = c.table[(size_t)b * c.max_pages + slot];
     const long long at = tile_offset(page, c.n_pages, c.Hkv, h, c.tpp, tile - slot * c.tpp,
                                      tile_bytes(c.dk, c.dv));
     if (at < 0) {
@@ -192,7 +192,11 @@ __device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float 
 // The cache's kernels are launched as programmatic dependents, so that their blocks are
 // set up while the kernel before them in the stream ends.  Every thread waits for that
 // kernel's end before it reads or writes what a kernel before may write or read, so
-// when this kernel has ended, so have those before it.  Calls in a row, us: attention over
+// when this kernel has ended, so have those before it.  What they read from global
+// memory they read with ordinary loads: the non-coherent kind (__ldg, ld.global.nc) is
+// for data that nothing writes while the kernel runs, and these kernels are running when
+// the kernel before writes the lengths or the rows; such loads, and the cache-hint
+// intrinsics, are also free to move up across the wait.  Calls in a row, us: attention over
 // 64 x 32/8 x 4096 x 128: 68.4 -> 65.0, one token at 64: 8.2 -> 5.5; in captured steps,
 // 16 x 4 kv heads x 3000 x 128: 17.2 -> 16.6, a token's write and attention over 8 x 8 kv
 // heads x 500 x 128: 12.0 -> 11.4.

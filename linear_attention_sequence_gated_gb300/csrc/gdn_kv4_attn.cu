@@ -133,8 +133,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 }
 
 __device__ __forceinline__ float element(const void *p, int type, size_t i) {
-    if (type == GDN_DTYPE_F32) return __ldg(static_cast<const float *>(p) + i);
-    const unsigned short u = __ldg(static_cast<const unsigned short *>(p) + i);
+    if (type == GDN_DTYPE_F32) return static_cast<const float *>(p)[i];
+    const unsigned short u = static_cast<const unsigned short *>(p)[i];
     return type == GDN_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
 }
 
@@ -184,7 +184,7 @@ __device__ __forceinline__ int runs_of(const Attn &a, int T, int U) { return min
 // Tiles of a unit of sequence b.
 __device__ __forceinline__ int tiles_at(const Attn &a, int b) {
     if (b >= a.n_seqs) return 0;
-    const int raw = __ldg(a.c.lens + b);
+    const int raw = a.c.lens[b];
     if (raw > capacity(a.c)) *a.c.status = GDN_ERR_PAGE;
     return tiles_of(min(max(raw, 0), capacity(a.c)));
 }
@@ -237,7 +237,7 @@ struct Unit {
     __device__ __forceinline__ void begin(const Attn &a, int b, int hk, int rb, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int rep = a.H / a.c.Hkv;
-        const int raw = max(__ldg(a.c.lens + b), 0), len = min(raw, capacity(a.c));
+        const int raw = max(a.c.lens[b], 0), len = min(raw, capacity(a.c));
         all = a.mask ? 0 : (a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len);
         // all loads first: a lane's elements are whole 16-byte words
         constexpr int QE = QLO ? 4 : 8, QW = ST * 4 / QE;   // elements a word, words a part
@@ -250,7 +250,7 @@ struct Unit {
         for (int c = 0; c < CK; ++c)
 #pragma unroll
             for (int i = 0; i < QW; ++i)
-                raw_q[c][i] = row < a.R ? __ldg(at + c * (128 / QE) + i) : make_uint4(0, 0, 0, 0);
+                raw_q[c][i] = row < a.R ? at[c * (128 / QE) + i] : make_uint4(0, 0, 0, 0);
         float x[CK * ST * 4];
         float big = 0.f;
 #pragma unroll
@@ -359,7 +359,7 @@ struct Unit {
         uint32_t ph[U][2], pl[PM == kHiLo ? U : 1][2];
         float cf[2];
         if (!plain) {
-            const int raw = max(__ldg(a.c.lens + b), 0);
+            const int raw = max(a.c.lens[b], 0);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 // (a length past the table counts in full for the causal limit)
@@ -710,8 +710,8 @@ struct Join {
             const float *at = ws + (size_t)partial_slot(w0 + mine, mine == 0) * kPartial<DV>;
             float m = -INFINITY, l = 0.f;
             if (mine < n) {
-                m = __ldcg(at + kRows * DV + local);
-                l = __ldcg(at + kRows * (DV + 1) + local);
+                m = at[kRows * DV + local];
+                l = at[kRows * (DV + 1) + local];
             }
             float top = m;
 #pragma unroll
@@ -736,10 +736,10 @@ struct Join {
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         if constexpr (V == 2) {
-                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(row) + lane);
+                            const float2 y = reinterpret_cast<const float2 *>(row)[lane];
                             v[i][0] = y.x; v[i][1] = y.y;
                         } else {
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(row + 128 * c) + lane);
+                            const float4 y = reinterpret_cast<const float4 *>(row + 128 * c)[lane];
                             v[i][4 * c] = y.x; v[i][4 * c + 1] = y.y; v[i][4 * c + 2] = y.z; v[i][4 * c + 3] = y.w;
                         }
                     }
