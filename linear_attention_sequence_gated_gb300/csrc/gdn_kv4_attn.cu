@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(Geo<DK, DV>::WARPS * 32, 1) attn_kernel(const 
     __shared__ int gave_up;                            // (a hint only: other waits need not run out too)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) gave_up = 0;
-    if (lane < ST) ptx::mbar_init(&full[warp][lane], 1);
-    if (lane == 0) ptx::fence_mbar_init();
+    if (lane < ST) {
+        ptx::mbar_init(&full[warp][lane], 1);
+        ptx::fence_mbar_init();        // (orders this lane's own barrier before the copies that signal it)
+    }
     __syncthreads();
     after_the_kernel_before();
     const int units = a.c.Hkv * a.n_rb;
