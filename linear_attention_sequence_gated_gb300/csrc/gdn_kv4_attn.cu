@@ -386,14 +386,21 @@ struct Unit {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             // The weight of a score x is 2^((x - maximum) log2 e + 12).  Without a
-            // mask that is one FMA on the MMAs' result, with the maximum's product
-            // rounded the same way wherever it is used.  Scores that took a mask
-            // are differences in natural units first: masks of the type's lowest
-            // value would overflow.
+            // mask that is one FMA on the MMAs' result and the maximum's rounded
+            // product; the factor for what earlier steps summed takes the difference
+            // of two such products, each rounded by itself (not contracted into an
+            // FMA), so it is exactly 1 while the maximum stands: a residue of one
+            // rounding there would scale the older tokens again at every step of a run
+            // (512 steps, scores near 40: outputs off by 2e-3 of their RMS).  Scores
+            // that took a mask are differences in natural units first: masks of the
+            // type's lowest value would overflow.  A step in part without a mask takes
+            // differences too, which is one rounding of the product apart from the
+            // others (2^-24 of the score), as parts of different maxima are in the join.
             const float old = m[r], mn = fmaxf(old, plain ? mx * f[r] : mx);
             m[r] = mn;
             const float base = mn == -INFINITY ? 0.f : mn;
-            cf[r] = exp2_approx(a.mask ? (old - base) * kLog2e : old * kLog2e - __fmul_rn(base, kLog2e));
+            cf[r] = exp2_approx(a.mask ? (old - base) * kLog2e
+                                       : __fsub_rn(__fmul_rn(old, kLog2e), __fmul_rn(base, kLog2e)));
             float sum = 0.f;
             if (plain) {
                 const float k = f[r] * kLog2e, z = kPBits - __fmul_rn(base, kLog2e);
