@@ -411,9 +411,22 @@ __device__ __forceinline__ void read_values(const Run &r, const Part &p, const u
     if (tile) {
         const int group = W == 64 ? g >> 1 : p.chunk * 8 + g;
         sw = *reinterpret_cast<const uint32_t *>(tile + 9 * r.c.dk + 8 * r.c.dv + group * 16 + 4 * t4);
+        uint32_t gone = 0;             // nibbles of a word
 #pragma unroll
         for (int i = 0; i < 4; ++i)    // absent tokens: zeros, whatever their bytes say
-            if (!p.present(p.t0 + 4 * t4 + i)) sw &= ~(0xffu << (8 * i));
+            if (!p.present(p.t0 + 4 * t4 + i)) {
+                sw &= ~(0xffu << (8 * i));
+                gone |= 0x0f0fu << (4 * (i & 1) + 16 * (i >> 1));
+            }
+        if (gone) {                    // (their signs too: -0 otherwise)
+#pragma unroll
+            for (int q = 0; q < W / 64; ++q) {
+                w4[q].x &= ~gone;
+                w4[q].y &= ~gone;
+                w4[q].z &= ~gone;
+                w4[q].w &= ~gone;
+            }
+        }
     }
     // pairs of tokens to pairs of elements
     Raw<T, N> x[4];
