@@ -279,7 +279,8 @@ struct Unit {
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         // 2^14 / (the power of two at or below the row's largest element)
-        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 126);
+        // (an fp32 query's exponent reaches 127; below 2^-100 the factor stands still)
+        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
         const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
         const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(a.scale);
         const float sup = a.scale < 0.f ? -up : up;   // q takes the scale's sign
