@@ -279,8 +279,9 @@ struct Unit {
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         // 2^14 / (the power of two at or below the row's largest element)
-        // (an fp32 query's exponent reaches 127; below 2^-100 the factor stands still)
-        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+        // (from 2^-112 down the factor stays 2^126, with which the least fp32 number, 2^-149,
+        // is still two units of f16's subnormals)
+        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -112), 127);
         const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
         const float back = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(a.scale);
         const float sup = a.scale < 0.f ? -up : up;   // q takes the scale's sign

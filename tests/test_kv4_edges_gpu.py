@@ -29,3 +29,12 @@ def test_fp32_queries_up_to_the_largest_number(rep):
         c.q[..., at] = sign * top
         got, _ = c.check(scale=2.0 ** -128)
         assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("e", [-111, -113, -124, -126])
+def test_queries_down_to_the_least_normal_number(dtype, e):
+    """Rows whose largest elements are near 2^(e + 2), their small ones subnormal, with the scale that brings them back."""
+    c = Case([60, 300], 8, 2, 1, 64, dtype=dtype, seed=5)
+    c.q = (c.q.double() * 2.0 ** e).to(c.q.dtype)
+    c.check(scale=2.0 ** -e / 8)
