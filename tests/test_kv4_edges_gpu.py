@@ -38,3 +38,33 @@ def test_queries_down_to_the_least_normal_number(dtype, e):
     c = Case([60, 300], 8, 2, 1, 64, dtype=dtype, seed=5)
     c.q = (c.q.double() * 2.0 ** e).to(c.q.dtype)
     c.check(scale=2.0 ** -e / 8)
+
+
+@pytest.mark.parametrize("n_q,rep", [(2, 2), (5, 4)])
+def test_f16_masks_of_the_lowest_value(n_q, rep):
+    """A row hidden by -65504 throughout is the softmax of score - 65504 in fp32, whose unit there is 2^-8.  A score
+    comes to lie at most half a unit, 2^-9, and what it is off itself (TOL) beside itself, a weight over the sum of the
+    weights is off by twice that at most, and the output by as much of sum p |v|."""
+    c = Case([50, 333], 2 * rep, 2, n_q, 128, dtype="f16", seed=3)
+    low = torch.finfo(torch.float16).min
+    m = torch.zeros((2, 1, n_q, c.cap), device="cuda", dtype=torch.float16)
+    m[:, 0, 0] = low                                       # whole rows
+    m[1, 0, 1, ::2] = low                                  # every other token of a row: as good as hidden
+    got, ref, weight = np64(c.run(mask=m)), c.want(mask=m), c.want(mask=m, absolute=True)
+    off = np.expm1(2 * (2.0 ** -9 + TOL)) * weight
+    assert (np.abs(got - ref)[:, 0] <= off[:, 0]).all()
+    rest = np.abs(got - ref)[:, 1:]
+    assert rest.max() <= TOL * np.sqrt((ref[:, 1:] ** 2).mean())
+    # the bound tells the row from one without weights: the mean of the values is further off
+    plain = c.want(scale=0.0)[:, 0]
+    assert (np.abs(plain - ref[:, 0]) > 2 * off[:, 0]).mean() > 0.5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (256, 64)])
+def test_many_rows_around_steps(dtype, dk, dv):
+    """12 rows a kv head, two blocks; lengths around steps of 2 and 4 tiles and runs of several."""
+    lens = [31, 32, 33, 47, 63, 64, 65, 95, 96, 97, 127, 128, 129, 191, 193, 0, 1]
+    c = Case(lens, 8, 2, 3, dk, dv, page=16, dtype=dtype, seed=dk + dv)
+    c.check()
+    c.check(causal=True)
