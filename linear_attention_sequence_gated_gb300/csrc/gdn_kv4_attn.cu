@@ -47,7 +47,8 @@ namespace gdn {
 namespace kv4 {
 namespace {
 
-constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for
+constexpr int kGrid = 152;             // CTAs: one per SM of the GPU this is written for (and what the
+                                       // workspace's size goes by, on any device)
 
 // Rows of a unit: one MMA column tile.  More rows of a kv head are more units, which
 // decode the tiles again (from L2): blocks of 16 rows decode half as often, but took
@@ -60,9 +61,11 @@ constexpr int kRows = 8;
 // Shape of the kernel for widths DK and DV.  Each warp streams its run through a ring
 // of its own in shared memory: stages of U tiles, each tile one bulk copy.  12 warps
 // and steps of 4 tiles where 168 registers a thread hold the output tile and two
-// steps' tiles, else 8 and 2.  (64 x 32/8 x 4096 x 128: 64 us; 12 warps with steps of 2
-// tiles 72, with steps of 3 68; 8 warps with steps of 4 82, 16 with steps of 2 72, both
-// when it took 68.)
+// steps' tiles (kColumns and kHi: 143 to 160 registers; kHiLo spills 20 to 80 bytes a
+// thread there, with fp32 queries 24 to 140), else 8 and 2 (256 x 256 with fp32 queries
+// spills 16).  (64 x 32/8 x 4096 x 128: 63 us; 12 warps with steps of 2 tiles 72, with
+// steps of 3 68; 8 warps with steps of 4 82, 16 with steps of 2 72, both when it took
+// 68.)
 constexpr int warps_of(int dk, int dv) { return dk <= 128 && dv <= 128 ? 12 : 8; }
 constexpr int step_of(int dk, int dv) { return warps_of(dk, dv) == 12 ? 4 : 2; }
 template <int DK, int DV>
@@ -90,8 +93,11 @@ struct Attn {
     bool alone;                        // a block a unit, and no partial results
 };
 
-// How the weights enter the MMAs.  kHi: 11 bits, for 16-bit outputs.  kHiLo: the
-// remainder's 11 bits in a second MMA.  kColumns: of at most 4 rows, the remainder
+// How the weights enter the MMAs.  kHi: 11 bits, for 16-bit outputs of 16-bit queries,
+// whose own rounding is as large or larger: over 60 shapes the error against 64 bits is
+// 1.00 to 1.01 of what that rounding alone makes for bf16, 1.00 to 1.37 for f16.  (22
+// bits cost 0.3 to 0.5 us a call with kColumns.)  kHiLo: the remainder's 11 bits in a
+// second MMA.  kColumns: of at most 4 rows, the remainder
 // in the other 4 columns of the same MMA, where row r's queries stand again as
 // column r + 4; the two columns' outputs are added at the end.
 enum Weights { kHi = 0, kHiLo = 1, kColumns = 2 };
@@ -393,7 +399,7 @@ struct Unit {
             // of two such products, each rounded by itself (not contracted into an
             // FMA), so it is exactly 1 while the maximum stands: a residue of one
             // rounding there would scale the older tokens again at every step of a run
-            // (512 steps, scores near 40: outputs off by 2e-3 of their RMS).  Scores
+            // (512 steps, scores near 40: outputs off by 1.6e-3 of their RMS, 9e-5 without it).  Scores
             // that took a mask are differences in natural units first: masks of the
             // type's lowest value would overflow.  A step in part without a mask takes
             // differences too, which is one rounding of the product apart from the
@@ -907,7 +913,7 @@ cudaError_t launch(const Attn &a, cudaStream_t stream) {
 }
 
 // fp32 queries keep 22 bits and give fp32 outputs or 16-bit ones alike; 16-bit
-// queries are exact in one f16, and 16-bit outputs need 11 bits of the weights.
+// queries are exact in one f16, and their 16-bit outputs take 11 bits of the weights.
 template <int DK, int DV>
 cudaError_t launch_d(const Attn &a, cudaStream_t stream) {
     if (a.q_type == GDN_DTYPE_F32) return launch<DK, DV, true, kHiLo>(a, stream);
@@ -939,6 +945,7 @@ bool plan(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, long long tiles, 
     if (!host::mul_ok((unsigned long long)n_seqs, (unsigned long long)(Hkv * n_rb), &units) ||
         !host::mul_ok(units, (unsigned long long)tiles, &all) || all > (unsigned long long)INT_MAX)
         return false;
+    // The lengths are on the device, so the tables' room decides.
     // Up to a unit an SM, of few tiles: a CTA each, whose warps meet in shared memory.  It
     // takes as long as 4 tiles a warp do, times how many of those the unit has; the more
     // units, the later runs over the whole GPU and a join are faster.  n tokens a sequence
