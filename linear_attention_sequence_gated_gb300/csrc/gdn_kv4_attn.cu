@@ -61,8 +61,8 @@ constexpr int kRows = 8;
 // Shape of the kernel for widths DK and DV.  Each warp streams its run through a ring
 // of its own in shared memory: stages of U tiles, each tile one bulk copy.  12 warps
 // and steps of 4 tiles where 168 registers a thread hold the output tile and two
-// steps' tiles (kColumns and kHi: 143 to 160 registers; kHiLo spills 20 to 80 bytes a
-// thread there, with fp32 queries 24 to 140), else 8 and 2 (256 x 256 with fp32 queries
+// steps' tiles (kColumns and kHi: 143 to 162 registers; kHiLo spills 20 to 80 bytes a
+// thread there, with fp32 queries 24 to 136), else 8 and 2 (256 x 256 with fp32 queries
 // spills 16).  (64 x 32/8 x 4096 x 128: 63 us; 12 warps with steps of 2 tiles 72, with
 // steps of 3 68; 8 warps with steps of 4 82, 16 with steps of 2 72, both when it took
 // 68.)
@@ -104,6 +104,7 @@ enum Weights { kHi = 0, kHiLo = 1, kColumns = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPBits = 12.f;         // probabilities are scaled by 2^12
+constexpr float kFar = 65536.f;        // scores from which weights go by differences (fp32's unit: 2^-7)
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -399,18 +400,22 @@ struct Unit {
             // of two such products, each rounded by itself (not contracted into an
             // FMA), so it is exactly 1 while the maximum stands: a residue of one
             // rounding there would scale the older tokens again at every step of a run
-            // (512 steps, scores near 40: outputs off by 1.6e-3 of their RMS, 9e-5 without it).  Scores
-            // that took a mask are differences in natural units first: masks of the
-            // type's lowest value would overflow.  A step in part without a mask takes
-            // differences too, which is one rounding of the product apart from the
-            // others (2^-24 of the score), as parts of different maxima are in the join.
+            // (512 steps, scores near 40: outputs off by 1.6e-3 of their RMS, 9e-5
+            // without it).  Scores that took a mask are differences in natural units
+            // first: masks of the type's lowest value would overflow.  So are scores
+            // beside a maximum of kFar and more, where the product's rounding would move
+            // all weights together, at 1e7 out of f16's range.  A step in part without a
+            // mask takes differences too, which is one rounding of the product apart from
+            // the others (2^-24 of the score), as parts of different maxima are in the
+            // join.
             const float old = m[r], mn = fmaxf(old, plain ? mx * f[r] : mx);
             m[r] = mn;
             const float base = mn == -INFINITY ? 0.f : mn;
-            cf[r] = exp2_approx(a.mask ? (old - base) * kLog2e
-                                       : __fsub_rn(__fmul_rn(old, kLog2e), __fmul_rn(base, kLog2e)));
+            const bool far = !(fabsf(base) < kFar);
+            cf[r] = exp2_approx(a.mask || far ? (old - base) * kLog2e
+                                              : __fsub_rn(__fmul_rn(old, kLog2e), __fmul_rn(base, kLog2e)));
             float sum = 0.f;
-            if (plain) {
+            if (plain && !far) {
                 const float k = f[r] * kLog2e, z = kPBits - __fmul_rn(base, kLog2e);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -418,10 +423,17 @@ struct Unit {
                     s[u][r + 2] = exp2_approx(fmaf(s[u][r + 2], k, z));
                 }
             } else {
+                if (plain) {           // (the others took their factor above)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        s[u][r] = __fmul_rn(s[u][r], f[r]);
+                        s[u][r + 2] = __fmul_rn(s[u][r + 2], f[r]);
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    s[u][r] = exp2_approx(fmaf(s[u][r] - base, kLog2e, kPBits));
-                    s[u][r + 2] = exp2_approx(fmaf(s[u][r + 2] - base, kLog2e, kPBits));
+                    s[u][r] = exp2_approx(fmaf(__fsub_rn(s[u][r], base), kLog2e, kPBits));
+                    s[u][r + 2] = exp2_approx(fmaf(__fsub_rn(s[u][r + 2], base), kLog2e, kPBits));
                 }
             }
 #pragma unroll

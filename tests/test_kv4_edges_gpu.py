@@ -7,6 +7,7 @@ import torch
 
 import linear_attention_sequence_gated_gb300 as gdn
 import oracle
+from oracle import kv4
 from test_kv4_attn_gpu import Case, TOL, np64
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +69,24 @@ def test_many_rows_around_steps(dtype, dk, dv):
     c = Case(lens, 8, 2, 3, dk, dv, page=16, dtype=dtype, seed=dk + dv)
     c.check()
     c.check(causal=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [1e5, 1e7, 1e8, 1e12, -1e20, 1e30])
+def test_scores_up_to_the_largest_numbers(dtype, scale):
+    """Scores of `scale` times a few units, far apart against their fp32 units: each row is its best token's values.
+    Whole steps and a part of one, one CTA a unit and runs that are joined, one row and several a kv head."""
+    for lens, H, n_q in (([64, 200], 4, 1), ([3000, 64, 900], 16, 3)):
+        c = Case(lens, H, 2, n_q, 64, dtype=dtype, seed=6, page=64)
+        q, k, v = np64(c.q), kv4.kept(np64(c.k)), kv4.kept(np64(c.v))
+        got = np64(c.run(scale=scale))
+        assert np.isfinite(got).all()
+        for b, n in enumerate(lens):
+            s = np.einsum("hid,hjd->hij", q[b], np.repeat(k[b, :, :n], H // 2, axis=0)) * np.sign(scale)
+            order = np.sort(s, axis=-1)
+            # the best token's lead, in natural units of the score, against what fp32 sums of 64 products are off by
+            clear = (order[..., -1] - order[..., -2]) * abs(scale) > 30 + 2.0 ** -20 * 64 * abs(scale)
+            assert clear.mean() > 0.5
+            best = v[b, np.arange(H)[:, None] // (H // 2), s.argmax(-1)]           # (H, n_q, dv)
+            off = np.abs(got[b].transpose(1, 0, 2) - best).max(-1)
+            assert off[clear].max() <= TOL
