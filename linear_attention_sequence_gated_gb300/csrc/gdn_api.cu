@@ -51,13 +51,20 @@ cudaMemPool_t pool_for_current_device() {
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
+        // A stream capture forbids the creation of a pool, though it does not touch the
+        // captured stream: this thread is let off while it makes one, so that a call may
+        // be captured before any has run.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
         cudaMemPool_t pool = nullptr;
-        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return nullptr;
-        unsigned long long keep = kPoolKeepBytes;
-        if (cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
-            cudaMemPoolDestroy(pool);
-            return nullptr;
+        bool ok = cudaMemPoolCreate(&pool, &props) == cudaSuccess;
+        if (ok) {
+            unsigned long long keep = kPoolKeepBytes;
+            ok = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) == cudaSuccess;
+            if (!ok) cudaMemPoolDestroy(pool);
         }
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (!ok) return nullptr;
         g_pool[dev] = pool;
     }
     return g_pool[dev];
