@@ -365,9 +365,9 @@ int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, 
  * sequence's start, every token hidden by -inf) is zeros.  A mask of the type's
  * lowest finite value takes part in the softmax as the number it is.
  * Accumulation is fp32, one addition for 64 tokens (32 where a width is 256), so its
- * error grows with the length: 1e-5 to 9e-5 of the output's RMS after 512 of them.  The
- * cache's values enter exactly, q exactly (fp32 as 22 bits), the
- * softmax weights with 22 bits (11 where q and out are both 16-bit).
+ * error grows with the length: 1e-5 to 6e-5 of the output's RMS after 512 of them, up
+ * to 1.1e-4 with scores near 40.  The cache's values enter exactly, q exactly (fp32 as
+ * 22 bits), the softmax weights with 22 bits (11 where q and out are both 16-bit).
  * Results do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), the cache's widths and page
  * sizes, n_heads_kv dividing n_heads, page tables with room for fewer than 2^31
@@ -377,7 +377,7 @@ int gdn_kv4_read(const void *cache, const int *page_table, const int *seq_lens, 
  * Speed: the lengths are on the device, so the call is shared out by max_pages *
  *   page_size.  Few sequences whose tables have little room run as one kernel
  *   without a workspace, with more room as two (1 x 16/4 heads x 141 tokens x 256:
- *   8.6 us with room for 192 tokens, 13.8 with room for 32768).
+ *   8.5 us with room for 192 tokens, 13.4 with room for 32768).
  * workspace: caller's device buffer of gdn_flash_attn_kv4_workspace_bytes (0 where
  *   the call needs none, and for sizes that are not supported), 256-byte aligned,
  *   its contents ignored on entry and garbage on return, for one call at a time; or

@@ -63,7 +63,7 @@ constexpr int kRows = 8;
 // and steps of 4 tiles where 168 registers a thread hold the output tile and two
 // steps' tiles (kColumns and kHi: 143 to 162 registers; kHiLo spills 20 to 80 bytes a
 // thread there, with fp32 queries 24 to 136), else 8 and 2 (256 x 256 with fp32 queries
-// spills 16).  (64 x 32/8 x 4096 x 128: 63 us; 12 warps with steps of 2 tiles 72, with
+// spills 16).  (64 x 32/8 x 4096 x 128: 61 us; 12 warps with steps of 2 tiles 72, with
 // steps of 3 68; 8 warps with steps of 4 82, 16 with steps of 2 72, both when it took
 // 68.)
 constexpr int warps_of(int dk, int dv) { return dk <= 128 && dv <= 128 ? 12 : 8; }
@@ -401,7 +401,7 @@ struct Unit {
             // FMA), so it is exactly 1 while the maximum stands: a residue of one
             // rounding there would scale the older tokens again at every step of a run
             // (512 steps, scores near 40: outputs off by 1.6e-3 of their RMS, 9e-5
-            // without it).  Scores that took a mask are differences in natural units
+            // at most without it).  Scores that took a mask are differences in natural units
             // first: masks of the type's lowest value would overflow.  So are scores
             // beside a maximum of kFar and more, where the product's rounding would move
             // all weights together, at 1e7 out of f16's range.  A step in part without a
