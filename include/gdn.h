@@ -77,9 +77,9 @@ enum gdn_status {
     GDN_ERR_WORKSPACE = -7, /* caller workspace NULL, too small or misaligned */
     GDN_ERR_NOMEM = -8,     /* stream-ordered workspace allocation failed */
     GDN_ERR_DTYPE = -9,     /* dtype not supported on the requested path (chunked: bf16 only) */
-    GDN_ERR_SHAPE = -10,    /* shape outside the op's scope (attention: 20 or more queries; page size) */
+    GDN_ERR_SHAPE = -10,    /* shape outside the op's scope (attention: 20 or more queries; page size; strides) */
     GDN_ERR_SCRATCH = -11,  /* gdn_forward_noalloc: the call needs more than its fixed scratch */
-    GDN_ERR_PAGE = -12      /* 4-bit cache: a page or length outside the cache (device status only) */
+    GDN_ERR_PAGE = -12      /* a page or length outside the cache, or no page left (device status only) */
 };
 
 /* dtype of q, k, v (F16: decode attention only) */
@@ -226,8 +226,8 @@ int gdn_supports(int head_dim);
  * gdn_get_device_status -- synchronises `stream`, then returns and clears
  * the library's device status word on the current device: GDN_OK, or what
  * was recorded last since the last query: GDN_ERR_TIMEOUT if a kernel's
- * bounded wait gave up, GDN_ERR_PAGE if a 4-bit cache call met a page or a
- * length outside its cache.
+ * bounded wait gave up, GDN_ERR_PAGE if a call met a page or a length outside its
+ * cache, or a stack of pages that had run out.
  * Returns GDN_ERR_CUDA if the synchronisation itself failed.
  */
 int gdn_get_device_status(gdn_stream_t stream);
@@ -390,6 +390,137 @@ int gdn_flash_attn_kv4(const void *q, const void *cache, const int *page_table, 
                        size_t workspace_bytes, gdn_stream_t stream);
 size_t gdn_flash_attn_kv4_workspace_bytes(int n_seqs, int n_heads, int n_heads_kv, int n_q, int head_dim_k,
                                           int head_dim_v, int page_size, int max_pages);
+
+/*
+ * Pages handed out on the device: the page tables that the paged caches (4-bit and
+ * other) take, and the slots and positions of a step's new tokens, from the sequences'
+ * lengths.  None of these calls has a counterpart in the pages.
+ *
+ * free_pages: (n_pages) int32, a stack: entries 0 .. *free_count - 1 name the pages that nobody
+ * holds, the next one to be handed out last.  free_count: one int32 in device memory.  A
+ * sequence's table entries 0 .. ceil(len / page_size) - 1 are the pages that it holds.
+ *
+ * gdn_page_assign -- a step that adds tokens to the sequences.
+ * seq_lens: (n_seqs) int32, lengths that COUNT the new tokens; new_lens: (n_seqs) int32, clamped to
+ *   [0, n_new], or NULL: n_new of each.  Token i of sequence b has position seq_lens[b] - n + i,
+ *   n = new_lens[b]; tokens at negative positions (a padded batch's empty sequence) are not there.
+ * page_table: (n_seqs, max_pages) int32; pages that the new tokens are the first to need are taken off the stack,
+ *   sequence by sequence and in the order of positions, and written into it; no other entry is.
+ * slots, positions (may be NULL): int32, page * page_size + offset and the position of each new token; -1 and 0 where
+ *   there is none.  token_offsets NULL: (n_seqs, n_new), token i of sequence b at b * n_new + i.  Otherwise
+ *   token_offsets is (n_seqs + 1) int32, written: sums of new_lens from 0 on, and slots and positions are
+ *   (n_tokens), token i of sequence b at token_offsets[b] + i.
+ * GDN_ERR_PAGE in the device status word, with every buffer left in order: the stack runs out (the
+ *   pages that are left go to the first that need them, the other entries and slots are -1), a length above
+ *   max_pages * page_size (tokens behind have no slot), more packed tokens than n_tokens (the rest is not
+ *   written), a slot in a page outside [0, n_pages) (-1), a count outside [0, n_pages] (clamped).
+ *
+ * gdn_page_release -- tokens of the sequences that are given up: pages ceil(to / page_size) ..
+ *   ceil(from / page_size) - 1 of each table go back onto the stack, to_lens[b] (NULL: 0, the sequence has
+ *   ended) tokens stay of from_lens[b].  Pages go back in the opposite of the order in which gdn_page_assign
+ *   hands them out, so a step that is called off leaves the stack as it was.  Entries outside [0, n_pages)
+ *   are left out (GDN_ERR_PAGE), as is what the stack has no room for; page_table is not written.  A page that
+ *   other tables name too, or that is given back twice, is the caller's to keep track of.
+ *
+ * Any page_size from 1 on (the caches want multiples of 16), n_seqs <= 16384, else GDN_ERR_SHAPE.  Outputs must not
+ * overlap each other or an input.  Calls on one stack are to be ordered (one stream, or events).
+ */
+int gdn_page_assign(int *page_table, const int *seq_lens, const int *new_lens, const int *free_pages,
+                    int *free_count, int *slots, int *positions, int *token_offsets, int n_seqs, int n_new,
+                    int n_tokens, int page_size, int max_pages, int n_pages, gdn_stream_t stream);
+int gdn_page_release(const int *page_table, const int *from_lens, const int *to_lens, int *free_pages,
+                     int *free_count, int n_seqs, int page_size, int max_pages, int n_pages, gdn_stream_t stream);
+
+/*
+ * Rotary positions with one or several axes (time, height and width of a video's tokens), and rows
+ * written into the pages of a cache.  No counterpart in the pages.
+ *
+ * gdn_rotary turns pairs of elements of each row of q (n_tokens, n_heads, head_dim) and k (n_tokens, n_heads_kv,
+ * head_dim): for frequency j < rot_dim / 2 of axis a_j
+ *     angle = positions[a_j][token] * freqs[j]
+ *     (x, y) -> (x cos - y sin, y cos + x sin)
+ * where (x, y) are elements j and j + rot_dim / 2, or 2j and 2j + 1 with GDN_ROTARY_NEIGHBOURS.  Elements from
+ * rot_dim on are copied.  GDN_ROTARY_INVERSE turns by -angle: the inverse, and the gradient (of q and k
+ * from those of q_out and k_out).  Computed in fp32 and rounded once; angles are exact modulo a turn to 2^-31 of
+ * it for every 32-bit position (with frequencies of up to one radian a position; beyond that fp64's share of
+ * a turn limits them).
+ * positions: (n_axes, n_tokens) int32, negative ones too.
+ * plan: (rot_dim / 2) entries of 16 bytes in device memory, 16-byte aligned, as gdn_rotary_plan fills them in
+ *   host memory from freqs and axes (NULL: all 0).  An axis from n_axes on counts as n_axes - 1.
+ * strides: NULL for dense tensors, or 8 host values in elements: token and head strides of q, q_out, k and k_out.
+ *   Rows are contiguous, their addresses multiples of 16 bytes.  q_out may be q itself (same strides), and k_out
+ *   k; any other overlap of an output is GDN_ERR_ALIAS, except that tensors of one token stride may take turns
+ *   in a buffer (the heads of a joint projection).
+ * head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up to head_dim (0: copies), else GDN_ERR_HEADDIM.
+ * n_heads or n_heads_kv may be 0 (and the pointers NULL).  All rows of one dtype: GDN_DTYPE_F32, _BF16, _F16.
+ *
+ * gdn_paged_write copies token t's rows of k (n_tokens, n_heads_kv, head_dim_k) and v to the slot slots[t] (as
+ * gdn_page_assign gives them) of k_cache (n_pages, n_heads_kv, page_size, head_dim_k) and v_cache (...,
+ * head_dim_v).  Tokens of negative slots are not written; a slot from n_pages * page_size on is GDN_ERR_PAGE
+ * in the device status word, and not written.  Slots of one call must differ: the contents of one that occurs twice are
+ * undefined.  Nothing else in the cache changes, and it needs no initial contents.
+ * strides: NULL, or token and head strides of k and v.  cache_strides: NULL, or page, head and token strides of k_cache and
+ *   v_cache (a cache whose pages are token-major has them so); rows and addresses as above, no two rows of a
+ *   cache may overlap.
+ *
+ * gdn_rotary_write is both in one launch: q is turned into q_out, k on its way into the cache, v is copied.
+ * q_strides: NULL, or token and head strides of q and q_out; kv_strides and cache_strides as for gdn_paged_write.
+ */
+#define GDN_ROTARY_NEIGHBOURS 1
+#define GDN_ROTARY_INVERSE 2
+int gdn_rotary_plan(const double *freqs, const int *axes, int n, void *plan);
+int gdn_rotary(const void *q, void *q_out, const void *k, void *k_out, const long long *strides,
+               const int *positions, const void *plan, int n_tokens, int n_heads, int n_heads_kv, int head_dim,
+               int rot_dim, int n_axes, int flags, int dtype, gdn_stream_t stream);
+int gdn_paged_write(const void *k, const void *v, const long long *strides, void *k_cache, void *v_cache,
+                    const long long *cache_strides, const int *slots, int n_tokens, int n_heads_kv,
+                    int head_dim_k, int head_dim_v, int n_pages, int page_size, int dtype, gdn_stream_t stream);
+int gdn_rotary_write(const void *q, void *q_out, const void *k, const void *v, const long long *q_strides,
+                     const long long *kv_strides, void *k_cache, void *v_cache, const long long *cache_strides,
+                     const int *positions, const void *plan, const int *slots, int n_tokens, int n_heads,
+                     int n_heads_kv, int head_dim_k, int head_dim_v, int rot_dim, int n_axes, int n_pages,
+                     int page_size, int flags, int dtype, gdn_stream_t stream);
+
+/*
+ * gdn_flash_attn_paged -- gdn_flash_attn over the pages of a cache that gdn_paged_write fills, with each
+ * sequence's own length:
+ *
+ *   out[b, i, h, :] = sum_j softmax_j(scale * q[b,h,i,:] . k[b,hk,j,:]
+ *                                     + mask[b,0,i,j]) * v[b,hk,j,:]
+ *   over 0 <= j < seq_lens[b] (with causal: j <= seq_lens[b] - n_q + i, the
+ *   queries being the sequence's newest tokens); hk = h / (n_heads /
+ *   n_heads_kv); row j of sequence b lies in page page_table[b][j / page_size] at j % page_size.
+ *
+ * q:    (n_seqs, n_heads, n_q, head_dim_k) dtype; q_strides: NULL for dense, or its strides of sequence, head and query in
+ *       elements (rows contiguous, 16-byte aligned)
+ * k_cache, v_cache: (n_pages, n_heads_kv, page_size, head_dim_k / head_dim_v) dtype; cache_strides: NULL, or the page, head
+ *       and token strides of both, multiples of 16 bytes; in ascending order each must be a multiple of the
+ *       one before it and hold all of it, in any order of the three (else GDN_ERR_SHAPE)
+ * page_table, seq_lens: as for gdn_kv4_write; a negative length counts as 0.  An entry outside [0, n_pages) that a
+ *       length reaches, or a length above max_pages * page_size, is GDN_ERR_PAGE in the device status word: such tokens
+ *       count as absent
+ * mask: (n_seqs, 1, n_q, max_pages * page_size) dtype, additive (-inf hides a token), or NULL
+ * out:  (n_seqs, n_q, n_heads, head_dim_v) of out_dtype
+ * A row that sees no token is zeros.  Tokens that a row does not see (behind its sequence's end, after its own place, hidden
+ * by -inf) have no effect on it, whatever their rows hold, NaN and infinities among them.  A mask of the type's
+ * lowest finite value takes part in the softmax as the number it is.
+ * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 16 bits (bf16) or 22 (f16); fp32 q, k, v
+ * and weights with 22 bits (infinite elements of fp32 rows make NaN).  Results do not depend on timing.
+ * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), head_dim_k and head_dim_v each 64, 128 or 256 (else
+ *   GDN_ERR_HEADDIM; gdn_flash_attn_paged_supports), page_size a multiple of 16 (else GDN_ERR_SHAPE), n_heads_kv
+ *   dividing n_heads, tables with room for fewer than 2^31 tiles of 16 tokens over all sequences, kv heads
+ *   and blocks of rows.  out must not overlap an input.
+ * workspace: as for gdn_flash_attn_kv4, gdn_flash_attn_paged_workspace_bytes of it (0 where the call needs none).
+ */
+int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *k_cache, const void *v_cache,
+                         const long long *cache_strides, const int *page_table, const int *seq_lens,
+                         const void *mask, void *out, int n_seqs, int n_heads, int n_heads_kv, int n_q,
+                         int head_dim_k, int head_dim_v, int n_pages, int page_size, int max_pages, float scale,
+                         int causal, int dtype, int out_dtype, void *workspace, size_t workspace_bytes,
+                         gdn_stream_t stream);
+size_t gdn_flash_attn_paged_workspace_bytes(int n_seqs, int n_heads, int n_heads_kv, int n_q, int head_dim_k,
+                                            int head_dim_v, int page_size, int max_pages, int dtype);
+int gdn_flash_attn_paged_supports(int n_q, int head_dim_k, int head_dim_v);
 
 /*
  * gdn_selftest_wait_timeout -- exercises the library's failure path on the

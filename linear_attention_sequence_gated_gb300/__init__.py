@@ -24,6 +24,16 @@ values, and a paged 4-bit cache (``kv4_cache``, ``kv4_write``, ``kv4_read``,
     lens += 1
     kv4_write(k, v, cache, page_table, lens)
     out = flash_attn_kv4(q, cache, page_table, lens)
+
+and a paged cache of 16- or 32-bit rows (``paged_cache``, ``paged_write``,
+``flash_attn_paged``) with rotary positions (``rotary_plan``, ``rotary``,
+``rotary_write``).  Tables, slots and positions come from ``page_assign`` (the
+tables serve the 4-bit cache too), and ``page_release`` takes pages back:
+
+    lens += 1                                                      # once a step
+    slots, positions, _ = page_assign(page_table, lens, free_pages, free_count, page_size)
+    q = rotary_write(q, k, v, positions, plan, k_cache, v_cache, slots)     # each layer
+    out = flash_attn_paged(q.unsqueeze(2), k_cache, v_cache, page_table, lens)
 """
 from __future__ import annotations
 
@@ -46,7 +56,11 @@ EXPORTS = ["gdn_forward", "gdn_forward_bf16", "gdn_forward_ex", "gdn_workspace_b
            "gdn_select_path", "gdn_supports", "gdn_get_device_status", "gdn_status_string",
            "gdn_version", "gdn_flash_attn", "gdn_flash_attn_supports", "gdn_forward_noalloc",
            "gdn_selftest_wait_timeout", "gdn_kv4_supports", "gdn_kv4_cache_bytes", "gdn_kv4_write",
-           "gdn_kv4_read", "gdn_flash_attn_kv4", "gdn_flash_attn_kv4_workspace_bytes"]
+           "gdn_kv4_read", "gdn_flash_attn_kv4", "gdn_flash_attn_kv4_workspace_bytes",
+           "gdn_page_assign", "gdn_page_release", "gdn_rotary_plan", "gdn_rotary", "gdn_paged_write",
+           "gdn_rotary_write", "gdn_flash_attn_paged", "gdn_flash_attn_paged_workspace_bytes",
+           "gdn_flash_attn_paged_supports"]
+ROTARY_NEIGHBOURS, ROTARY_INVERSE = 1, 2
 
 _lib = None
 
@@ -104,6 +118,20 @@ def lib():
         L.gdn_flash_attn_kv4.restype = i
         L.gdn_flash_attn_kv4_workspace_bytes.argtypes = [i] * 8
         L.gdn_flash_attn_kv4_workspace_bytes.restype = sz
+        L.gdn_page_assign.argtypes = [vp] * 8 + [i] * 6 + [vp]
+        L.gdn_page_release.argtypes = [vp] * 5 + [i] * 4 + [vp]
+        L.gdn_rotary_plan.argtypes = [vp, vp, i, vp]
+        L.gdn_rotary.argtypes = [vp] * 7 + [i] * 8 + [vp]
+        L.gdn_paged_write.argtypes = [vp] * 7 + [i] * 7 + [vp]
+        L.gdn_rotary_write.argtypes = [vp] * 12 + [i] * 11 + [vp]
+        L.gdn_flash_attn_paged.argtypes = [vp] * 9 + [i] * 9 + [ctypes.c_float, i, i, i, vp, sz, vp]
+        for f in (L.gdn_page_assign, L.gdn_page_release, L.gdn_rotary_plan, L.gdn_rotary, L.gdn_paged_write,
+                  L.gdn_rotary_write, L.gdn_flash_attn_paged):
+            f.restype = i
+        L.gdn_flash_attn_paged_workspace_bytes.argtypes = [i] * 9
+        L.gdn_flash_attn_paged_workspace_bytes.restype = sz
+        L.gdn_flash_attn_paged_supports.argtypes = [i, i, i]
+        L.gdn_flash_attn_paged_supports.restype = i
         _lib = L
     return _lib
 
@@ -493,6 +521,345 @@ def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, s
             0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
         if rc != OK:
             raise GdnError(rc, "gdn_flash_attn_kv4")
+        return o
+
+    return _kv4_call(torch, dev, stream, call)
+
+
+# ------------------------------------------------------- pages, rotary positions, 16- and 32-bit cache
+
+
+def _int32(t, shape, dev, name):
+    if t.shape != shape or t.dtype != _torch.int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {shape} int32 on the other tensors' device, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _pages_check(page_table, lens, free_pages, free_count):
+    """Shapes, types and devices of tables and a stack of pages; their device, sequences, entries, pages."""
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table must be 2-D and free_pages 1-D")
+    dev = page_table.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    B, max_pages = page_table.shape
+    _int32(page_table, (B, max_pages), dev, "page_table")
+    _int32(free_pages, free_pages.shape, dev, "free_pages")
+    _int32(free_count, (1,), dev, "free_count")
+    _int32(lens, (B,), dev, "lengths")
+    return dev, B, max_pages, free_pages.shape[0]
+
+
+def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_new: int = 1, new_lens=None, *,
+                n_tokens=None, slots=None, positions=None, offsets=None, stream=None):
+    """Pages, slots and positions for a step's new tokens; returns (slots, positions, offsets).
+
+    page_table (n_seqs, max_pages), seq_lens (n_seqs), free_pages (n_pages),
+    free_count (1), new_lens (n_seqs) or None (n_new each): int32.  seq_lens count
+    the new tokens.  Pages that they are the first to need leave the stack
+    free_pages[:free_count] from its end and enter the table; free_count and the
+    table are updated in place.  Without ``n_tokens`` slots and positions are
+    (n_seqs, n_new), -1 and 0 where there is no token, and offsets is None; with it
+    they are packed, (n_tokens,), sequence b's from offsets[b] on, offsets
+    (n_seqs + 1).  A stack that runs out, and whatever else only the device can
+    see, shows as ERR_PAGE in device_status().  The rest of the contract is with
+    gdn_page_assign in include/gdn.h."""
+    L, torch = lib(), _kv4_torch()
+    dev, B, max_pages, n_pages = _pages_check(page_table, seq_lens, free_pages, free_count)
+    if new_lens is not None:
+        _int32(new_lens, (B,), dev, "new_lens")
+    packed = n_tokens is not None
+    shape = (n_tokens,) if packed else (B, n_new)
+    for name, t, want in (("slots", slots, shape), ("positions", positions, shape), ("offsets", offsets, (B + 1,))):
+        if t is not None:
+            _int32(t, want, dev, name)
+    if offsets is not None and not packed:
+        raise ValueError("offsets go with n_tokens")
+
+    def call(handle):
+        new = lambda t, s: torch.empty(s, dtype=torch.int32, device=page_table.device) if t is None else t  # noqa: E731
+        s, p, o = new(slots, shape), new(positions, shape), new(offsets, (B + 1,)) if packed else None
+        rc = L.gdn_page_assign(page_table.data_ptr(), seq_lens.data_ptr(),
+                               None if new_lens is None else new_lens.data_ptr(), free_pages.data_ptr(),
+                               free_count.data_ptr(), s.data_ptr(), p.data_ptr(), o.data_ptr() if packed else None, B,
+                               n_new, n_tokens if packed else 0, page_size, max_pages, n_pages, handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_page_assign")
+        return s, p, o
+
+    return _kv4_call(torch, dev, stream, call)
+
+
+def page_release(page_table, from_lens, free_pages, free_count, page_size: int, to_lens=None, *, stream=None):
+    """Give back the pages of sequences that shrink from ``from_lens`` to ``to_lens`` tokens (None: to none).
+
+    Arguments as for page_assign; free_pages and free_count are updated in place.
+    A step called off (to_lens: the lengths before it) leaves the stack as it was."""
+    L, torch = lib(), _kv4_torch()
+    dev, B, max_pages, n_pages = _pages_check(page_table, from_lens, free_pages, free_count)
+    if to_lens is not None:
+        _int32(to_lens, (B,), dev, "to_lens")
+    rc = _kv4_call(torch, dev, stream, lambda handle: L.gdn_page_release(
+        page_table.data_ptr(), from_lens.data_ptr(), None if to_lens is None else to_lens.data_ptr(),
+        free_pages.data_ptr(), free_count.data_ptr(), B, page_size, max_pages, n_pages, handle))
+    if rc != OK:
+        raise GdnError(rc, "gdn_page_release")
+
+
+class RotaryPlan:
+    """Frequencies of rotary positions on a device, made by rotary_plan."""
+
+    def __init__(self, data, rot_dim, n_axes, neighbours):
+        self.data, self.rot_dim, self.n_axes, self.neighbours = data, rot_dim, n_axes, neighbours
+
+
+def rotary_plan(rot_dim: int, base: float = 10000.0, *, freqs=None, sections=None, dealt: bool = False,
+                neighbours: bool = False, device="cuda"):
+    """A plan for ``rotary`` and ``rotary_write``: pair j of a row's first ``rot_dim`` elements turns by its
+    axis's position times base ** (-2 j / rot_dim), or times freqs[j] (radians a position) where given.
+
+    sections: how many frequencies belong to each axis (their sum is rot_dim / 2;
+    default one axis), one axis after another, or with ``dealt`` dealt out in turn
+    (0, 1, 2, 0, 1, 2, ...) while an axis has any left.  Pairs are elements j and j + rot_dim / 2, or with
+    ``neighbours`` 2 j and 2 j + 1."""
+    L, torch = lib(), _kv4_torch()
+    n = rot_dim // 2
+    if rot_dim < 0 or rot_dim % 16 != 0:
+        raise GdnError(ERR_HEADDIM, "rotary_plan")
+    f = [float(base) ** (-2.0 * j / rot_dim) for j in range(n)] if freqs is None else [float(x) for x in freqs]
+    left = [n] if sections is None else [int(x) for x in sections]
+    if len(f) != n or not left or min(left) < 0 or sum(left) != n:
+        raise ValueError(f"expected {n} frequencies, and sections of as many in all")
+    n_axes, axes = len(left), []
+    if dealt:
+        while len(axes) < n:
+            for a in range(n_axes):
+                if left[a] > 0:
+                    axes.append(a)
+                    left[a] -= 1
+    else:
+        axes = [a for a in range(n_axes) for _ in range(left[a])]
+    host = torch.zeros((n, 2), dtype=torch.int64)
+    rc = L.gdn_rotary_plan((ctypes.c_double * n)(*f), (ctypes.c_int * n)(*axes), n, host.data_ptr())
+    if rc != OK:
+        raise GdnError(rc, "gdn_rotary_plan")
+    return RotaryPlan(host.to(device), rot_dim, n_axes, bool(neighbours))
+
+
+def _rows_check(x, dt, dev, name, T=None, H=None, d=None):
+    """(n_tokens, heads, width) of one dtype and device with contiguous rows."""
+    s = x.shape
+    if len(s) != 3 or x.dtype != dt or (T is not None and s[0] != T) or (H is not None and s[1] != H) \
+            or (d is not None and s[2] != d):
+        want = tuple("any" if v is None else v for v in (T, H, d))
+        raise ValueError(f"{name}: expected (n_tokens, heads, head_dim) = {want} {dt}, got {tuple(s)} {x.dtype}")
+    if x.get_device() != dev:
+        raise ValueError("all tensors must be on one CUDA device")
+    if x.stride(2) != 1 and x.numel():
+        raise ValueError(f"rows of {name} must be contiguous")
+
+
+def _positions_check(positions, plan, T, dev):
+    shape = (T,) if positions.dim() == 1 and plan.n_axes == 1 else (plan.n_axes, T)
+    _int32(positions, shape, dev, "positions")
+    if plan.data.get_device() != dev:
+        raise ValueError("plan must be on the tensors' device")
+
+
+def _strides(*xs):
+    """Host array of the strides of every dimension but the last."""
+    v = [s for x in xs for s in x.stride()[:-1]]
+    return (ctypes.c_longlong * len(v))(*v)
+
+
+def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Turn pairs of elements of q (n_tokens, n_heads, head_dim) and k (n_tokens, n_heads_kv, head_dim, or
+    None) by their tokens' positions; returns (q_out, k_out).
+
+    positions: (n_tokens,) int32, or (n_axes, n_tokens) for a plan of several
+    axes.  fp32, bf16 or fp16; any strides with contiguous, 16-byte aligned rows.
+    q_out and k_out may be q and k themselves (default: new dense tensors).
+    ``inverse`` turns back, which is also the gradient: rotary(dq_out, dk_out,
+    positions, plan, inverse=True) is (dq, dk)."""
+    L, torch = lib(), _kv4_torch()
+    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
+    _rows_check(q, q.dtype, dev, "q")
+    T, H, d = q.shape
+    Hk = 0
+    if k is not None:
+        _rows_check(k, q.dtype, dev, "k", T, None, d)
+        Hk = k.shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out goes with k")
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    _positions_check(positions, plan, T, dev)
+    for name, t, h in (("q_out", q_out, H), ("k_out", k_out, Hk)):
+        if t is not None:
+            _rows_check(t, q.dtype, dev, name, T, h, d)
+
+    def call(handle):
+        qo = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        ko = None if k is None else torch.empty((T, Hk, d), dtype=q.dtype, device=q.device) if k_out is None else k_out
+        st = _strides(q, qo) if k is None else _strides(q, qo, k, ko)
+        if k is None:
+            st = (ctypes.c_longlong * 8)(*st, 0, 0, 0, 0)
+        rc = L.gdn_rotary(q.data_ptr(), qo.data_ptr(), None if k is None else k.data_ptr(),
+                          None if k is None else ko.data_ptr(), st, positions.data_ptr(), plan.data.data_ptr(), T, H,
+                          Hk, d, plan.rot_dim, plan.n_axes,
+                          (ROTARY_NEIGHBOURS if plan.neighbours else 0) | (ROTARY_INVERSE if inverse else 0), dt, handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_rotary")
+        return qo, ko
+
+    return _kv4_call(torch, dev, stream, call)
+
+
+def paged_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, head_dim_v=None, *, dtype=None,
+                device="cuda"):
+    """An empty cache of 16- or 32-bit rows: (k_cache, v_cache) of shapes (n_pages, n_heads_kv, page_size, dk) and
+    (..., dv), bf16 where no dtype is given.  The calls below take any strides that nest (pages may be
+    token-major: a transposed view of (n_pages, page_size, n_heads_kv, dk))."""
+    torch = _kv4_torch()
+    dtype = torch.bfloat16 if dtype is None else dtype
+    _kv4_dtype(dtype, "dtype")
+    dv = head_dim_k if head_dim_v is None else head_dim_v
+    return tuple(torch.empty((n_pages, n_heads_kv, page_size, d), dtype=dtype, device=device) for d in (head_dim_k, dv))
+
+
+def _paged_check(k_cache, v_cache, dt, dev):
+    kn, vn = k_cache.shape, v_cache.shape
+    if len(kn) != 4 or vn[:3] != kn[:3] or len(vn) != 4 or k_cache.dtype != dt or v_cache.dtype != dt:
+        raise ValueError(f"k_cache, v_cache: expected (n_pages, n_heads_kv, page_size, dk / dv) {dt}, got {tuple(kn)} "
+                         f"{k_cache.dtype}, {tuple(vn)} {v_cache.dtype}")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or dev < 0:
+        raise ValueError("all tensors must be on one CUDA device")
+    if (k_cache.stride(3) != 1 or v_cache.stride(3) != 1) and k_cache.numel():
+        raise ValueError("rows of a cache must be contiguous")
+    return kn[0], kn[1], kn[2], kn[3], vn[3]
+
+
+def paged_write(k, v, k_cache, v_cache, slots, *, stream=None):
+    """Copy rows k, v (n_tokens, n_heads_kv, dk / dv) to their slots; returns (k_cache, v_cache).
+
+    slots: (n_tokens,) int32 as page_assign gives them (a padded batch's flattened),
+    negative: not written; they must differ."""
+    L, torch = lib(), _kv4_torch()
+    dt, dev = _kv4_dtype(k.dtype, "k/v"), k.get_device()
+    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, k.dtype, dev)
+    _rows_check(k, k.dtype, dev, "k", None, Hkv, dk)
+    T = k.shape[0]
+    _rows_check(v, k.dtype, dev, "v", T, Hkv, dv)
+    _int32(slots, (T,), dev, "slots")
+    st = None if k.is_contiguous() and v.is_contiguous() else _strides(k, v)
+    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
+    rc = _kv4_call(torch, dev, stream, lambda handle: L.gdn_paged_write(
+        k.data_ptr(), v.data_ptr(), st, k_cache.data_ptr(), v_cache.data_ptr(), cs, slots.data_ptr(), T, Hkv, dk, dv,
+        n_pages, page, dt, handle))
+    if rc != OK:
+        raise GdnError(rc, "gdn_paged_write")
+    return k_cache, v_cache
+
+
+def rotary_write(q, k, v, positions, plan, k_cache, v_cache, slots, *, q_out=None, stream=None):
+    """rotary of q and k and paged_write of the turned k and of v, in one launch; returns q_out (default: a new dense
+    tensor; may be q itself).  Arguments as for rotary and paged_write."""
+    L, torch = lib(), _kv4_torch()
+    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
+    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, q.dtype, dev)
+    _rows_check(q, q.dtype, dev, "q", None, None, dk)
+    T, H, _ = q.shape
+    _rows_check(k, q.dtype, dev, "k", T, Hkv, dk)
+    _rows_check(v, q.dtype, dev, "v", T, Hkv, dv)
+    _positions_check(positions, plan, T, dev)
+    _int32(slots, (T,), dev, "slots")
+    if q_out is not None:
+        _rows_check(q_out, q.dtype, dev, "q_out", T, H, dk)
+    st = None if k.is_contiguous() and v.is_contiguous() else _strides(k, v)
+    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
+
+    def call(handle):
+        qo = torch.empty((T, H, dk), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        qs = None if q.is_contiguous() and qo.is_contiguous() else _strides(q, qo)
+        rc = L.gdn_rotary_write(
+            q.data_ptr(), qo.data_ptr(), k.data_ptr(), v.data_ptr(), qs, st, k_cache.data_ptr(), v_cache.data_ptr(), cs,
+            positions.data_ptr(), plan.data.data_ptr(), slots.data_ptr(), T, H, Hkv, dk, dv, plan.rot_dim, plan.n_axes,
+            n_pages, page, ROTARY_NEIGHBOURS if plan.neighbours else 0, dt, handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_rotary_write")
+        return qo
+
+    return _kv4_call(torch, dev, stream, call)
+
+
+def flash_attn_paged_supports(n_q: int, head_dim_k: int, head_dim_v: int) -> bool:
+    """Whether ``flash_attn_paged`` serves this shape (fewer than 20 queries; widths each 64, 128 or 256)."""
+    return bool(lib().gdn_flash_attn_paged_supports(int(n_q), int(head_dim_k), int(head_dim_v)))
+
+
+def flash_attn_paged_workspace_bytes(n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, page_size, max_pages,
+                                     dtype=None) -> int:
+    """Bytes that ``flash_attn_paged`` needs as its ``workspace`` (0: none) for rows of ``dtype`` (default bf16)."""
+    torch = _kv4_torch()
+    return int(lib().gdn_flash_attn_paged_workspace_bytes(
+        n_seqs, n_heads, n_heads_kv, n_q, head_dim_k, head_dim_v, page_size, max_pages,
+        _kv4_dtype(torch.bfloat16 if dtype is None else dtype, "dtype")))
+
+
+def flash_attn_paged(q, k_cache, v_cache, page_table, seq_lens, mask=None, scale=None, *, causal: bool = False,
+                     out=None, out_dtype=None, workspace=None, stream=None):
+    """Decode attention over a paged cache: out[b, i, h] = softmax_j(scale q[b,h,i] . k[b,hk,j] + mask[b,0,i,j])
+    v[b,hk,j] over the seq_lens[b] tokens of each sequence (with ``causal``, j <= seq_lens[b] - n_q + i), hk = h //
+    (n_heads / n_heads_kv).
+
+    q: (n_seqs, n_heads, n_q, dk), any strides with contiguous, 16-byte aligned rows; k_cache, v_cache: (n_pages,
+    n_heads_kv, page_size, dk / dv) of q's dtype (fp32, bf16 or fp16); page_table (n_seqs, max_pages) and seq_lens
+    (n_seqs) int32; mask: (n_seqs, 1, n_q, max_pages * page_size) of q's dtype, additive, or None; scale defaults
+    to 1/sqrt(dk).  Returns out (n_seqs, n_q, n_heads, dv) of ``out_dtype`` (fp32 by default, or a given out's
+    dtype).  Rows that see no token are zeros; tokens that a row does not see have no effect on it.
+    ``workspace``: an optional uint8 CUDA tensor of flash_attn_paged_workspace_bytes(...) bytes for one call at a
+    time; without it the library allocates in stream order."""
+    L, torch = lib(), _kv4_torch()
+    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
+    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, q.dtype, dev)
+    if q.dim() != 4 or q.shape[3] != dk:
+        raise ValueError(f"q: expected (n_seqs, n_heads, n_q, {dk}), got {tuple(q.shape)}")
+    B, H, n_q, _ = q.shape
+    if q.stride(3) != 1 and q.numel():
+        raise ValueError("rows of q must be contiguous")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D")
+    max_pages = page_table.shape[1]
+    _int32(page_table, (B, max_pages), dev, "page_table")
+    _int32(seq_lens, (B,), dev, "lengths")
+    if mask is not None and (tuple(mask.shape) != (B, 1, n_q, max_pages * page) or mask.dtype != q.dtype):
+        raise ValueError(f"mask: expected {(B, 1, n_q, max_pages * page)} {q.dtype}, got {tuple(mask.shape)} {mask.dtype}")
+    for t in (mask, workspace):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("mask and workspace must be contiguous and on the tensors' device")
+    if out is not None:
+        if out_dtype is None:
+            out_dtype = out.dtype
+        if tuple(out.shape) != (B, n_q, H, dv) or out.dtype != out_dtype or not out.is_contiguous() \
+                or out.get_device() != dev:
+            raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype} on the tensors' device")
+    elif out_dtype is None:
+        out_dtype = torch.float32
+    odt = _kv4_dtype(out_dtype, "out_dtype")
+    if scale is None:
+        scale = dk ** -0.5
+    qs = None if q.is_contiguous() else _strides(q)
+    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
+
+    def call(handle):
+        o = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=q.device) if out is None else out
+        rc = L.gdn_flash_attn_paged(
+            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), cs, page_table.data_ptr(), seq_lens.data_ptr(),
+            None if mask is None else mask.data_ptr(), o.data_ptr(), B, H, Hkv, n_q, dk, dv, n_pages, page, max_pages,
+            scale, 1 if causal else 0, dt, odt, None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
+        if rc != OK:
+            raise GdnError(rc, "gdn_flash_attn_paged")
         return o
 
     return _kv4_call(torch, dev, stream, call)

@@ -15,9 +15,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_recurrent.cu", "gdn_chunked.cu", "gdn_attn.cu",
-           "gdn_kv4.cu", "gdn_kv4_attn.cu"]
+           "gdn_kv4.cu", "gdn_kv4_attn.cu", "gdn_pages.cu", "gdn_paged.cu", "gdn_paged_attn.cu"] + \
+          [f"gdn_paged_attn_{t}_{d}.cu" for t in ("bf16", "f16", "f32") for d in (64, 128, 256)]
 HEADERS = [os.path.join(CSRC, "gdn_internal.h"), os.path.join(CSRC, "gdn_ptx.cuh"),
-           os.path.join(CSRC, "gdn_kv4.cuh"),
+           os.path.join(CSRC, "gdn_kv4.cuh"), os.path.join(CSRC, "gdn_paged_attn.cuh"),
            os.path.join(os.path.dirname(PKG), "include", "gdn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
