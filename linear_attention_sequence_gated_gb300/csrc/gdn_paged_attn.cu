@@ -105,7 +105,7 @@ bool make_map(CUtensorMap *map, const void *p, const Layout &x, int d, int dtype
 
 // How a call is shared out.
 struct Plan {
-    int n_rb, rows;                    // blocks of rows of a kv head, rows of one
+    Share share;
     int cluster, grid;
     size_t bytes;                      // of the workspace
 };
@@ -113,22 +113,22 @@ struct Plan {
 // CTAs a unit, or 0 for equal runs, by the room that the tables have (the lengths are on the device): what the
 // slowest CTA streams, in bytes, and for runs the second kernel's time as 128 KB more.
 bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int max_pages, int elt, Plan *p) {
-    const int R = H / Hkv * n_q;
-    p->rows = kBlock * blocks_of(dk > 128 || dv > 128, elt == 4, R);
-    p->n_rb = (R + p->rows - 1) / p->rows;
-    const long long units = (long long)n_seqs * Hkv * p->n_rb, tiles = ((long long)max_pages * page + kTile - 1) / kTile;
-    if (units > INT_MAX || tiles > INT_MAX || (tiles > 0 && units > INT_MAX / tiles)) return false;
-    const int warps = warps_of(dk, dv, elt);
+    p->share = share_of(dk, dv, elt, H / Hkv * n_q);
+    const long long units = (long long)n_seqs * Hkv * p->share.units, groups = p->share.groups;
+    const long long tiles = ((long long)max_pages * page + kTile - 1) / kTile;
+    const long long steps = tiles ? tiles + kUnitCost : 0;
+    if (units > INT_MAX || steps > INT_MAX || (steps > 0 && units > INT_MAX / steps)) return false;
     const long long stage = (long long)kTile * (dk + dv) * elt;
     long long cl = 1;
-    while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * warps) cl *= 2;
+    while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * groups) cl *= 2;
     const long long waves = (units * cl + kGrid - 1) / kGrid;
     const long long by_cluster = waves * ((tiles + cl - 1) / cl) * stage;
     const long long by_runs = (units * tiles + kGrid - 1) / kGrid * stage + (128 << 10);
     p->cluster = by_cluster <= by_runs ? (int)cl : 0;
-    const long long runs = (units * tiles + warps - 1) / warps;
+    const long long runs = (units * steps + groups - 1) / groups;
     p->grid = p->cluster ? (int)(units * cl) : (int)(runs < kGrid ? runs : kGrid);
-    p->bytes = p->cluster || p->grid < 2 ? 0 : (size_t)2 * p->grid * p->rows * (dv + 2) * sizeof(float);
+    p->bytes = p->cluster || p->grid < 2 ? 0
+                                         : (size_t)2 * p->grid * p->share.blocks * kBlock * (dv + 2) * sizeof(float);
     return units * cl <= INT_MAX;
 }
 
@@ -251,7 +251,9 @@ int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *
     a.Hkv = n_heads_kv;
     a.n_q = n_q;
     a.R = n_heads / n_heads_kv * n_q;
-    a.n_rb = plan.n_rb;
+    a.n_rb = plan.share.units;
+    a.blocks = plan.share.blocks;
+    a.groups = plan.share.groups;
     a.n_pages = n_pages;
     a.tpp = page_size / kTile;
     a.max_pages = max_pages;

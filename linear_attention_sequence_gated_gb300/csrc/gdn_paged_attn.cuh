@@ -45,6 +45,7 @@ constexpr int kBlock = 8;              // rows of an MMA column tile
 constexpr int kGrid = 152;             // runs at most: one CTA per SM of the GPU this is written for (the
                                        // workspace's size goes by it on any device)
 constexpr int kMaxCluster = 8;         // the largest portable size
+constexpr int kUnitCost = 4;           // tiles that beginning and ending a unit counts for when runs are cut
 
 struct Attn {
     const void *q, *mask;
@@ -53,7 +54,8 @@ struct Attn {
     const int *table, *lens;
     int *status;
     long long q_seq, q_head, q_query;  // in elements
-    int n_seqs, H, Hkv, n_q, R, n_rb;  // R rows a kv head in n_rb blocks
+    int n_seqs, H, Hkv, n_q, R, n_rb;  // R rows a kv head in n_rb units,
+    int blocks, groups;                // each of `blocks` blocks of 8, one a warp of each of a CTA's groups
     int n_pages, tpp, max_pages;       // tpp: tiles of a page
     float scale;
     int out_type, cluster;             // CTAs a unit, or 0: equal runs
@@ -61,14 +63,51 @@ struct Attn {
     int k_order, v_order;              // of the tensor maps' outer coordinates: two bits each, 0 token, 1 head, 2 page
 };
 
-// Blocks of 8 rows that a unit takes: the cache is read once for all of them.  (Four of them fill the
-// registers where a width is 256.)
-constexpr int blocks_of(bool wide, bool fp32, int R) {
-    return fp32 || R <= kBlock ? 1 : R <= 2 * kBlock || wide ? 2 : 4;
+// Shared memory of the kernel for widths dk and dv, rows of elt bytes and `warps` warps, each with a block of 8 rows at
+// a time, `most` different ones at most.
+struct Room {
+    int columns;                       // the warps' outputs are joined so many columns at a time,
+    int merge;                         // in rows padded against bank conflicts
+    int q_row, q;                      // fp32 queries as hi and lo, in padded rows (16-bit ones are in registers)
+    int weights, sums;                 // fp32 weights on their way to B operands; maxima and sums
+    int tiles;                         // of all rings
+};
+constexpr int kSmemMax = 227 * 1024;
+constexpr Room room_of(int dk, int dv, int elt, int warps, int most) {
+    const int limit = (elt == 2 ? 32 : 16) * 1024, row = warps * kBlock * 4;
+    Room r{};
+    r.columns = row * (dv + 4) <= limit ? dv : dv > 128 && row * 132 <= limit ? 128 : 64;
+    r.merge = row * (r.columns + 4);
+    r.q_row = dk * 8 + 64;
+    r.q = elt == 2 ? 0 : most * kBlock * r.q_row;
+    r.weights = elt == 2 ? 0 : warps * kBlock * 20 * 4;
+    r.sums = 2 * (warps + most) * kBlock * 4;
+    // (1 KB for the ring's alignment, 1 KB for barriers and the like)
+    const int tiles = (kSmemMax - 2048 - r.merge - r.q - r.weights - r.sums) / (kTile * (dk + dv) * elt);
+    r.tiles = tiles < 48 ? tiles : 48;
+    return r;
 }
-// Warps of a CTA: 8 with tiles of 8 KB, fewer with larger ones, so that the ring holds 2 or 3 a warp.
-constexpr int warps_of(int dk, int dv, int elt) {
-    return kTile * (dk + dv) * elt <= 8192 ? 8 : kTile * (dk + dv) * elt <= 16384 ? 4 : 2;
+
+// How the rows of a kv head and the warps of a CTA are shared out.  A group of warps streams tiles through a ring of
+// its own, each warp for another block of 8 rows, so that the cache is read once for all of them.  Up to 8
+// rows: 8 groups of one warp with tiles of 8 KB, fewer with larger ones, so that the rings hold 2 or 3 each.
+// More rows: 12 warps where 168 registers hold a block's output, else 8, as so many groups as there are blocks and
+// tiles in shared memory for.
+struct Share {
+    int warps, most;                   // warps, and blocks of rows of a unit at most
+    int blocks, groups, units;         // blocks of a unit, groups of so many warps, units of a kv head
+};
+constexpr Share share_of(int dk, int dv, int elt, int R) {
+    const int tile = kTile * (dk + dv) * elt;
+    const bool wide = elt == 4 || dk > 128 || dv > 128;
+    if (R <= kBlock) {
+        const int warps = tile <= 8192 ? 8 : tile <= 16384 ? 4 : 2;
+        return {warps, 1, 1, warps, 1};
+    }
+    const int warps = wide ? 8 : 12, most = wide ? 4 : 6, tiles = room_of(dk, dv, elt, warps, most).tiles;
+    const int all = (R + kBlock - 1) / kBlock, units = (all + most - 1) / most, blocks = (all + units - 1) / units;
+    const int groups = warps / blocks, fed = tiles / 2;
+    return {warps, most, blocks, groups < fed ? groups : fed, units};
 }
 
 // The kernel for rows of type T and keys of width DK (one translation unit each).
@@ -83,33 +122,20 @@ using kv4::run_begin;
 using kv4::run_of;
 using kv4::partial_slot;
 
-constexpr int kSmemMax = 227 * 1024;
-
-// Shape of the kernel for widths DK and DV, type T and NB blocks of 8 rows.
-template <typename T, int DK, int DV, int NB>
+// Shape of the kernel for widths DK and DV, type T and WARPS warps, which take U tiles at a time.
+template <typename T, int DK, int DV, int WARPS, int MOST, int U_>
 struct Geo {
-    static constexpr int E = (int)sizeof(T);
+    static constexpr int E = (int)sizeof(T), U = U_;
     static constexpr bool MMA16 = E == 2;
     static constexpr int BOX = 128 / E;                // elements of a box's row
     static constexpr int KB = kTile * DK * E, VB = kTile * DV * E, STAGE = KB + VB;
-    static constexpr int WARPS = warps_of(DK, DV, E);
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int ROWS = NB * kBlock;
-    // the warps' outputs of 8 rows, to be joined
-    static constexpr int MERGE = WARPS * kBlock * DV * 4;
-    // queries in shared memory, rows padded against bank conflicts: 16-bit ones (one block stays in registers), fp32
-    // ones as hi and lo
-    static constexpr int QROW = MMA16 ? DK * 2 + 16 : DK * 8 + 64;
-    static constexpr int Q = MMA16 && NB == 1 ? 0 : ROWS * QROW;
-    static constexpr int PT = MMA16 ? 0 : WARPS * kBlock * 20 * 4;     // fp32 weights on their way to B operands
-    static constexpr int ML = 2 * (WARPS + 1) * ROWS * 4;
-    static constexpr int FIXED = 1024 + MERGE + Q + PT + ML;               // (1024: the ring's alignment)
-    static constexpr int FIT = (kSmemMax - 768 - FIXED) / (WARPS * STAGE);  // (768: barriers and the like)
-    static constexpr int STAGES = FIT < 6 ? FIT : 6;
-    static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int SMEM = RING + FIXED;
-    static_assert(STAGES >= 2, "ring");
-    static_assert(MERGE % 16 == 0 && Q % 16 == 0 && PT % 16 == 0 && ML % 8 == 0, "alignment");
+    static constexpr Room R = room_of(DK, DV, E, WARPS, MOST);
+    static constexpr int MC = R.columns, QROW = R.q_row, STAGES = R.tiles, RING = STAGES * STAGE;
+    static constexpr int SMEM = 1024 + RING + R.merge + R.q + R.weights + R.sums;
+    static_assert(STAGES >= 4, "ring");
+    static_assert(R.merge % 16 == 0 && R.q % 16 == 0 && R.weights % 16 == 0 && DV % MC == 0, "alignment");
+    static_assert(WARPS * kBlock * (DV + 4) * 4 <= RING, "a cluster's CTAs join in the ring");
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -155,6 +181,25 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same with zero accumulators
+template <typename T>
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else if constexpr (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // 8 x 8 transpose of 16-bit elements across the warp: lane (g, t) gives row g, columns 2t,
 // 2t + 1 and gets row g of the transpose.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -162,29 +207,28 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// (x, y) as 16-bit pairs hi + lo
+// (x, y) as a 16-bit pair, and what is left of them
 template <typename T>
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ uint32_t round2(float &x, float &y) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
         const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
+        x -= f.x;
+        y -= f.y;
+        return *reinterpret_cast<const uint32_t *>(&h);
     } else {
         const __half2 h = __floats2half2_rn(x, y);
         const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
+        x -= f.x;
+        y -= f.y;
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
-// fp32 as tf32 hi + lo: 11 bits each, to nearest, so 22 of the value's 24
+// fp32 as tf32 hi + lo: hi to nearest, so that lo has 12 bits and keeps 11 of them.  (A NaN's hi may be
+// anything, but its lo is NaN; so is an infinity's.)
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    const float r = x - __uint_as_float(hi);
-    lo = (__float_as_uint(r) + 0x1000u) & 0xffffe000u;
-    if (r != r) lo = 0x7fffffffu;      // (a NaN's payload may carry into the sign; an infinity is NaN too)
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
 template <typename T> __device__ __forceinline__ float to_float(T x);
@@ -216,7 +260,7 @@ __device__ __forceinline__ int tiles_at(const Attn &a, int b) {
 __device__ __forceinline__ int units_of(const Attn &a) { return a.Hkv * a.n_rb; }     // of a sequence
 
 // A partial result: [rows][DV] outputs, [rows] maxima, [rows] sums.
-template <int ROWS, int DV> constexpr size_t kPartial = (size_t)ROWS * (DV + 2);
+__device__ __forceinline__ size_t partial_size(int rows, int dv) { return (size_t)rows * (dv + 2); }
 
 // Sum of x over the block, in every thread; `part` is 32 ints, free again after the next barrier.
 __device__ __forceinline__ int block_sum(int x, int *part, int warps) {
@@ -227,21 +271,24 @@ __device__ __forceinline__ int block_sum(int x, int *part, int warps) {
     return __reduce_add_sync(0xffffffffu, lane < warps ? part[lane] : 0);
 }
 
-// Tiles of all units; a length beyond the table shows in the status word.
-__device__ __forceinline__ int total_tiles(const Attn &a, int *part, int threads) {
+// Steps of a unit of n tiles: the first kUnitCost stand for its beginning and end.
+__device__ __forceinline__ int steps_of(int n) { return n ? n + kUnitCost : 0; }
+
+// Steps of all units; a length beyond the table shows in the status word.
+__device__ __forceinline__ int total_steps(const Attn &a, int *part, int threads) {
     int n = 0;
     for (int b = threadIdx.x; b < a.n_seqs; b += threads) {
-        n += tiles_at(a, b);
+        n += steps_of(tiles_at(a, b));
         if (a.lens[b] > capacity(a)) *a.status = GDN_ERR_PAGE;
     }
     return block_sum(n, part, threads / 32) * units_of(a);
 }
 
-// Whole warp: the sequence that tile x of all lies in, and the tiles before it.
-__device__ __forceinline__ int find_tile(const Attn &a, int x, int lane, int *before) {
+// Whole warp: the sequence that step x of all lies in, and the steps before it.
+__device__ __forceinline__ int find_step(const Attn &a, int x, int lane, int *before) {
     int done = 0;
     for (int base = 0;; base += 32) {
-        const int n = base + lane < a.n_seqs ? tiles_at(a, base + lane) * units_of(a) : 0;
+        const int n = base + lane < a.n_seqs ? steps_of(tiles_at(a, base + lane)) * units_of(a) : 0;
         int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -259,44 +306,53 @@ __device__ __forceinline__ int find_tile(const Attn &a, int x, int lane, int *be
     }
 }
 
-// Runs of a call of T tiles: fewer where they would have less than a tile for each warp.
-__device__ __forceinline__ int runs_of(int T, int warps) { return min(kGrid, (T + warps - 1) / warps); }
+// Runs of a call of T steps: fewer where they would have less than a tile for each group.
+__device__ __forceinline__ int runs_of(const Attn &a, int T) { return min(kGrid, (T + a.groups - 1) / a.groups); }
 
-// A walk over the tiles of a CTA's run: a segment is the part of a unit that lies in it.
+// A walk over the units of a CTA's run: a segment is the part of a unit that lies in it.
 struct Walk {
-    int left;                          // tiles of the run from this segment on
+    int left;                          // steps of the run from this segment on
     int b, j;                          // sequence, unit in it
-    int begin, end, n;                 // tiles [begin, end) of the unit's n
-    __device__ __forceinline__ void cut() { end = min(n, begin + left); }
+    int from, to;                      // steps of the unit, and
+    int begin, end, n;                 // tiles [begin, end) of its n
+    int raw;                           // the sequence's length
+    __device__ __forceinline__ void set(const Attn &a) {
+        raw = max(a.lens[b], 0);
+        n = (min(raw, capacity(a)) + kTile - 1) / kTile;
+    }
+    __device__ __forceinline__ bool cut() {
+        to = min(n + kUnitCost, from + left);
+        begin = max(from - kUnitCost, 0);
+        end = max(to - kUnitCost, 0);
+        return begin < end;
+    }
     __device__ __forceinline__ bool next(const Attn &a) {
-        left -= end - begin;
+        left -= to - from;
         if (left <= 0) return false;
-        begin = 0;
+        from = 0;
         if (++j == units_of(a)) {
             j = 0;
             do {
                 if (++b >= a.n_seqs) return false;
-                n = tiles_at(a, b);
+                set(a);
             } while (n == 0);
         }
-        cut();
-        return true;
+        return cut();                  // (a run may end within a unit's first steps)
     }
 };
 
-// What fills a warp's ring: a walk that runs ahead of the computation.
+// What fills a group's ring: a walk that runs ahead of the computation, by the group's first warp.
 template <typename G>
 struct Feed {
     Walk w;
     bool more;
-    int at;                            // the warp's next tile of the segment
-    int page, off;                     // lane i: page and first token in it of its tile first + i * WARPS
+    int at;                            // the group's next tile of the segment
+    int page, off;                     // lane i: page and first token in it of its tile first + i * groups
     int first;
-    uint32_t bad;                      // stages whose tile is in no page of the cache
 
     __device__ __forceinline__ void look(const Attn &a, int lane) {
         first = at;
-        const int tile = at + lane * G::WARPS;
+        const int tile = at + lane * a.groups;
         page = -1;
         off = 0;
         if (more && tile < w.end) {
@@ -305,32 +361,32 @@ struct Feed {
             off = (tile - slot * a.tpp) * kTile;
         }
     }
-    __device__ __forceinline__ void start(const Attn &a, const Walk &run, bool any, int warp, int lane) {
+    __device__ __forceinline__ void start(const Attn &a, const Walk &run, bool any, int group, int lane) {
         w = run;
         more = any;
-        bad = 0;
-        at = w.begin + warp;
-        settle(a, warp);
+        at = w.begin + group;
+        settle(a, group);
         look(a, lane);
     }
-    // on to a segment in which this warp has a tile
-    __device__ __forceinline__ bool settle(const Attn &a, int warp) {
+    // on to a segment in which this group has a tile
+    __device__ __forceinline__ bool settle(const Attn &a, int group) {
         bool moved = false;
         while (more && at >= w.end) {
             more = w.next(a);
-            at = w.begin + warp;
+            at = w.begin + group;
             moved = true;
         }
         return moved;
     }
+    // the next tile into a stage; *none: it is in no page of the cache
     __device__ __forceinline__ void issue(const Attn &a, const CUtensorMap *km, const CUtensorMap *vm, uint8_t *stage,
-                                          uint64_t *bar, int s, int warp, int lane) {
+                                          uint64_t *bar, uint8_t *none, int group, int lane) {
         if (!more) return;
-        const int i = (at - first) / G::WARPS;
+        const int i = (at - first) / a.groups;
         const int p = __shfl_sync(0xffffffffu, page, i), o = __shfl_sync(0xffffffffu, off, i);
-        const bool ok = (unsigned)p < (unsigned)a.n_pages;
-        bad = ok ? bad & ~(1u << s) : bad | 1u << s;
         if (lane == 0) {
+            const bool ok = (unsigned)p < (unsigned)a.n_pages;
+            *none = !ok;
             if (!ok) {
                 *a.status = GDN_ERR_PAGE;
                 ptx::mbar_arrive(bar);
@@ -348,120 +404,113 @@ struct Feed {
                     ptx::tma_load_4d(stage + G::KB + c * 2048, vm, bar, c * G::BOX, v1, v2, v3);
             }
         }
-        at += G::WARPS;
-        if (settle(a, warp) || i == 31) look(a, lane);
+        at += a.groups;
+        if (settle(a, group) || i == 31) look(a, lane);
     }
 };
 
-// One warp's share of one unit: an online softmax over tiles.
-template <typename T, int DK, int DV, int NB, bool COLS>
+// The warps of a group, which use one tile at a time together.
+struct Group {
+    int id, threads;                   // named barrier; 32: a warp by itself
+    __device__ __forceinline__ void sync() const {
+        if (threads == 32) __syncwarp();
+        else ptx::named_sync(id, threads);
+    }
+    __device__ __forceinline__ bool any(bool x) const {
+        if (threads == 32) return __any_sync(0xffffffffu, x);
+        int y;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
+                     "selp.s32 %0, 1, 0, q;\n\t}" : "=r"(y) : "r"((int)x), "r"(id), "r"(threads) : "memory");
+        return y != 0;
+    }
+};
+
+// One warp's share of one unit: an online softmax of 8 rows over tiles.
+template <typename T, int DK, int DV, typename G, bool COLS>
 struct Unit {
-    using G = Geo<T, DK, DV, NB>;
     static constexpr bool MMA16 = G::MMA16;
+    static constexpr int U = G::U;
     static constexpr int KS = DK / 16, MT = DV / 16;   // 16-element steps of a key, blocks of a value row
     // weights of f16 rows are scaled by 2^12, so that small ones keep their bits
     static constexpr float kBits = std::is_same<T, __half>::value ? 12.f : 0.f;
 
-    uint32_t qf[MMA16 && NB == 1 ? KS : 1][2];
-    float m[NB][2], l[NB][2];          // of rows 2t, 2t + 1: running maximum, this lane's sum of weights
-    float o[NB][MT][4];
-    int qi[NB][2];                     // the row's query; -1: no such row
+    uint32_t qf[MMA16 ? KS : 1][2];
+    float m[2], l[2];                  // of rows 2t, 2t + 1: running maximum, this lane's sum of weights
+    float o[MT][4];
+    int qi[2];                         // the row's query; -1: no such row
     int raw, all, len;                 // length; tokens that every row sees and no mask changes; in the table
     int b;
 
-    __device__ __forceinline__ static int row_of(int rb, int nb, int c) {
-        return COLS ? c & 3 : rb * G::ROWS + nb * kBlock + c;
-    }
     __device__ __forceinline__ static const T *q_row(const Attn &a, int b, int hk, int row) {
         const int h = hk * (a.H / a.Hkv) + row / a.n_q, i = row % a.n_q;
         return static_cast<const T *>(a.q) + b * a.q_seq + h * a.q_head + i * a.q_query;
     }
 
-    // Queries to shared memory, by the whole block (a barrier follows).
-    __device__ __forceinline__ static void stage_queries(const Attn &a, int b, int hk, int rb, uint8_t *sq) {
-        constexpr int PER = 16 / (int)sizeof(T);
-        for (int x = threadIdx.x; x < G::ROWS * (DK / PER); x += G::THREADS) {
-            const int r = x / (DK / PER), c = x - r * (DK / PER), row = rb * G::ROWS + r;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row < a.R) w = *reinterpret_cast<const uint4 *>(q_row(a, b, hk, row) + c * PER);
-            if constexpr (MMA16) {
-                *reinterpret_cast<uint4 *>(sq + r * G::QROW + c * 16) = w;
-            } else {
-                uint4 hi, lo;
-                split_tf32(__uint_as_float(w.x), hi.x, lo.x);
-                split_tf32(__uint_as_float(w.y), hi.y, lo.y);
-                split_tf32(__uint_as_float(w.z), hi.z, lo.z);
-                split_tf32(__uint_as_float(w.w), hi.w, lo.w);
-                *reinterpret_cast<uint4 *>(sq + r * G::QROW + c * 16) = hi;
-                *reinterpret_cast<uint4 *>(sq + r * G::QROW + DK * 4 + c * 16) = lo;
-            }
+    // fp32 queries of the unit's blocks to shared memory, by the whole CTA (a barrier follows).
+    __device__ __forceinline__ static void stage_queries(const Attn &a, int b, int hk, int row0, uint8_t *sq) {
+        for (int x = threadIdx.x; x < a.blocks * kBlock * (DK / 4); x += G::THREADS) {
+            const int r = x / (DK / 4), c = x - r * (DK / 4);
+            uint4 w = make_uint4(0, 0, 0, 0), hi, lo;
+            if (row0 + r < a.R) w = *reinterpret_cast<const uint4 *>(q_row(a, b, hk, row0 + r) + c * 4);
+            split_tf32(__uint_as_float(w.x), hi.x, lo.x);
+            split_tf32(__uint_as_float(w.y), hi.y, lo.y);
+            split_tf32(__uint_as_float(w.z), hi.z, lo.z);
+            split_tf32(__uint_as_float(w.w), hi.w, lo.w);
+            *reinterpret_cast<uint4 *>(sq + r * G::QROW + c * 16) = hi;
+            *reinterpret_cast<uint4 *>(sq + r * G::QROW + DK * 4 + c * 16) = lo;
         }
     }
 
-    __device__ __forceinline__ void begin(const Attn &a, int seq, int hk, int rb, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-        b = seq;
-        raw = max(a.lens[b], 0);
-        len = min(raw, capacity(a));
-        all = a.mask ? 0 : a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len;
-        if constexpr (MMA16 && NB == 1) {
-            const int row = row_of(rb, 0, g);
+    // 16-bit queries of rows row0 .. row0 + 7 of kv head hk, as B operands.
+    __device__ __forceinline__ static void load_queries(const Attn &a, int b, int hk, int row0, int lane,
+                                                        uint32_t (&q)[MMA16 ? KS : 1][2]) {
+        if constexpr (MMA16) {
+            const int g = lane >> 2, t = lane & 3, row = COLS ? g & 3 : row0 + g;
             const bool ok = row < a.R;
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(q_row(a, b, hk, ok ? row : 0));
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(q_row(a, b, hk, ok ? row : 0)) + t;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                qf[s][0] = ok ? p[s * 8 + t] : 0u;
-                qf[s][1] = ok ? p[s * 8 + 4 + t] : 0u;
+                q[s][0] = ok ? p[s * 8] : 0u;
+                q[s][1] = ok ? p[s * 8 + 4] : 0u;
             }
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = row_of(rb, nb, 2 * t + r);
-                qi[nb][r] = row < a.R ? row % a.n_q : -1;
-                m[nb][r] = -INFINITY;
-                l[nb][r] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nb][i][e] = 0.f;
         }
     }
+    __device__ __forceinline__ void begin(const Attn &a, const Walk &w, int row0, int lane) {
+        const int t = lane & 3;
+        b = w.b;
+        raw = w.raw;
+        len = min(raw, capacity(a));
+        all = a.mask ? 0 : a.causal ? min(len, max(raw - a.n_q + 1, 0)) : len;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = COLS ? (2 * t + r) & 3 : row0 + 2 * t + r;
+            qi[r] = row < a.R ? row % a.n_q : -1;
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    }
 
-    // S^T of a tile: entry e is token g + 8 (e >> 1) and row 2t + (e & 1) of block nb.
-    __device__ __forceinline__ void scores(uint32_t k, const uint8_t *sq, int lane, float (&s)[NB][4]) const {
+    // S^T of a tile: entry e is token g + 8 (e >> 1) and row 2t + (e & 1).
+    __device__ __forceinline__ void scores(uint32_t k, const uint8_t *sq, int lane, float (&s)[4]) const {
         const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
         if constexpr (MMA16) {
             const uint32_t row = k + (lane & 15) * 128, x = lane & 7, half = lane >> 4;
-            float s2[4] = {0.f, 0.f, 0.f, 0.f};        // a second chain of products where there is one block
+            float s2[4];               // two chains of products
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
                 uint32_t A[4];
                 ldsm4(A, row + (c >> 2) * 2048 + (((2 * (c & 3) + half) ^ x) << 4));
-                if constexpr (NB == 1) {
-                    if (c & 1) mma<T>(s2, A, qf[c][0], qf[c][1]);
-                    else mma<T>(s[0], A, qf[c][0], qf[c][1]);
-                } else {
-                    // two blocks' B operands: rows (lane & 7) of block 2 p + (lane >> 4), half (lane >> 3) & 1
-#pragma unroll
-                    for (int p = 0; p < NB / 2; ++p) {
-                        uint32_t B[4];
-                        ldsm4(B, ptx::smem_u32(sq) + ((2 * p + (lane >> 4)) * kBlock + (lane & 7)) * G::QROW + c * 32 +
-                                     ((lane >> 3) & 1) * 16);
-                        mma<T>(s[2 * p], A, B[0], B[1]);
-                        mma<T>(s[2 * p + 1], A, B[2], B[3]);
-                    }
-                }
+                if (c == 0) mma0<T>(s, A, qf[c][0], qf[c][1]);
+                else if (c == 1) mma0<T>(s2, A, qf[c][0], qf[c][1]);
+                else if (c & 1) mma<T>(s2, A, qf[c][0], qf[c][1]);
+                else mma<T>(s, A, qf[c][0], qf[c][1]);
             }
-            if constexpr (NB == 1)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
+            for (int e = 0; e < 4; ++e) s[e] += s2[e];
         } else {
             // Lane (g, t) has elements 4t .. 4t + 3 of each 16 of tokens g and g + 8: the first two
             // are columns t and t + 4 of one k8 product, the others of the next (the queries' likewise).
@@ -469,6 +518,8 @@ struct Unit {
             const uint32_t ra = k + g * 128, x = g & 7, odd = g & 1;
             const uint8_t *q = sq + g * G::QROW + t * 16;
             float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = 0.f;
 #pragma unroll 2
             for (int c = 0; c < DK / 32; ++c) {
                 const uint32_t p0 = ra + c * 2048 + (((t + 4 * odd) ^ x) << 4);
@@ -486,22 +537,22 @@ struct Unit {
                     split_tf32(__uint_as_float(v.y), hi[3], lo[3]);
                     mma<T>(s1, lo, qh.x, qh.y);
                     mma<T>(s2, hi, ql.x, ql.y);
-                    mma<T>(s[0], hi, qh.x, qh.y);
+                    mma<T>(s, hi, qh.x, qh.y);
                     split_tf32(__uint_as_float(u.z), hi[0], lo[0]);
                     split_tf32(__uint_as_float(v.z), hi[1], lo[1]);
                     split_tf32(__uint_as_float(u.w), hi[2], lo[2]);
                     split_tf32(__uint_as_float(v.w), hi[3], lo[3]);
                     mma<T>(s1, lo, qh.z, qh.w);
                     mma<T>(s2, hi, ql.z, ql.w);
-                    mma<T>(s[0], hi, qh.z, qh.w);
+                    mma<T>(s, hi, qh.z, qh.w);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[0][e] += s1[e] + s2[e];
+            for (int e = 0; e < 4; ++e) s[e] += s1[e] + s2[e];
         }
     }
 
-    // Element of value row `tok` that o[.][i][e] sums, as the stage holds it.
+    // Element of a value row that o[i][e] sums, and where the stage holds it.
     __device__ __forceinline__ static int element_of(int i, int e, int g) {
         return MMA16 ? i * 16 + g + 8 * (e >> 1) : (i >> 1) * 32 + 4 * g + 2 * (i & 1) + (e >> 1);
     }
@@ -512,47 +563,44 @@ struct Unit {
 
     // Values of tokens that some row must not see may be anything, infinities and NaN among them, and
     // a weight of 0 does not silence those in a product.  Where such a tile has any, the rows that
-    // see them take them one by one, and the products take zeros for them.
-    __device__ __forceinline__ void odd_values(uint8_t *v, const float (&p)[NB][4], const float (&x)[NB][4],
-                                            const float (&cf)[NB][2], int lane) {
+    // see them take them one by one, and the products take zeros for them.  (p: weights, x: scores.)
+    __device__ __forceinline__ void odd_values(const Group &grp, uint8_t *v, const float (&p)[4], const float (&x)[4],
+                                               float (&cf)[2], int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nb][i][e] *= cf[nb][e & 1];
+            for (int e = 0; e < 4; ++e) o[i][e] *= cf[e & 1];
+        cf[0] = cf[1] = 1.f;
 #pragma unroll 1
         for (int tok = 0; tok < kTile; ++tok) {
             const int src = (tok & 7) * 4 + t;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int r = 0; r < 2; ++r) {
+                const float w0 = __shfl_sync(0xffffffffu, p[r], src), w1 = __shfl_sync(0xffffffffu, p[r + 2], src);
+                const float x0 = __shfl_sync(0xffffffffu, x[r], src), x1 = __shfl_sync(0xffffffffu, x[r + 2], src);
+                const float w = tok < 8 ? w0 : w1, sc = tok < 8 ? x0 : x1;
+                if (sc == -INFINITY || (COLS && t >= 2)) continue;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float w0 = __shfl_sync(0xffffffffu, p[nb][r], src), w1 = __shfl_sync(0xffffffffu, p[nb][r + 2], src);
-                    const float x0 = __shfl_sync(0xffffffffu, x[nb][r], src), x1 = __shfl_sync(0xffffffffu, x[nb][r + 2], src);
-                    const float w = tok < 8 ? w0 : w1, sc = tok < 8 ? x0 : x1;
-                    if (sc == -INFINITY || (COLS && t >= 2)) continue;
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = r; e < 4; e += 2) {
-                            const float y = to_float<T>(*reinterpret_cast<const T *>(v + value_at(tok, element_of(i, e, g))));
-                            if (!isfinite(y)) o[nb][i][e] = fmaf(w, y, o[nb][i][e]);
-                        }
-                }
+                    for (int e = r; e < 4; e += 2) {
+                        const float y = to_float<T>(*reinterpret_cast<const T *>(v + value_at(tok, element_of(i, e, g))));
+                        if (!isfinite(y)) o[i][e] = fmaf(w, y, o[i][e]);
+                    }
+            }
         }
-        __syncwarp();
-        for (int i = lane; i < kTile * DV; i += 32) {
+        grp.sync();
+        for (int i = lane; i < kTile * DV; i += 32) {  // (every warp of the group alike)
             T *y = reinterpret_cast<T *>(v + value_at(i / DV, i % DV));
             if (!isfinite(to_float<T>(*y))) *y = T(0.f);
         }
-        ptx::fence_proxy_async_smem();  // (the next copy into this stage comes after these stores)
-        __syncwarp();
+        ptx::fence_proxy_async_smem();                 // (the next copy into this stage comes after these stores)
+        grp.sync();
     }
     __device__ __forceinline__ static bool any_odd(const uint8_t *v, int lane) {
         bool bad = false;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < G::VB / 512; ++i) {
             const uint4 w = *reinterpret_cast<const uint4 *>(v + (i * 32 + lane) * 16);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -569,84 +617,134 @@ struct Unit {
         return __any_sync(0xffffffffu, bad);
     }
 
-    // The tile in `stage`, tokens pos .. pos + 15 of the sequence; `good`: it is there.
-    __device__ __forceinline__ void tile(const Attn &a, uint8_t *stage, const uint8_t *sq, float *pt, int pos, bool good,
-                                         int lane) {
+    // One tile or (U = 2) two: tokens pos[u] .. pos[u] + 15 of the sequence, in stage[u].
+    __device__ __forceinline__ void tiles(const Attn &a, const Group &grp, uint8_t *const (&stage)[U], const int (&pos)[U],
+                                          bool two, const uint8_t *sq, float *pt, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        if (!good) return;
-        const uint32_t k = ptx::smem_u32(stage), v = k + G::KB;
-        float s[NB][4], x[NB][4], cf[NB][2];
-        scores(k, sq, lane, s);
-        const bool plain = pos + kTile <= all;
+        float s[U][4], x[U][4], cf[2];
+        bool plain = true;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int u = 0; u < U; ++u) {
+            if (u == 0 || two) {
+                scores(ptx::smem_u32(stage[u]), sq, lane, s[u]);
+                plain &= pos[u] + kTile <= all;
+            }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int e = 0; e < 4; ++e) x[u][e] = u == 0 || two ? s[u][e] * a.scale : -INFINITY;
+        }
+        if (!plain) {
 #pragma unroll
-                for (int e = r; e < 4; e += 2) x[nb][e] = s[nb][e] * a.scale;
-                if (!plain) {
-                    const int i = qi[nb][r];
+            for (int u = 0; u < U; ++u) {
+                if (u == 1 && !two) break;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = qi[r];
                     const long long lim = a.causal ? min((long long)len, (long long)raw - a.n_q + 1 + i) : len;
 #pragma unroll
                     for (int e = r; e < 4; e += 2) {
-                        const int j = pos + g + 8 * (e >> 1);
+                        const int j = pos[u] + g + 8 * (e >> 1);
                         if (i < 0 || j >= lim) {
-                            x[nb][e] = -INFINITY;
+                            x[u][e] = -INFINITY;
                         } else if (a.mask) {
-                            const float add = to_float<T>(static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j]);
-                            x[nb][e] = add == -INFINITY ? add : x[nb][e] + add;
+                            const float add = to_float<T>(
+                                static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j]);
+                            x[u][e] = add == -INFINITY ? add : x[u][e] + add;
                         }
                     }
                 }
-                float mx = fmaxf(x[nb][r], x[nb][r + 2]);
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                // Weights go by differences, 2^((x - maximum) log2 e), which are exact where they matter:
-                // masks of the type's lowest value and scores of any size keep their order, and the factor of
-                // earlier tiles is exactly 1 while the maximum stands.
-                const float old = m[nb][r], mn = fmaxf(old, mx), base = mn == -INFINITY ? 0.f : mn;
-                m[nb][r] = mn;
-                cf[nb][r] = exp2_approx((old - base) * kLog2e);
-                s[nb][r] = exp2_approx(fmaf(x[nb][r] - base, kLog2e, kBits));
-                s[nb][r + 2] = exp2_approx(fmaf(x[nb][r + 2] - base, kLog2e, kBits));
-                l[nb][r] = fmaf(l[nb][r], cf[nb][r], s[nb][r] + s[nb][r + 2]);
             }
-        if (!plain && any_odd(stage + G::KB, lane)) {
-            odd_values(stage + G::KB, s, x, cf, lane);
+        }
+        float mx[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
+        if constexpr (U == 2) {
+            mx[0] = fmaxf(mx[0], fmaxf(x[1][0], x[1][2]));
+            mx[1] = fmaxf(mx[1], fmaxf(x[1][1], x[1][3]));
+        }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) cf[nb][0] = cf[nb][1] = 1.f;
+        for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], off));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            // Weights go by differences, 2^((x - maximum) log2 e), which are exact where they matter:
+            // masks of the type's lowest value and scores of any size keep their order, and the factor of
+            // earlier tiles is exactly 1 while the maximum stands.
+            const float old = m[r], mn = fmaxf(old, mx[r]), base = mn == -INFINITY ? 0.f : mn;
+            m[r] = mn;
+            cf[r] = exp2_approx((old - base) * kLog2e);
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u][r] = exp2_approx(fmaf(x[u][r] - base, kLog2e, kBits));
+                s[u][r + 2] = exp2_approx(fmaf(x[u][r + 2] - base, kLog2e, kBits));
+                sum += s[u][r] + s[u][r + 2];
+            }
+            l[r] = fmaf(l[r], cf[r], sum);
+        }
+        if (!plain) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if ((u == 0 || two) && any_odd(stage[u] + G::KB, lane)) odd_values(grp, stage[u] + G::KB, s[u], x[u], cf, lane);
         }
         if constexpr (MMA16) {
-            uint32_t ph[NB][2], pl[NB][2];
+            // Weights as 16-bit terms, largest first: two, and a third of bf16 where the outputs are fp32.  In
+            // COLS the second stands in columns 4 .. 7 of the first's products, where the rows' queries stand again.
+            constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+            const bool third = BF && a.out_type == GDN_DTYPE_F32;
+            uint32_t p1[U][2], p2[U][2], p3[U][2];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t hi, lo;
-                    split2<T>(s[nb][2 * h], s[nb][2 * h + 1], hi, lo);
+                    float y = s[u][2 * h], z = s[u][2 * h + 1];
+                    p1[u][h] = round2<T>(y, z);
+                    p2[u][h] = round2<T>(y, z);
+                    if constexpr (BF) p3[u][h] = third ? round2<T>(y, z) : 0u;
                     if constexpr (COLS) {
-                        ph[nb][h] = transpose8(t >= 2 ? lo : hi);      // columns 4 .. 7: the remainders
-                    } else {
-                        ph[nb][h] = transpose8(hi);
-                        pl[nb][h] = transpose8(lo);
+                        p1[u][h] = t >= 2 ? p2[u][h] : p1[u][h];
+                        if constexpr (BF) p2[u][h] = t >= 2 ? 0u : p3[u][h];
                     }
+                    p1[u][h] = transpose8(p1[u][h]);
+                    if (!COLS || third) p2[u][h] = transpose8(p2[u][h]);
+                    if (!COLS && third) p3[u][h] = transpose8(p3[u][h]);
                 }
             const uint32_t tok = (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t row = v + tok * 128, sw = lane & 7, half = (lane >> 3) & 1;
+            const uint32_t row = tok * 128 + G::KB, sw = lane & 7, half = (lane >> 3) & 1;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
+                const uint32_t at = row + (i >> 2) * 2048 + (((2 * (i & 3) + half) ^ sw) << 4);
                 uint32_t A[4];
-                ldsm4_t(A, row + (i >> 2) * 2048 + (((2 * (i & 3) + half) ^ sw) << 4));
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (!COLS) mma<T>(d, A, pl[nb][0], pl[nb][1]);   // small terms first
-                    mma<T>(d, A, ph[nb][0], ph[nb][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nb][i][e] = fmaf(o[nb][i][e], cf[nb][e & 1], d[e]);
+                float d[4];
+                ldsm4_t(A, ptx::smem_u32(stage[0]) + at);
+                if constexpr (COLS) {  // small terms first
+                    if (third) {
+                        mma0<T>(d, A, p2[0][0], p2[0][1]);
+                        mma<T>(d, A, p1[0][0], p1[0][1]);
+                    } else {
+                        mma0<T>(d, A, p1[0][0], p1[0][1]);
+                    }
+                } else {
+                    if (third) {
+                        mma0<T>(d, A, p3[0][0], p3[0][1]);
+                        mma<T>(d, A, p2[0][0], p2[0][1]);
+                    } else {
+                        mma0<T>(d, A, p2[0][0], p2[0][1]);
+                    }
+                    mma<T>(d, A, p1[0][0], p1[0][1]);
                 }
+                if constexpr (U == 2) {
+                    if (two) {
+                        ldsm4_t(A, ptx::smem_u32(stage[1]) + at);
+                        if (!COLS && third) mma<T>(d, A, p3[1][0], p3[1][1]);
+                        if (!COLS || third) mma<T>(d, A, p2[1][0], p2[1][1]);
+                        mma<T>(d, A, p1[1][0], p1[1][1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = fmaf(o[i][e], cf[e & 1], d[e]);
             }
         } else {
+            static_assert(MMA16 || U == 1, "one tile of fp32 rows at a time");
+            const uint32_t v = ptx::smem_u32(stage[0]) + G::KB;
             // weights to [row][token]; lane (g, t) takes row g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
             pt[(2 * t) * 20 + g] = s[0][0];
             pt[(2 * t + 1) * 20 + g] = s[0][1];
@@ -675,7 +773,7 @@ struct Unit {
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    float d[4];
                     uint32_t hi[2][4], lo[2][4];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
@@ -684,34 +782,31 @@ struct Unit {
                         split_tf32(__uint_as_float(w[2 * n + 1][2 * i]), hi[n][2], lo[n][2]);
                         split_tf32(__uint_as_float(w[2 * n + 1][2 * i + 1]), hi[n][3], lo[n][3]);
                     }
+                    mma0<T>(d, lo[0], ph[0], ph[1]);
+                    mma<T>(d, lo[1], ph[2], ph[3]);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma<T>(d, lo[n], ph[2 * n], ph[2 * n + 1]);
-                        mma<T>(d, hi[n], pl[2 * n], pl[2 * n + 1]);
-                    }
+                    for (int n = 0; n < 2; ++n) mma<T>(d, hi[n], pl[2 * n], pl[2 * n + 1]);
 #pragma unroll
                     for (int n = 0; n < 2; ++n) mma<T>(d, hi[n], ph[2 * n], ph[2 * n + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[0][2 * c + i][e] = fmaf(o[0][2 * c + i][e], cf[0][e & 1], d[e]);
+                    for (int e = 0; e < 4; ++e) o[2 * c + i][e] = fmaf(o[2 * c + i][e], cf[e & 1], d[e]);
                 }
             }
+            __syncwarp();
         }
     }
 
-    // Sums over the lanes that share rows; in COLS, the remainders' columns.
+    // Sums over the lanes that share rows; in COLS, the other columns' terms.
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
+            for (int r = 0; r < 2; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+        if constexpr (COLS)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], off);
-            if constexpr (COLS)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nb][i][e] += __shfl_xor_sync(0xffffffffu, o[nb][i][e], 2);
-        }
+                for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
     }
 };
 
@@ -739,38 +834,39 @@ __device__ __forceinline__ float4 fma4(float w, float4 x, float4 y) {
     return make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
 }
 
-// Output row `row` of (b, hk), elements 4c .. : x / l
-template <int DV>
-__device__ __forceinline__ void write_out(const Attn &a, int b, int hk, int row, int c, float4 x, float l) {
-    if (row >= a.R) return;
-    const int h = hk * (a.H / a.Hkv) + row / a.n_q, i = row % a.n_q;
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-    store4(a.out, a.out_type, (((size_t)b * a.n_q + i) * a.H + h) * DV + 4 * c,
-           make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+// Which row of the output, (n_seqs, n_q, n_heads), belongs to row `row` of (b, hk)
+__device__ __forceinline__ long long out_row(const Attn &a, int b, int hk, int row) {
+    const int h = row / a.n_q, i = row - h * a.n_q;
+    return ((long long)b * a.n_q + i) * a.H + hk * (a.H / a.Hkv) + h;
 }
 
-template <typename T, int DK, int DV, int NB, bool COLS>
-__global__ void __launch_bounds__(Geo<T, DK, DV, NB>::THREADS, 1)
+template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
+__global__ void __launch_bounds__(WARPS * 32, 1)
 attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const Attn a) {
-    using G = Geo<T, DK, DV, NB>;
-    using U = Unit<T, DK, DV, NB, COLS>;
+    using G = Geo<T, DK, DV, WARPS, MOST, U>;
+    using Part = Unit<T, DK, DV, G, COLS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
-    float *merge = reinterpret_cast<float *>(ring + G::RING);              // [WARPS][8][DV]
-    uint8_t *sq = ring + G::RING + G::MERGE;
-    float *pts = reinterpret_cast<float *>(sq + G::Q);
-    float *sm = reinterpret_cast<float *>(sq + G::Q + G::PT);              // [WARPS + 1][ROWS] maxima
-    float *sl = sm + (G::WARPS + 1) * G::ROWS;                             // ... and sums; the last: the block's
-    __shared__ uint64_t full[G::WARPS][G::STAGES];
+    float *merge = reinterpret_cast<float *>(ring + G::RING);              // [WARPS][8][MC + 4]
+    uint8_t *sq = ring + G::RING + G::R.merge;
+    float *pts = reinterpret_cast<float *>(sq + G::R.q);
+    float *sm = reinterpret_cast<float *>(sq + G::R.q + G::R.weights);     // [WARPS][8] maxima, then the CTA's
+    float *sl = sm + (WARPS + MOST) * kBlock;                              // ... and sums
+    __shared__ uint64_t full[G::STAGES];
+    __shared__ uint8_t none[G::STAGES];
     __shared__ int part[32], start[2], gave_up;
+    __shared__ long long place[MOST * kBlock];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (lane == 0) {
-        for (int s = 0; s < G::STAGES; ++s) ptx::mbar_init(&full[warp][s], 1);
-        ptx::fence_mbar_init();
-    }
+    // groups of a.blocks warps (the warps left over only help to join)
+    const int group = warp / a.blocks, block = warp - group * a.blocks;
+    const bool works = group < a.groups, leads = works && block == 0;
+    const Group grp{1 + group, 32 * a.blocks};
+    const int stages = min(G::STAGES / a.groups, 8);
     if (tid == 0) {
         gave_up = 0;
+        for (int s = 0; s < G::STAGES; ++s) ptx::mbar_init(&full[s], 1);
+        ptx::fence_mbar_init();
         if (a.n_pages) {
             ptx::prefetch_tmap(&km);
             ptx::prefetch_tmap(&vm);
@@ -779,28 +875,29 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     kv4::after_the_kernel_before();
 
     // ---- this CTA's run
-    Walk run{0, 0, 0, 0, 0, 0};
+    Walk run{0, 0, 0, 0, 0, 0, 0, 0, 0};
     int rank = 0, cta = 0;
+    bool any = false;
     if (a.cluster) {
         rank = (int)(blockIdx.x % (unsigned)a.cluster);
         const int unit = (int)(blockIdx.x / (unsigned)a.cluster);
         run.b = unit / units_of(a);
         run.j = unit - run.b * units_of(a);
-        run.n = tiles_at(a, run.b);
-        if (tid == 0 && a.lens[run.b] > capacity(a)) *a.status = GDN_ERR_PAGE;
+        run.set(a);
+        if (tid == 0 && run.raw > capacity(a)) *a.status = GDN_ERR_PAGE;
         run.begin = (int)((long long)run.n * rank / a.cluster);
         run.end = (int)((long long)run.n * (rank + 1) / a.cluster);
-        run.left = run.end - run.begin;
+        any = run.begin < run.end;
         __syncthreads();
     } else {
         cta = (int)blockIdx.x;
-        const int total = total_tiles(a, part, G::THREADS);
-        const int runs = runs_of(total, G::WARPS);
+        const int total = total_steps(a, part, G::THREADS);
+        const int runs = runs_of(a, total);
         const int from = cta < runs ? run_begin(total, runs, cta) : 0;
         run.left = cta < runs ? run_begin(total, runs, cta + 1) - from : 0;
         if (warp == 0 && run.left > 0) {
             int before;
-            const int b = find_tile(a, from, lane, &before);
+            const int b = find_step(a, from, lane, &before);
             if (lane == 0) {
                 start[0] = b;
                 start[1] = from - before;
@@ -814,155 +911,225 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         __syncthreads();
         if (run.left > 0) {
             run.b = start[0];
-            run.n = tiles_at(a, run.b);
-            run.j = start[1] / run.n;
-            run.begin = start[1] - run.j * run.n;
-            run.cut();
+            run.set(a);
+            run.j = start[1] / steps_of(run.n);
+            run.from = start[1] - run.j * steps_of(run.n);
+            any = run.cut();
         }
     }
-    const bool any = run.left > 0;
 
-    uint8_t *mine = ring + warp * (G::STAGES * G::STAGE);
+    const int slot0 = group * stages;  // the group's ring
     float *pt = pts + (G::MMA16 ? 0 : warp * kBlock * 20);
     Feed<G> feed;
-    feed.start(a, run, any, warp, lane);
-    for (int s = 0; s < G::STAGES; ++s) feed.issue(a, &km, &vm, mine + s * G::STAGE, &full[warp][s], s, warp, lane);
+    if (leads) {
+        feed.start(a, run, any, group, lane);
+        for (int s = slot0; s < slot0 + stages; ++s)
+            feed.issue(a, &km, &vm, ring + s * G::STAGE, &full[s], &none[s], group, lane);
+    }
 
     // ---- segments
-    int it = 0;                        // tiles of this warp so far
+    int s = 0;                         // the ring's next stage, and its phase
+    uint32_t phase = 0;
     bool dead = false;
+    uint32_t next_q[Part::MMA16 ? Part::KS : 1][2];    // the next segment's queries, loaded while this one's parts join
+    auto row0_of = [&](const Walk &w) { return w.j % a.n_rb * a.blocks * kBlock; };
+    if (any || a.cluster) Part::load_queries(a, run.b, run.j / a.n_rb, row0_of(run) + block * kBlock, lane, next_q);
     for (bool more = any || a.cluster; more;) {
-        const int hk = run.j / a.n_rb, rb = run.j - hk * a.n_rb;
-        U u;
-        if constexpr (G::Q != 0) {
-            U::stage_queries(a, run.b, hk, rb, sq);
+        const int hk = run.j / a.n_rb, row0 = row0_of(run);
+        Part u;
+        if constexpr (G::R.q != 0) {
+            Part::stage_queries(a, run.b, hk, row0, sq);
             __syncthreads();
         }
-        u.begin(a, run.b, hk, rb, lane);
-        for (int tile = run.begin + warp; tile < run.end; tile += G::WARPS, ++it) {
-            const int s = it % G::STAGES;
-            uint8_t *stage = mine + s * G::STAGE;
+#pragma unroll
+        for (int i = 0; i < (Part::MMA16 ? Part::KS : 1); ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) u.qf[i][e] = next_q[i][e];
+        u.begin(a, run, row0 + block * kBlock, lane);
+        for (int tile = works ? run.begin + group : run.end; tile < run.end; tile += U * a.groups) {
+            const bool pair = U == 2 && tile + a.groups < run.end;
+            uint8_t *stage[U];
+            int at[U], pos[U];
+            bool there[U], came = true;
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                if (x == 1 && !pair) break;
+                at[x] = slot0 + s;
+                stage[x] = ring + at[x] * G::STAGE;
+                pos[x] = (tile + x * a.groups) * kTile;
+                if (!dead) came &= ptx::mbar_wait(&full[at[x]], phase, &gave_up);
+                there[x] = !none[at[x]];
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
             if (!dead) {
-                const bool came = ptx::mbar_wait(&full[warp][s], (it / G::STAGES) & 1, &gave_up);
-                dead = __any_sync(0xffffffffu, !came);
+                dead = grp.any(!came); // (the same for all warps of a group: they meet at its barriers)
                 if (dead) {
                     gave_up = 1;
                     *a.status = GDN_ERR_TIMEOUT;
                 }
             }
             if (dead) continue;
-            u.tile(a, stage, sq, pt, tile * kTile, !(feed.bad >> s & 1u), lane);
-            __syncwarp();
-            feed.issue(a, &km, &vm, stage, &full[warp][s], s, warp, lane);
+            bool two = false, one = there[0];
+            if constexpr (U == 2) {
+                two = pair && there[1];
+                if (!pair) {
+                    stage[1] = stage[0];
+                    pos[1] = pos[0];
+                } else if (two && !there[0]) {         // only the second is there: it stands for the first
+                    stage[0] = stage[1];
+                    pos[0] = pos[1];
+                    one = true;
+                    two = false;
+                }
+            }
+            if (one) u.tiles(a, grp, stage, pos, two, sq + block * kBlock * G::QROW, pt, lane);
+            grp.sync();
+            if (leads) {
+#pragma unroll
+                for (int x = 0; x < U; ++x)
+                    if (x == 0 || pair)
+                        feed.issue(a, &km, &vm, ring + at[x] * G::STAGE, &full[at[x]], &none[at[x]], group, lane);
+            }
         }
         u.finish();
+        Walk next = run;
+        more = any && next.next(a);
+        if (more) Part::load_queries(a, next.b, next.j / a.n_rb, row0_of(next) + block * kBlock, lane, next_q);
 
-        // ---- the warps' parts of the segment join
+        // ---- the groups' parts of the segment join: MC columns at a time, or, when no more tiles come, all of
+        // them in the ring
         const int g = lane >> 2, t = lane & 3;
-        const bool whole = run.begin == 0 && run.end == run.n;
+        const bool whole = run.begin == 0 && run.end == run.n, mine = works && !(COLS && t >= 2);
+        const int rows = a.blocks * kBlock, valid = COLS ? 4 : rows;
+        const bool last = !more && !dead, final = whole && a.cluster < 2;
         float *part_out = whole || a.cluster ? nullptr
-                                             : a.ws + partial_slot(cta, run.begin == 0) * kPartial<G::ROWS, DV>;
-        if (g == 0 && !(COLS && t >= 2))
+                                             : a.ws + partial_slot(cta, run.begin == 0) * partial_size(rows, DV);
+        const int width = last ? DV : G::MC, pitch = width + 4;
+        float *parts = last ? reinterpret_cast<float *>(ring) : merge;
+        if (g == 0 && mine)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int r = 0; r < 2; ++r) {
+                sm[warp * kBlock + 2 * t + r] = u.m[r];
+                sl[warp * kBlock + 2 * t + r] = u.l[r];
+            }
+        __syncthreads();               // (every group is done with the ring, too)
+        // a thread a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output
+        if (tid < valid) {
+            float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    sm[warp * G::ROWS + nb * kBlock + 2 * t + r] = u.m[nb][r];
-                    sl[warp * G::ROWS + nb * kBlock + 2 * t + r] = u.l[nb][r];
+            for (int w = 0; w < WARPS; ++w)
+                if (w < a.groups) M = fmaxf(M, sm[w * rows + tid]);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                if (w < a.groups) {
+                    const float lw = sl[w * rows + tid];
+                    // (a part of NaN scores has no maximum: the row is NaN)
+                    const float f = lw == lw ? weight(sm[w * rows + tid], M) : lw;
+                    L = fmaf(f, lw, L);
+                    sm[w * rows + tid] = f;
                 }
+            if (final) {
+                const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            if (!(COLS && t >= 2))
+                for (int w = 0; w < WARPS; ++w)
+                    if (w < a.groups) sm[w * rows + tid] *= f;
+            } else if (part_out) {
+                part_out[rows * DV + tid] = M;
+                part_out[rows * (DV + 1) + tid] = L;
+            } else {
+                sm[WARPS * kBlock + tid] = M;
+                sl[WARPS * kBlock + tid] = L;
+            }
+            place[tid] = row0 + tid < a.R ? out_row(a, run.b, hk, row0 + tid) : -1;
+        }
 #pragma unroll
-                for (int i = 0; i < U::MT; ++i)
+        for (int c0 = 0; c0 < DV; c0 += G::MC) {
+            if (mine) {
+                float *p = parts + (warp * kBlock + 2 * t) * pitch + Part::element_of(0, 0, g) + (last ? c0 : 0);
+#pragma unroll
+                for (int i = 0; i < G::MC / 16; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        merge[(warp * kBlock + 2 * t + (e & 1)) * DV + U::element_of(i, e, g)] = u.o[nb][i][e];
+                        p[(e & 1) * pitch + Part::element_of(i, e, 0)] = u.o[c0 / 16 + i][e];
+            }
+            if (last && c0 + G::MC < DV) continue;
+            const int from = last ? 0 : c0;
             __syncthreads();
-            constexpr int VALID = COLS ? 4 : kBlock;
-            for (int x = tid; x < VALID * (DV / 4); x += G::THREADS) {
-                const int r = x / (DV / 4), c = x - r * (DV / 4), row = nb * kBlock + r;
-                float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < G::WARPS; ++w) M = fmaxf(M, sm[w * G::ROWS + row]);
+#pragma unroll 1
+            for (int x = tid; x < valid * (width / 4); x += G::THREADS) {
+                const int row = x / (width / 4), c = x - row * (width / 4);    // (a power of two)
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                float L = 0.f;
 #pragma unroll
-                for (int w = 0; w < G::WARPS; ++w) {
-                    const float f = weight(sm[w * G::ROWS + row], M);
-                    const float lw = sl[w * G::ROWS + row];
-                    if (f != 0.f || lw != lw) {        // (a row of NaN scores has no maximum)
-                        L = fmaf(f, lw, L);
-                        y = fma4(f, *reinterpret_cast<const float4 *>(merge + (w * kBlock + r) * DV + 4 * c), y);
-                    }
-                }
-                if (a.cluster > 1) {
-                    *reinterpret_cast<float4 *>(merge + r * DV + 4 * c) = y;
-                    if (c == 0) {
-                        sm[G::WARPS * G::ROWS + row] = M;
-                        sl[G::WARPS * G::ROWS + row] = L;
-                    }
+                for (int w = 0; w < WARPS; ++w)
+                    if (w < a.groups)
+                        y = fma4(sm[w * rows + row], *reinterpret_cast<const float4 *>(parts + (w * rows + row) * pitch + 4 * c), y);
+                if (final) {
+                    if (place[row] >= 0) store4(a.out, a.out_type, (size_t)place[row] * DV + from + 4 * c, y);
                 } else if (part_out) {
-                    *reinterpret_cast<float4 *>(part_out + row * DV + 4 * c) = y;
-                    if (c == 0) {
-                        part_out[G::ROWS * DV + row] = M;
-                        part_out[G::ROWS * (DV + 1) + row] = L;
-                    }
+                    *reinterpret_cast<float4 *>(part_out + row * DV + from + 4 * c) = y;
                 } else {
-                    write_out<DV>(a, run.b, hk, rb * G::ROWS + row, c, y, L);
+                    *reinterpret_cast<float4 *>(parts + row * pitch + 4 * c) = y;
                 }
             }
-            if (a.cluster > 1) {       // ... and the CTAs': each takes its share of the rows' elements
-                cluster_sync();
-                for (int x = rank * G::THREADS + tid; x < VALID * (DV / 4); x += a.cluster * G::THREADS) {
-                    const int r = x / (DV / 4), c = x - r * (DV / 4), row = nb * kBlock + r;
-                    float mk[kMaxCluster], M = -INFINITY, L = 0.f;
-#pragma unroll
-                    for (int p = 0; p < kMaxCluster; ++p) {
-                        mk[p] = p < a.cluster ? peer_float(sm + G::WARPS * G::ROWS + row, p) : -INFINITY;
-                        M = fmaxf(M, mk[p]);
-                    }
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int p = 0; p < kMaxCluster; ++p) {
-                        const float f = weight(mk[p], M);
-                        if (p >= a.cluster) continue;
-                        const float lp = peer_float(sl + G::WARPS * G::ROWS + row, p);
-                        if (f != 0.f || lp != lp) {
-                            L = fmaf(f, lp, L);
-                            y = fma4(f, peer_float4(merge + r * DV + 4 * c, p), y);
-                        }
-                    }
-                    write_out<DV>(a, run.b, hk, rb * G::ROWS + row, c, y, L);
-                }
-                cluster_sync();        // peers are done reading
-            } else {
-                __syncthreads();
-            }
+            if (!last) __syncthreads();
         }
-        more = any && run.next(a);
+        if (a.cluster > 1) {           // ... and the CTAs': each takes its share of the rows' elements
+            cluster_sync();
+            // (a CTA whose waits gave up has joined them elsewhere: the outputs are lost, the status says so)
+            for (int x = rank * G::THREADS + tid; x < valid * (DV / 4); x += a.cluster * G::THREADS) {
+                const int row = x / (DV / 4), c = x - row * (DV / 4);
+                float mk[kMaxCluster], lk[kMaxCluster], M = -INFINITY, L = 0.f;
+                float4 yk[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int p = 0; p < kMaxCluster; ++p) {
+                    const int q = p < a.cluster ? p : 0;
+                    mk[p] = peer_float(sm + WARPS * kBlock + row, q);
+                    lk[p] = peer_float(sl + WARPS * kBlock + row, q);
+                    yk[p] = peer_float4(reinterpret_cast<float *>(ring) + row * (DV + 4) + 4 * c, q);
+                }
+#pragma unroll
+                for (int p = 0; p < kMaxCluster; ++p)
+                    if (p < a.cluster) M = fmaxf(M, mk[p]);
+#pragma unroll
+                for (int p = 0; p < kMaxCluster; ++p) {
+                    const float f = lk[p] == lk[p] ? weight(mk[p], M) : lk[p];
+                    if (p < a.cluster) {
+                        L = fmaf(f, lk[p], L);
+                        y = fma4(f, yk[p], y);
+                    }
+                }
+                const float f = L == 0.f ? 0.f : 1.f / L;
+                if (place[row] >= 0)
+                    store4(a.out, a.out_type, (size_t)place[row] * DV + 4 * c, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+            }
+            cluster_sync();            // peers are done reading
+        }
+        run = next;
     }
 }
 
 // Joins the parts of units that runs cut: block (c - 1, y) is for the unit that the boundary between runs c - 1
 // and c cuts, if it is the first to cut it, and rows y, y + gridDim.y, ... of it.
 constexpr int kJoinThreads = 256;
-template <int ROWS, int DV>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const int warps) {
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
     constexpr int COLS4 = DV / 4, GROUPS = kJoinThreads / COLS4;           // groups of threads share a row's parts
     __shared__ int part[32], found[2];
     __shared__ float4 sums[kJoinThreads];
     __shared__ float sums_l[GROUPS];
     kv4::after_the_kernel_before();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int total = total_tiles(a, part, kJoinThreads);
-    const int runs = runs_of(total, warps);
+    const int total = total_steps(a, part, kJoinThreads);
+    const int runs = runs_of(a, total), rows = a.blocks * kBlock;
     const int c = (int)blockIdx.x + 1;
     if (c >= runs) return;
     const int cut = run_begin(total, runs, c);
     if (tid < 32) {
         int before;
-        const int b = find_tile(a, cut, lane, &before);
+        const int b = find_step(a, cut, lane, &before);
         if (lane == 0) {
             found[0] = b;
             found[1] = before;
@@ -970,17 +1137,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const 
     }
     __syncthreads();
     const int b = found[0], n = tiles_at(a, b);
-    const int j = (cut - found[1]) / n, first = found[1] + j * n;
-    if (cut == first) return;
+    const int j = (cut - found[1]) / steps_of(n), first = found[1] + j * steps_of(n) + kUnitCost;      // its first tile
+    if (cut <= first) return;
     const int r0 = run_of(total, runs, first), r1 = run_of(total, runs, first + n - 1);
     if (c != r0 + 1) return;
     const int hk = j / a.n_rb, rb = j - hk * a.n_rb, parts = r1 - r0 + 1;
     const int group = tid / COLS4, col = tid - group * COLS4;
     // part p: of run r0 + p; the unit begins in run r0
-    auto at = [&](int p) { return a.ws + partial_slot(r0 + p, p == 0) * kPartial<ROWS, DV>; };
-    for (int row = (int)blockIdx.y; row < ROWS && rb * ROWS + row < a.R; row += gridDim.y) {
+    auto at = [&](int p) { return a.ws + partial_slot(r0 + p, p == 0) * partial_size(rows, DV); };
+    for (int row = (int)blockIdx.y; row < rows && rb * rows + row < a.R; row += gridDim.y) {
         float M = -INFINITY;
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, at(p)[ROWS * DV + row]);
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, at(p)[rows * DV + row]);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -988,13 +1155,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const 
 #pragma unroll 4
         for (int p = group; p < parts; p += GROUPS) {
             const float *q = at(p);
-            const float m = q[ROWS * DV + row], l = q[ROWS * (DV + 1) + row];
+            const float m = q[rows * DV + row], l = q[rows * (DV + 1) + row];
             const float4 x = *reinterpret_cast<const float4 *>(q + row * DV + 4 * col);
-            const float f = weight(m, M);
-            if (f != 0.f || l != l) {
-                L = fmaf(f, l, L);
-                y = fma4(f, x, y);
-            }
+            const float f = l == l ? weight(m, M) : l;
+            L = fmaf(f, l, L);
+            y = fma4(f, x, y);
         }
         sums[tid] = y;
         if (col == 0) sums_l[group] = L;
@@ -1004,18 +1169,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const 
                 y = fma4(1.f, sums[k * COLS4 + col], y);
                 L += sums_l[k];
             }
-            write_out<DV>(a, b, hk, rb * ROWS + row, col, y, L);
+            const float f = L == 0.f ? 0.f : 1.f / L;
+            store4(a.out, a.out_type, (size_t)out_row(a, b, hk, rb * rows + row) * DV + 4 * col,
+                   make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
         }
         __syncthreads();
     }
 }
 
-template <typename T, int DK, int DV, int NB, bool COLS>
+template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
 cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn &a, int grid, cudaStream_t stream) {
-    using G = Geo<T, DK, DV, NB>;
+    using G = Geo<T, DK, DV, WARPS, MOST, U>;
     static PerDeviceOnce setup;
     cudaError_t e = setup.run([] {
-        return cudaFuncSetAttribute(attn_kernel<T, DK, DV, NB, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
@@ -1032,29 +1199,24 @@ cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, DK, DV, NB, COLS>, km, vm, a);
+    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, km, vm, a);
     if (e != cudaSuccess || a.cluster || grid < 2) return e;
-    const int rows = a.R < G::ROWS ? a.R : G::ROWS;
-    return kv4::launch_early(join_kernel<G::ROWS, DV>, dim3((unsigned)grid - 1, (unsigned)(rows < 8 ? rows : 8)),
-                             kJoinThreads, 0, stream, a, G::WARPS);
+    return kv4::launch_early(join_kernel<DV>, dim3((unsigned)grid - 1, (unsigned)(a.R < 8 ? a.R : 8)), kJoinThreads, 0, stream,
+                             a);
 }
 
 template <typename T, int DK, int DV>
 cudaError_t launch_rows(const CUtensorMap &km, const CUtensorMap &vm, const Attn &a, int grid, cudaStream_t stream) {
-    if constexpr (sizeof(T) == 4) {
-        return launch_one<T, DK, DV, 1, false>(km, vm, a, grid, stream);
-    } else {
-        constexpr bool wide = DK > 128 || DV > 128;
-        // of at most 4 rows, the weights' remainders enter in the free columns of the same MMAs
-        if (a.R <= 4) return launch_one<T, DK, DV, 1, true>(km, vm, a, grid, stream);
-        switch (blocks_of(wide, false, a.R)) {
-            case 1: return launch_one<T, DK, DV, 1, false>(km, vm, a, grid, stream);
-            case 2: return launch_one<T, DK, DV, 2, false>(km, vm, a, grid, stream);
-            default:
-                if constexpr (!wide) return launch_one<T, DK, DV, 4, false>(km, vm, a, grid, stream);
-                return cudaErrorInvalidValue;
-        }
+    constexpr int E = (int)sizeof(T);
+    constexpr Share few = share_of(DK, DV, E, 1), many = share_of(DK, DV, E, kBlock + 1);
+    // two tiles at a time where registers and the groups' rings allow
+    constexpr int U = many.warps == 12 ? 2 : 1;
+    if (a.R > kBlock) return launch_one<T, DK, DV, many.warps, many.most, U, false>(km, vm, a, grid, stream);
+    if constexpr (E == 2) {
+        // of at most 4 rows, the weights' second terms enter in the free columns of the same MMAs
+        if (a.R <= 4) return launch_one<T, DK, DV, few.warps, 1, 1, true>(km, vm, a, grid, stream);
     }
+    return launch_one<T, DK, DV, few.warps, 1, 1, false>(km, vm, a, grid, stream);
 }
 
 }  // namespace
