@@ -527,27 +527,45 @@ def flash_attn_kv4(q, cache, page_table, seq_lens, head_dim_v=None, mask=None, s
 
 
 # ------------------------------------------------------- pages, rotary positions, 16- and 32-bit cache
+#
+# Each call first looks whether its arguments are as expected, in as few steps as it takes; what is
+# wrong with the others is found out afterwards (_refuse), and strides go along only where a tensor is not dense.
+# Where another device is current, or a stream is given, the call makes them current and starts again (_there).
 
 
-def _int32(t, shape, dev, name):
-    if t.shape != shape or t.dtype != _torch.int32 or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {shape} int32 on the other tensors' device, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+def _refuse(checks):
+    """Raise for the first (name, tensor, shape, dtype, device index) that is not so; None in a shape: any size."""
+    for name, t, shape, dtype, dev in checks:
+        if t is None:
+            continue
+        if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)) or t.dtype != dtype:
+            want = "(" + ", ".join("any" if w is None else str(w) for w in shape) + ")"
+            raise ValueError(f"{name}: expected {want} {dtype}, got {tuple(t.shape)} {t.dtype}")
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{name}: all tensors must be on one CUDA device")
+        if dtype == _torch.int32 and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"rows of {name} must be contiguous")
+    raise ValueError("arguments do not fit together")
 
 
-def _pages_check(page_table, lens, free_pages, free_count):
-    """Shapes, types and devices of tables and a stack of pages; their device, sequences, entries, pages."""
-    if page_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("page_table must be 2-D and free_pages 1-D")
-    dev = page_table.get_device()
-    if dev < 0:
-        raise ValueError("all tensors must be CUDA tensors")
-    B, max_pages = page_table.shape
-    _int32(page_table, (B, max_pages), dev, "page_table")
-    _int32(free_pages, free_pages.shape, dev, "free_pages")
-    _int32(free_count, (1,), dev, "free_count")
-    _int32(lens, (B,), dev, "lengths")
-    return dev, B, max_pages, free_pages.shape[0]
+def _there(dev, stream, call, *args, **kw):
+    """call(*args, **kw) with ``dev`` current, and ``stream`` too if one is given, so that what the call
+    allocates belongs to its stream."""
+    if stream is None:
+        with _torch.cuda.device(dev):
+            return call(*args, **kw)
+    if stream.device.index != dev:
+        raise ValueError("stream must be on the tensors' device")
+    with _torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _strides(*xs):
+    """Host array of the strides of every dimension but the last."""
+    v = [s for x in xs for s in x.stride()[:-1]]
+    return (ctypes.c_longlong * len(v))(*v)
 
 
 def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_new: int = 1, new_lens=None, *,
@@ -564,30 +582,43 @@ def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_
     (n_seqs + 1).  A stack that runs out, and whatever else only the device can
     see, shows as ERR_PAGE in device_status().  The rest of the contract is with
     gdn_page_assign in include/gdn.h."""
-    L, torch = lib(), _kv4_torch()
-    dev, B, max_pages, n_pages = _pages_check(page_table, seq_lens, free_pages, free_count)
-    if new_lens is not None:
-        _int32(new_lens, (B,), dev, "new_lens")
+    L, torch = _lib or lib(), _torch or _kv4_torch()
+    i32, dev, table, lens, pool = torch.int32, page_table.get_device(), page_table.shape, seq_lens.shape, free_pages.shape
+    B = table[0] if table else 0
     packed = n_tokens is not None
+    if not (dev >= 0 and len(table) == 2 and page_table.dtype is i32 and page_table.is_contiguous()
+            and len(lens) == 1 and lens[0] == B and seq_lens.dtype is i32 and seq_lens.get_device() == dev
+            and seq_lens.is_contiguous()
+            and len(pool) == 1 and free_pages.dtype is i32 and free_pages.get_device() == dev
+            and free_pages.is_contiguous()
+            and free_count.shape == (1,) and free_count.dtype is i32 and free_count.get_device() == dev
+            and (new_lens is None or (new_lens.shape == lens and new_lens.dtype is i32
+                                      and new_lens.get_device() == dev and new_lens.is_contiguous()))):
+        _refuse((("page_table", page_table, (None, None), i32, dev), ("seq_lens", seq_lens, (B,), i32, dev),
+                 ("free_pages", free_pages, (None,), i32, dev), ("free_count", free_count, (1,), i32, dev),
+                 ("new_lens", new_lens, (B,), i32, dev)))
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _there(dev, stream, page_assign, page_table, seq_lens, free_pages, free_count, page_size, n_new, new_lens,
+                      n_tokens=n_tokens, slots=slots, positions=positions, offsets=offsets)
     shape = (n_tokens,) if packed else (B, n_new)
     for name, t, want in (("slots", slots, shape), ("positions", positions, shape), ("offsets", offsets, (B + 1,))):
-        if t is not None:
-            _int32(t, want, dev, name)
+        if t is not None and not (t.shape == want and t.dtype is i32 and t.get_device() == dev and t.is_contiguous()):
+            _refuse(((name, t, want, i32, dev),))
     if offsets is not None and not packed:
         raise ValueError("offsets go with n_tokens")
-
-    def call(handle):
-        new = lambda t, s: torch.empty(s, dtype=torch.int32, device=page_table.device) if t is None else t  # noqa: E731
-        s, p, o = new(slots, shape), new(positions, shape), new(offsets, (B + 1,)) if packed else None
-        rc = L.gdn_page_assign(page_table.data_ptr(), seq_lens.data_ptr(),
-                               None if new_lens is None else new_lens.data_ptr(), free_pages.data_ptr(),
-                               free_count.data_ptr(), s.data_ptr(), p.data_ptr(), o.data_ptr() if packed else None, B,
-                               n_new, n_tokens if packed else 0, page_size, max_pages, n_pages, handle)
-        if rc != OK:
-            raise GdnError(rc, "gdn_page_assign")
-        return s, p, o
-
-    return _kv4_call(torch, dev, stream, call)
+    if slots is None:
+        slots = torch.empty(shape, dtype=i32, device=page_table.device)
+    if positions is None:
+        positions = torch.empty(shape, dtype=i32, device=page_table.device)
+    if packed and offsets is None:
+        offsets = torch.empty((B + 1,), dtype=i32, device=page_table.device)
+    rc = L.gdn_page_assign(page_table.data_ptr(), seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
+                           free_pages.data_ptr(), free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                           offsets.data_ptr() if packed else None, B, n_new, n_tokens if packed else 0, page_size,
+                           table[1], pool[0], torch._C._cuda_getCurrentRawStream(dev))
+    if rc != OK:
+        raise GdnError(rc, "gdn_page_assign")
+    return slots, positions, offsets
 
 
 def page_release(page_table, from_lens, free_pages, free_count, page_size: int, to_lens=None, *, stream=None):
@@ -595,13 +626,25 @@ def page_release(page_table, from_lens, free_pages, free_count, page_size: int, 
 
     Arguments as for page_assign; free_pages and free_count are updated in place.
     A step called off (to_lens: the lengths before it) leaves the stack as it was."""
-    L, torch = lib(), _kv4_torch()
-    dev, B, max_pages, n_pages = _pages_check(page_table, from_lens, free_pages, free_count)
-    if to_lens is not None:
-        _int32(to_lens, (B,), dev, "to_lens")
-    rc = _kv4_call(torch, dev, stream, lambda handle: L.gdn_page_release(
-        page_table.data_ptr(), from_lens.data_ptr(), None if to_lens is None else to_lens.data_ptr(),
-        free_pages.data_ptr(), free_count.data_ptr(), B, page_size, max_pages, n_pages, handle))
+    L, torch = _lib or lib(), _torch or _kv4_torch()
+    i32, dev, table, lens, pool = torch.int32, page_table.get_device(), page_table.shape, from_lens.shape, free_pages.shape
+    B = table[0] if table else 0
+    if not (dev >= 0 and len(table) == 2 and page_table.dtype is i32 and page_table.is_contiguous()
+            and len(lens) == 1 and lens[0] == B and from_lens.dtype is i32 and from_lens.get_device() == dev
+            and from_lens.is_contiguous()
+            and len(pool) == 1 and free_pages.dtype is i32 and free_pages.get_device() == dev
+            and free_pages.is_contiguous()
+            and free_count.shape == (1,) and free_count.dtype is i32 and free_count.get_device() == dev
+            and (to_lens is None or (to_lens.shape == lens and to_lens.dtype is i32
+                                     and to_lens.get_device() == dev and to_lens.is_contiguous()))):
+        _refuse((("page_table", page_table, (None, None), i32, dev), ("from_lens", from_lens, (B,), i32, dev),
+                 ("free_pages", free_pages, (None,), i32, dev), ("free_count", free_count, (1,), i32, dev),
+                 ("to_lens", to_lens, (B,), i32, dev)))
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _there(dev, stream, page_release, page_table, from_lens, free_pages, free_count, page_size, to_lens)
+    rc = L.gdn_page_release(page_table.data_ptr(), from_lens.data_ptr(), None if to_lens is None else to_lens.data_ptr(),
+                            free_pages.data_ptr(), free_count.data_ptr(), B, page_size, table[1], pool[0],
+                            torch._C._cuda_getCurrentRawStream(dev))
     if rc != OK:
         raise GdnError(rc, "gdn_page_release")
 
@@ -611,6 +654,8 @@ class RotaryPlan:
 
     def __init__(self, data, rot_dim, n_axes, neighbours):
         self.data, self.rot_dim, self.n_axes, self.neighbours = data, rot_dim, n_axes, neighbours
+        # what every call hands on
+        self._ptr, self._dev, self._flags = data.data_ptr(), data.get_device(), ROTARY_NEIGHBOURS if neighbours else 0
 
 
 def rotary_plan(rot_dim: int, base: float = 10000.0, *, freqs=None, sections=None, dealt: bool = False,
@@ -646,32 +691,6 @@ def rotary_plan(rot_dim: int, base: float = 10000.0, *, freqs=None, sections=Non
     return RotaryPlan(host.to(device), rot_dim, n_axes, bool(neighbours))
 
 
-def _rows_check(x, dt, dev, name, T=None, H=None, d=None):
-    """(n_tokens, heads, width) of one dtype and device with contiguous rows."""
-    s = x.shape
-    if len(s) != 3 or x.dtype != dt or (T is not None and s[0] != T) or (H is not None and s[1] != H) \
-            or (d is not None and s[2] != d):
-        want = tuple("any" if v is None else v for v in (T, H, d))
-        raise ValueError(f"{name}: expected (n_tokens, heads, head_dim) = {want} {dt}, got {tuple(s)} {x.dtype}")
-    if x.get_device() != dev:
-        raise ValueError("all tensors must be on one CUDA device")
-    if x.stride(2) != 1 and x.numel():
-        raise ValueError(f"rows of {name} must be contiguous")
-
-
-def _positions_check(positions, plan, T, dev):
-    shape = (T,) if positions.dim() == 1 and plan.n_axes == 1 else (plan.n_axes, T)
-    _int32(positions, shape, dev, "positions")
-    if plan.data.get_device() != dev:
-        raise ValueError("plan must be on the tensors' device")
-
-
-def _strides(*xs):
-    """Host array of the strides of every dimension but the last."""
-    v = [s for x in xs for s in x.stride()[:-1]]
-    return (ctypes.c_longlong * len(v))(*v)
-
-
 def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=None, stream=None):
     """Turn pairs of elements of q (n_tokens, n_heads, head_dim) and k (n_tokens, n_heads_kv, head_dim, or
     None) by their tokens' positions; returns (q_out, k_out).
@@ -681,38 +700,52 @@ def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=No
     q_out and k_out may be q and k themselves (default: new dense tensors).
     ``inverse`` turns back, which is also the gradient: rotary(dq_out, dk_out,
     positions, plan, inverse=True) is (dq, dk)."""
-    L, torch = lib(), _kv4_torch()
-    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
-    _rows_check(q, q.dtype, dev, "q")
-    T, H, d = q.shape
-    Hk = 0
-    if k is not None:
-        _rows_check(k, q.dtype, dev, "k", T, None, d)
-        Hk = k.shape[1]
-    elif k_out is not None:
-        raise ValueError("k_out goes with k")
-    if dev < 0:
-        raise ValueError("all tensors must be CUDA tensors")
-    _positions_check(positions, plan, T, dev)
-    for name, t, h in (("q_out", q_out, H), ("k_out", k_out, Hk)):
-        if t is not None:
-            _rows_check(t, q.dtype, dev, name, T, h, d)
-
-    def call(handle):
-        qo = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        ko = None if k is None else torch.empty((T, Hk, d), dtype=q.dtype, device=q.device) if k_out is None else k_out
-        st = _strides(q, qo) if k is None else _strides(q, qo, k, ko)
-        if k is None:
-            st = (ctypes.c_longlong * 8)(*st, 0, 0, 0, 0)
-        rc = L.gdn_rotary(q.data_ptr(), qo.data_ptr(), None if k is None else k.data_ptr(),
-                          None if k is None else ko.data_ptr(), st, positions.data_ptr(), plan.data.data_ptr(), T, H,
-                          Hk, d, plan.rot_dim, plan.n_axes,
-                          (ROTARY_NEIGHBOURS if plan.neighbours else 0) | (ROTARY_INVERSE if inverse else 0), dt, handle)
-        if rc != OK:
-            raise GdnError(rc, "gdn_rotary")
-        return qo, ko
-
-    return _kv4_call(torch, dev, stream, call)
+    L, torch = _lib or lib(), _torch or _kv4_torch()
+    dtype, dev, qs, i32, axes, ps = q.dtype, q.get_device(), q.shape, torch.int32, plan.n_axes, positions.shape
+    dt = _KV4_DTYPES.get(dtype)
+    if dt is None or len(qs) != 3:
+        _kv4_dtype(dtype, "q")
+        raise ValueError(f"q: expected (n_tokens, n_heads, head_dim), got {tuple(qs)}")
+    T, H, d = qs
+    ks = (T, 0, d) if k is None else k.shape
+    if not (dev >= 0 and plan._dev == dev
+            and (k is None or (len(ks) == 3 and ks[0] == T and ks[2] == d and k.dtype is dtype and k.get_device() == dev))
+            and positions.dtype is i32 and positions.get_device() == dev and positions.is_contiguous()
+            and (ps == (axes, T) or (axes == 1 and ps == (T,)))):
+        _refuse((("q", q, (None, None, None), dtype, dev), ("k", k, (T, None, d), dtype, dev),
+                 ("plan", plan.data, (plan.rot_dim // 2, 2), torch.int64, dev),
+                 ("positions", positions, (T,) if len(ps) == 1 and axes == 1 else (axes, T), i32, dev)))
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _there(dev, stream, rotary, q, k, positions, plan, inverse=inverse, q_out=q_out, k_out=k_out)
+    dense = q.is_contiguous() and (k is None or k.is_contiguous())
+    if q_out is None:
+        q_out = torch.empty_like(q) if dense else torch.empty(qs, dtype=dtype, device=q.device)
+    elif not (q_out.shape == qs and q_out.dtype is dtype and q_out.get_device() == dev):
+        _refuse((("q_out", q_out, tuple(qs), dtype, dev),))
+    elif not q_out.is_contiguous():
+        dense = False
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out goes with k")
+    elif k_out is None:
+        k_out = torch.empty_like(k) if dense else torch.empty(ks, dtype=dtype, device=q.device)
+    elif not (k_out.shape == ks and k_out.dtype is dtype and k_out.get_device() == dev):
+        _refuse((("k_out", k_out, tuple(ks), dtype, dev),))
+    elif not k_out.is_contiguous():
+        dense = False
+    strides = None
+    if not dense:
+        every = (q, q_out, q, q_out) if k is None else (q, q_out, k, k_out)
+        if any(t.stride(2) != 1 and t.numel() for t in every):
+            raise ValueError("rows must be contiguous")
+        strides = _strides(*every)
+    rc = L.gdn_rotary(q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
+                      None if k is None else k_out.data_ptr(), strides, positions.data_ptr(), plan._ptr, T, H, ks[1], d,
+                      plan.rot_dim, axes, plan._flags | ROTARY_INVERSE if inverse else plan._flags, dt,
+                      torch._C._cuda_getCurrentRawStream(dev))
+    if rc != OK:
+        raise GdnError(rc, "gdn_rotary")
+    return q_out, k_out
 
 
 def paged_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, head_dim_v=None, *, dtype=None,
@@ -727,69 +760,77 @@ def paged_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, 
     return tuple(torch.empty((n_pages, n_heads_kv, page_size, d), dtype=dtype, device=device) for d in (head_dim_k, dv))
 
 
-def _paged_check(k_cache, v_cache, dt, dev):
-    kn, vn = k_cache.shape, v_cache.shape
-    if len(kn) != 4 or vn[:3] != kn[:3] or len(vn) != 4 or k_cache.dtype != dt or v_cache.dtype != dt:
-        raise ValueError(f"k_cache, v_cache: expected (n_pages, n_heads_kv, page_size, dk / dv) {dt}, got {tuple(kn)} "
-                         f"{k_cache.dtype}, {tuple(vn)} {v_cache.dtype}")
-    if k_cache.get_device() != dev or v_cache.get_device() != dev or dev < 0:
-        raise ValueError("all tensors must be on one CUDA device")
-    if (k_cache.stride(3) != 1 or v_cache.stride(3) != 1) and k_cache.numel():
-        raise ValueError("rows of a cache must be contiguous")
-    return kn[0], kn[1], kn[2], kn[3], vn[3]
-
-
 def paged_write(k, v, k_cache, v_cache, slots, *, stream=None):
     """Copy rows k, v (n_tokens, n_heads_kv, dk / dv) to their slots; returns (k_cache, v_cache).
 
     slots: (n_tokens,) int32 as page_assign gives them (a padded batch's flattened),
     negative: not written; they must differ."""
-    L, torch = lib(), _kv4_torch()
-    dt, dev = _kv4_dtype(k.dtype, "k/v"), k.get_device()
-    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, k.dtype, dev)
-    _rows_check(k, k.dtype, dev, "k", None, Hkv, dk)
-    T = k.shape[0]
-    _rows_check(v, k.dtype, dev, "v", T, Hkv, dv)
-    _int32(slots, (T,), dev, "slots")
-    st = None if k.is_contiguous() and v.is_contiguous() else _strides(k, v)
-    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
-    rc = _kv4_call(torch, dev, stream, lambda handle: L.gdn_paged_write(
-        k.data_ptr(), v.data_ptr(), st, k_cache.data_ptr(), v_cache.data_ptr(), cs, slots.data_ptr(), T, Hkv, dk, dv,
-        n_pages, page, dt, handle))
-    if rc != OK:
-        raise GdnError(rc, "gdn_paged_write")
+    rotary_write(None, k, v, None, None, k_cache, v_cache, slots, stream=stream)
     return k_cache, v_cache
 
 
 def rotary_write(q, k, v, positions, plan, k_cache, v_cache, slots, *, q_out=None, stream=None):
     """rotary of q and k and paged_write of the turned k and of v, in one launch; returns q_out (default: a new dense
     tensor; may be q itself).  Arguments as for rotary and paged_write."""
-    L, torch = lib(), _kv4_torch()
-    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
-    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, q.dtype, dev)
-    _rows_check(q, q.dtype, dev, "q", None, None, dk)
-    T, H, _ = q.shape
-    _rows_check(k, q.dtype, dev, "k", T, Hkv, dk)
-    _rows_check(v, q.dtype, dev, "v", T, Hkv, dv)
-    _positions_check(positions, plan, T, dev)
-    _int32(slots, (T,), dev, "slots")
-    if q_out is not None:
-        _rows_check(q_out, q.dtype, dev, "q_out", T, H, dk)
-    st = None if k.is_contiguous() and v.is_contiguous() else _strides(k, v)
-    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
-
-    def call(handle):
-        qo = torch.empty((T, H, dk), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        qs = None if q.is_contiguous() and qo.is_contiguous() else _strides(q, qo)
-        rc = L.gdn_rotary_write(
-            q.data_ptr(), qo.data_ptr(), k.data_ptr(), v.data_ptr(), qs, st, k_cache.data_ptr(), v_cache.data_ptr(), cs,
-            positions.data_ptr(), plan.data.data_ptr(), slots.data_ptr(), T, H, Hkv, dk, dv, plan.rot_dim, plan.n_axes,
-            n_pages, page, ROTARY_NEIGHBOURS if plan.neighbours else 0, dt, handle)
+    L, torch = _lib or lib(), _torch or _kv4_torch()
+    dtype, dev, ks, vs, cs, ws, i32 = k.dtype, k.get_device(), k.shape, v.shape, k_cache.shape, v_cache.shape, torch.int32
+    dt = _KV4_DTYPES.get(dtype)
+    if dt is None:
+        _kv4_dtype(dtype, "k/v")
+    if not (dev >= 0 and len(ks) == 3 and len(vs) == 3 and len(cs) == 4 and len(ws) == 4
+            and vs[0] == ks[0] and cs[0] == ws[0] and cs[2] == ws[2] and ks[1] == vs[1] == cs[1] == ws[1]
+            and cs[3] == ks[2] and ws[3] == vs[2]
+            and v.dtype is dtype and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and v.get_device() == dev and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and slots.shape == (ks[0],) and slots.dtype is i32 and slots.get_device() == dev and slots.is_contiguous()):
+        H = ks[1] if len(ks) == 3 else None
+        _refuse((("k", k, (None, None, None), dtype, dev), ("v", v, (ks[0], H, None), dtype, dev),
+                 ("k_cache", k_cache, (None, H, None, ks[-1]), dtype, dev),
+                 ("v_cache", v_cache, tuple(cs[:1]) + (H,) + tuple(cs[2:3]) + (vs[-1],), dtype, dev),
+                 ("slots", slots, (ks[0],), i32, dev)))
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _there(dev, stream, rotary_write, q, k, v, positions, plan, k_cache, v_cache, slots, q_out=q_out)
+    T, H, dk = ks
+    rows = pages = None
+    if not (k.is_contiguous() and v.is_contiguous()):
+        if k.numel() and (k.stride(2) != 1 or v.stride(2) != 1):
+            raise ValueError("rows of k and v must be contiguous")
+        rows = _strides(k, v)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        if k_cache.numel() and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+            raise ValueError("rows of a cache must be contiguous")
+        pages = _strides(k_cache, v_cache)
+    if plan is None:
+        rc = L.gdn_paged_write(k.data_ptr(), v.data_ptr(), rows, k_cache.data_ptr(), v_cache.data_ptr(), pages,
+                               slots.data_ptr(), T, H, dk, vs[2], cs[0], cs[2], dt, torch._C._cuda_getCurrentRawStream(dev))
         if rc != OK:
-            raise GdnError(rc, "gdn_rotary_write")
-        return qo
-
-    return _kv4_call(torch, dev, stream, call)
+            raise GdnError(rc, "gdn_paged_write")
+        return None
+    qs, axes, ps = q.shape, plan.n_axes, positions.shape
+    if not (len(qs) == 3 and qs[0] == T and qs[2] == dk and q.dtype is dtype and q.get_device() == dev and plan._dev == dev
+            and positions.dtype is i32 and positions.get_device() == dev and positions.is_contiguous()
+            and (ps == (axes, T) or (axes == 1 and ps == (T,)))
+            and (q_out is None or (q_out.shape == qs and q_out.dtype is dtype and q_out.get_device() == dev))):
+        _refuse((("q", q, (T, None, dk), dtype, dev), ("plan", plan.data, (plan.rot_dim // 2, 2), torch.int64, dev),
+                 ("positions", positions, (T,) if len(ps) == 1 and axes == 1 else (axes, T), i32, dev),
+                 ("q_out", q_out, tuple(qs), dtype, dev)))
+    dense = q.is_contiguous()
+    if q_out is None:
+        q_out = torch.empty_like(q) if dense else torch.empty(qs, dtype=dtype, device=q.device)
+    elif not q_out.is_contiguous():
+        dense = False
+    turned = None
+    if not dense:
+        if q.numel() and (q.stride(2) != 1 or q_out.stride(2) != 1):
+            raise ValueError("rows of q and q_out must be contiguous")
+        turned = _strides(q, q_out)
+    rc = L.gdn_rotary_write(
+        q.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(), turned, rows, k_cache.data_ptr(), v_cache.data_ptr(),
+        pages, positions.data_ptr(), plan._ptr, slots.data_ptr(), T, qs[1], H, dk, vs[2], plan.rot_dim, axes, cs[0], cs[2],
+        plan._flags, dt, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != OK:
+        raise GdnError(rc, "gdn_rotary_write")
+    return q_out
 
 
 def flash_attn_paged_supports(n_q: int, head_dim_k: int, head_dim_v: int) -> bool:
@@ -819,47 +860,62 @@ def flash_attn_paged(q, k_cache, v_cache, page_table, seq_lens, mask=None, scale
     dtype).  Rows that see no token are zeros; tokens that a row does not see have no effect on it.
     ``workspace``: an optional uint8 CUDA tensor of flash_attn_paged_workspace_bytes(...) bytes for one call at a
     time; without it the library allocates in stream order."""
-    L, torch = lib(), _kv4_torch()
-    dt, dev = _kv4_dtype(q.dtype, "q"), q.get_device()
-    n_pages, Hkv, page, dk, dv = _paged_check(k_cache, v_cache, q.dtype, dev)
-    if q.dim() != 4 or q.shape[3] != dk:
-        raise ValueError(f"q: expected (n_seqs, n_heads, n_q, {dk}), got {tuple(q.shape)}")
-    B, H, n_q, _ = q.shape
-    if q.stride(3) != 1 and q.numel():
-        raise ValueError("rows of q must be contiguous")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be 2-D")
-    max_pages = page_table.shape[1]
-    _int32(page_table, (B, max_pages), dev, "page_table")
-    _int32(seq_lens, (B,), dev, "lengths")
-    if mask is not None and (tuple(mask.shape) != (B, 1, n_q, max_pages * page) or mask.dtype != q.dtype):
-        raise ValueError(f"mask: expected {(B, 1, n_q, max_pages * page)} {q.dtype}, got {tuple(mask.shape)} {mask.dtype}")
-    for t in (mask, workspace):
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError("mask and workspace must be contiguous and on the tensors' device")
-    if out is not None:
+    L, torch = _lib or lib(), _torch or _kv4_torch()
+    dtype, dev, qs, cs, vs, ts, i32 = (q.dtype, q.get_device(), q.shape, k_cache.shape, v_cache.shape, page_table.shape,
+                                       torch.int32)
+    dt = _KV4_DTYPES.get(dtype)
+    if dt is None:
+        _kv4_dtype(dtype, "q")
+    if not (dev >= 0 and len(qs) == 4 and len(cs) == 4 and len(vs) == 4 and len(ts) == 2
+            and cs[0] == vs[0] and cs[1] == vs[1] and cs[2] == vs[2] and qs[3] == cs[3] and ts[0] == qs[0]
+            and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and page_table.dtype is i32 and page_table.get_device() == dev and page_table.is_contiguous()
+            and seq_lens.shape == (qs[0],) and seq_lens.dtype is i32 and seq_lens.get_device() == dev
+            and seq_lens.is_contiguous()):
+        _refuse((("q", q, (None, None, None, cs[-1]), dtype, dev), ("k_cache", k_cache, (None,) * 4, dtype, dev),
+                 ("v_cache", v_cache, tuple(cs[:3]) + (None,), dtype, dev),
+                 ("page_table", page_table, (qs[0], None), i32, dev), ("seq_lens", seq_lens, (qs[0],), i32, dev)))
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _there(dev, stream, flash_attn_paged, q, k_cache, v_cache, page_table, seq_lens, mask, scale, causal=causal,
+                      out=out, out_dtype=out_dtype, workspace=workspace)
+    B, H, n_q, dk = qs
+    n_pages, Hkv, page, dv = vs
+    rows = pages = None
+    if not q.is_contiguous():
+        if q.numel() and q.stride(3) != 1:
+            raise ValueError("rows of q must be contiguous")
+        rows = _strides(q)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        if k_cache.numel() and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+            raise ValueError("rows of a cache must be contiguous")
+        pages = _strides(k_cache, v_cache)
+    mask_at = ws_at = None
+    ws_bytes = 0
+    if mask is not None:
+        if mask.shape != (B, 1, n_q, ts[1] * page) or mask.dtype is not dtype or mask.get_device() != dev \
+                or not mask.is_contiguous():
+            raise ValueError(f"mask: expected contiguous {(B, 1, n_q, ts[1] * page)} {dtype} on the tensors' device, got "
+                             f"{tuple(mask.shape)} {mask.dtype}")
+        mask_at = mask.data_ptr()
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the tensors' device")
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if out is None:
         if out_dtype is None:
-            out_dtype = out.dtype
-        if tuple(out.shape) != (B, n_q, H, dv) or out.dtype != out_dtype or not out.is_contiguous() \
-                or out.get_device() != dev:
-            raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype} on the tensors' device")
-    elif out_dtype is None:
-        out_dtype = torch.float32
-    odt = _kv4_dtype(out_dtype, "out_dtype")
-    if scale is None:
-        scale = dk ** -0.5
-    qs = None if q.is_contiguous() else _strides(q)
-    cs = None if k_cache.is_contiguous() and v_cache.is_contiguous() else _strides(k_cache, v_cache)
-
-    def call(handle):
-        o = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=q.device) if out is None else out
-        rc = L.gdn_flash_attn_paged(
-            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), cs, page_table.data_ptr(), seq_lens.data_ptr(),
-            None if mask is None else mask.data_ptr(), o.data_ptr(), B, H, Hkv, n_q, dk, dv, n_pages, page, max_pages,
-            scale, 1 if causal else 0, dt, odt, None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
-        if rc != OK:
-            raise GdnError(rc, "gdn_flash_attn_paged")
-        return o
-
-    return _kv4_call(torch, dev, stream, call)
+            out_dtype = torch.float32
+        out = torch.empty((B, n_q, H, dv), dtype=out_dtype, device=q.device)
+    elif out.shape != (B, n_q, H, dv) or (out_dtype is not None and out.dtype != out_dtype) or not out.is_contiguous() \
+            or out.get_device() != dev:
+        raise ValueError(f"out must be contiguous {(B, n_q, H, dv)} {out_dtype or ''} on the tensors' device")
+    odt = _KV4_DTYPES.get(out.dtype)
+    if odt is None:
+        _kv4_dtype(out.dtype, "out_dtype")
+    rc = L.gdn_flash_attn_paged(
+        q.data_ptr(), rows, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_table.data_ptr(), seq_lens.data_ptr(),
+        mask_at, out.data_ptr(), B, H, Hkv, n_q, dk, dv, n_pages, page, ts[1], dk ** -0.5 if scale is None else scale,
+        1 if causal else 0, dt, odt, ws_at, ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != OK:
+        raise GdnError(rc, "gdn_flash_attn_paged")
+    return out

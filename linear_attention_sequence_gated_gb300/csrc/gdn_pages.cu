@@ -5,8 +5,10 @@
 // exclusive sums p_b of these numbers over the sequences, the k-th page of the step
 // (k = p_b + j - held_b for entry j of sequence b's table) is free[count - 1 - k].  Every
 // entry and every token's slot follows from the two sums (pages and tokens) alone, so all
-// are written at once; only `count` is both read and written, by the threads of one
-// cluster, whose barrier stands between the last read and the write.
+// are written at once, by one CTA for a decode step and by the whole GPU for prompts, each CTA with
+// the sums of all sequences in shared memory.  Only `count` is both read and written: after a barrier
+// in one CTA, by a second kernel where there are more.  Pages go back in one cluster, whose
+// CTAs count what they have to push (some entries may name no page) before any pushes.
 //
 // A decode step moves a few hundred bytes, so the call's time is one launch, the lengths'
 // latency, a scan and a dependent load or two.
@@ -23,8 +25,9 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxSeqs = 16384;        // the two sums of all sequences lie in shared memory
-// Work (tokens, pages, sequences) from which a call takes a cluster of CTAs instead of one.
+// Work (tokens, pages, sequences) from which a call takes more than one CTA.
 constexpr long long kManyItems = 4096;
+constexpr int kGrid = 304;             // CTAs at most, two per SM of the GPU this is written for
 constexpr int kCluster = 8;            // the largest portable size
 
 struct Step {
@@ -35,6 +38,7 @@ struct Step {
     int *slots, *positions, *offsets;
     int *status;
     int n_seqs, n_new, n_tokens, page, max_pages, n_pages;
+    uint32_t magic, shift;             // p / page = umulhi(p, magic) >> shift
     bool packed;
 };
 
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const Step s) {
         pg[s.n_seqs] = taken;
     }
     __syncthreads();
-    const int rank = cluster_rank(), step = cluster_size() * kThreads, me = rank * kThreads + tid;
+    const int step = gridDim.x * kThreads, me = blockIdx.x * kThreads + tid;
     // the k-th page of the step
     auto page_at = [&](int k) { return k < count ? s.free[count - 1 - k] : -1; };
     bad |= taken > count;
@@ -161,56 +165,87 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const Step s) {
         bad |= tokens > s.n_tokens;
         for (int b = me; b <= s.n_seqs; b += step) s.offsets[b] = tok[b];
     }
-    for (int i = me; i < items; i += step) {
-        int slot = -1, pos = 0;
-        if (!s.packed || i < tokens) {
-            const int b = s.packed ? owner(tok, s.n_seqs, i) : i / s.n_new;
-            const int t = i - (s.packed ? tok[b] : b * s.n_new);
+    // A warp's tokens lie together, a thread's 32 apart, mostly of one sequence.
+    const int each = ((items + step - 1) / step) * 32, begin = (me >> 5) * each, lane = tid & 31;
+    const int end = min(begin + each, items);
+    int b = -1, next = 0, base = 0;    // the sequence of token i, where the one after it begins, and it
+    Seq q = {0, 0, 0, 0};
+    for (int i = begin + lane; i < end; i += 32) {
+        if (b < 0 || i >= next) {
             bool past;
-            const Seq q = seq_of(s, b, &past);
-            const int p = t < q.n ? q.first + t : -1, j = p / s.page;
-            if (p >= 0 && j < s.max_pages) {
-                const int page = j < q.held ? s.table[(size_t)b * s.max_pages + j] : page_at(pg[b] + j - q.held);
-                pos = p;
-                if ((unsigned)page < (unsigned)s.n_pages) slot = page * s.page + p - j * s.page;
-                else bad = true;
+            if (s.packed) {
+                b = i < tokens ? owner(tok, s.n_seqs, i) : s.n_seqs;
+                base = tok[b];
+                next = b < s.n_seqs ? tok[b + 1] : items;
+            } else {
+                b = i / s.n_new;
+                base = b * s.n_new;
+                next = base + s.n_new;
             }
+            q = {0, 0, 0, 0};
+            if (b < s.n_seqs) q = seq_of(s, b, &past);
+        }
+        const int p = i - base < q.n ? q.first + i - base : -1;
+        const int j = p < 0 ? s.max_pages : (int)(s.page == 1 ? (uint32_t)p : __umulhi((uint32_t)p, s.magic) >> s.shift);
+        int slot = -1, pos = 0;
+        if (j < s.max_pages) {
+            const int page = j < q.held ? s.table[(size_t)b * s.max_pages + j] : page_at(pg[b] + j - q.held);
+            pos = p;
+            if ((unsigned)page < (unsigned)s.n_pages) slot = page * s.page + p - j * s.page;
+            else bad = true;
         }
         s.slots[i] = slot;
         if (s.positions) s.positions[i] = pos;
     }
     if (bad) *s.status = GDN_ERR_PAGE;
-    cluster_sync();                    // every thread has read the count
-    if (me == 0) *s.count = max(count - taken, 0);
+    if (gridDim.x == 1) {
+        __syncthreads();               // every thread has read the count
+        if (tid == 0) *s.count = max(count - taken, 0);
+    }
 }
 
-// Entry k of all that the step gives back, in the order in which an assign took them.
+// The count after a step of more than one CTA.
+__global__ void __launch_bounds__(kThreads) count_kernel(const Step s) {
+    __shared__ int part[kWarps];
+    kv4::after_the_kernel_before();
+    int n = 0, taken;
+    for (int b = threadIdx.x; b < s.n_seqs; b += kThreads) {
+        bool past;
+        const Seq q = seq_of(s, b, &past);
+        n += q.after - q.held;
+    }
+    block_scan(n, part, &taken);
+    if (threadIdx.x == 0) *s.count = max(min(max(*s.count, 0), s.n_pages) - taken, 0);
+}
+
+// A thread takes kRun neighbouring entries of all that go back, in the order in which an assign took them.
+constexpr int kRun = 8;
 __global__ void __launch_bounds__(kThreads) release_kernel(const Release s) {
-    extern __shared__ int pg[];        // [n_seqs + 1]
+    extern __shared__ int sums[];      // [n_seqs + 1] pages given back before a sequence's, [n_seqs] its first
     __shared__ int part[2][kWarps];
     __shared__ int mine;
+    int *pg = sums, *first = sums + s.n_seqs + 1;
     kv4::after_the_kernel_before();
     const int tid = threadIdx.x;
-    const int raw_count = *s.count;
+    const int raw_count = *s.count, cap = s.max_pages * s.page;
     bool bad = raw_count < 0 || raw_count > s.n_pages;
     const int count = min(max(raw_count, 0), s.n_pages);
-    auto range = [&](int b, int *n) {  // its first page that goes back, and how many
-        const int cap = s.max_pages * s.page;
-        const int from = pages_of(min(s.from[b], cap), s.page);
-        const int to = s.to ? min(pages_of(min(s.to[b], cap), s.page), from) : 0;
-        *n = from - to;
-        return to;
-    };
     int given = 0;
     for (int base = 0, turn = 0; base < s.n_seqs; base += kThreads, turn ^= 1) {
         const int b = base + tid;
-        int n = 0, all;
+        int n = 0, to = 0, all;
         if (b < s.n_seqs) {
-            range(b, &n);
-            bad |= s.from[b] > s.max_pages * s.page;
+            const int len = s.from[b];
+            const int from = pages_of(min(len, cap), s.page);
+            to = s.to ? min(pages_of(min(s.to[b], cap), s.page), from) : 0;
+            n = from - to;
+            bad |= len > cap;
         }
         const int p = block_scan(n, part[turn], &all);
-        if (b < s.n_seqs) pg[b] = given + p;
+        if (b < s.n_seqs) {
+            pg[b] = given + p;
+            first[b] = to;
+        }
         given += all;
     }
     if (tid == 0) pg[s.n_seqs] = given;
@@ -218,20 +253,33 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const Release s) {
     // a contiguous share of the entries; those that name no page (the stack had run out) are left out
     const int rank = cluster_rank(), size = cluster_size();
     const int lo = (int)((long long)given * rank / size), hi = (int)((long long)given * (rank + 1) / size);
-    auto entry = [&](int k) {
-        const int b = owner(pg, s.n_seqs, k);
-        int n;
-        const int page = s.table[(size_t)b * s.max_pages + range(b, &n) + k - pg[b]];
-        return (unsigned)page < (unsigned)s.n_pages ? page : -1;
+    auto load = [&](int k0, int (&page)[kRun]) {
+        int n = 0;
+        int b = k0 < hi ? owner(pg, s.n_seqs, k0) : 0;
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            const int k = k0 + u;
+            page[u] = -1;
+            if (k < hi) {
+                while (k >= pg[b + 1]) ++b;
+                page[u] = s.table[(size_t)b * s.max_pages + first[b] + k - pg[b]];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            if ((unsigned)page[u] >= (unsigned)s.n_pages) page[u] = -1;
+            n += page[u] >= 0;
+        }
+        return n;
     };
-    int held = 0;
-    for (int base = lo; base < hi; base += kThreads) {
-        const int k = base + tid;
-        held += __syncthreads_count(k < hi && entry(k) >= 0);
-    }
-    if (tid == 0) mine = held;
+    constexpr int kBatch = kThreads * kRun;
+    int page[kRun], n = 0, held = 0, all;
+    for (int base = lo; base < hi; base += kBatch) held += n = load(base + tid * kRun, page);
+    block_scan(held, part[0], &all);
+    if (tid == 0) mine = all;
     cluster_sync();
-    int before = 0, all = 0;
+    int before = 0;
+    all = 0;
     for (int r = 0; r < size; ++r) {
         const int x = peer_int(&mine, r);
         if (r < rank) before += x;
@@ -239,21 +287,23 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const Release s) {
     }
     cluster_sync();                    // every thread has read the count and its peers' shares
     bad |= all != given || count + all > s.n_pages;
-    for (int base = lo, turn = 0; base < hi; base += kThreads, turn ^= 1) {
-        const int k = base + tid;
-        const int page = k < hi ? entry(k) : -1;
-        int n;
-        const int q = before + block_scan(page >= 0 ? 1 : 0, part[turn], &n);
-        const int at = count + all - 1 - q;
-        if (page >= 0 && at < s.n_pages) s.free[at] = page;
-        before += n;
+    for (int base = lo, turn = 1; base < hi; base += kBatch, turn ^= 1) {
+        if (hi - lo > kBatch) n = load(base + tid * kRun, page);       // (else they are here already)
+        int sum;
+        int at = count + all - 1 - before - block_scan(n, part[turn], &sum);
+#pragma unroll
+        for (int u = 0; u < kRun; ++u)
+            if (page[u] >= 0) {
+                if (at < s.n_pages) s.free[at] = page[u];
+                --at;
+            }
+        before += sum;
     }
     if (bad) *s.status = GDN_ERR_PAGE;
     if (rank == 0 && tid == 0) *s.count = min(count + all, s.n_pages);
 }
 
-template <typename A>
-cudaError_t launch(void (*kernel)(A), const A &args, long long items, size_t smem, cudaStream_t stream) {
+cudaError_t launch_cluster(const Release &args, long long items, size_t smem, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const unsigned cl = items >= kManyItems ? kCluster : 1;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -268,7 +318,7 @@ cudaError_t launch(void (*kernel)(A), const A &args, long long items, size_t sme
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, args);
+    return cudaLaunchKernelEx(&cfg, release_kernel, args);
 }
 
 // The checks that both calls share; fills the status word's address.
@@ -278,7 +328,7 @@ int check(const int *table, const int *free_pages, const int *count, int n_seqs,
     if (n_seqs < 0 || max_pages < 0 || n_pages < 0) return GDN_ERR_ARG;
     if (page < 1 || n_seqs > kMaxSeqs) return GDN_ERR_SHAPE;
     if ((long long)max_pages * page > INT_MAX || (long long)n_pages * page > INT_MAX ||
-        (long long)n_seqs * max_pages > INT_MAX - kCluster * kThreads)    // (indices step past the end)
+        (long long)n_seqs * max_pages > INT_MAX - kGrid * kThreads)       // (indices step past the end)
         return GDN_ERR_ARG;
     if (n_seqs == 0) return GDN_OK;
     if ((max_pages > 0 && !table) || (n_pages > 0 && !free_pages) || !count) return GDN_ERR_ARG;
@@ -293,7 +343,7 @@ int opt_in() {                         // shared memory for the sums of kMaxSeqs
                                              2 * (kMaxSeqs + 1) * (int)sizeof(int));
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (kMaxSeqs + 1) * (int)sizeof(int));
+                                     (2 * kMaxSeqs + 1) * (int)sizeof(int));
         return e;
     }) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -315,7 +365,7 @@ int gdn_page_assign(int *page_table, const int *seq_lens, const int *new_lens, c
     if ((long long)n_seqs * n_new > INT_MAX) return GDN_ERR_ARG;
     const bool packed = token_offsets != nullptr;
     const long long items = packed ? n_tokens : (long long)n_seqs * n_new;
-    if (items > INT_MAX - kCluster * kThreads) return GDN_ERR_ARG;
+    if (items > INT_MAX - kGrid * kThreads) return GDN_ERR_ARG;
     if (n_seqs == 0 && items == 0 && !packed) return GDN_OK;
     if ((n_seqs > 0 && !seq_lens) || (items > 0 && !slots) || !free_count) return GDN_ERR_ARG;
     if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(slots, 4) || !aligned(positions, 4) ||
@@ -336,10 +386,24 @@ int gdn_page_assign(int *page_table, const int *seq_lens, const int *new_lens, c
     }
     int *status = gdn::status_word();
     if (!status || opt_in() != GDN_OK) return GDN_ERR_CUDA;
+    // p / page for 0 <= p < 2^31: with 2^l >= page, ceil(2^(31 + l) / page) has 32 bits, and its excess times p is
+    // below 2^31, 1 / page of the quotient's unit at most
+    uint32_t magic = 0, shift = 0;
+    if (page_size > 1) {
+        int l = 1;
+        while ((1ll << l) < page_size) ++l;
+        magic = (uint32_t)(((1ull << (31 + l)) + (unsigned)page_size - 1) / (unsigned)page_size);
+        shift = (uint32_t)(l - 1);
+    }
     const Step s{page_table, seq_lens, new_lens, free_pages, free_count, slots, positions, token_offsets, status,
-                 n_seqs, n_new, n_tokens, page_size, max_pages, n_pages, packed};
-    return launch(assign_kernel, s, items + n_seqs, 2 * ((size_t)n_seqs + 1) * sizeof(int),
-                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+                 n_seqs, n_new, n_tokens, page_size, max_pages, n_pages, magic, shift, packed};
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // a thread takes two tokens or more before there are more CTAs
+    const long long work = items + n_seqs;
+    const unsigned grid = work < kManyItems ? 1u : (unsigned)(work / (2 * kThreads) < kGrid ? work / (2 * kThreads) : kGrid);
+    cudaError_t e = gdn::kv4::launch_early(assign_kernel, dim3(grid), kThreads, 2 * ((size_t)n_seqs + 1) * sizeof(int), st, s);
+    if (e == cudaSuccess && grid > 1) e = gdn::kv4::launch_early(count_kernel, dim3(1), kThreads, 0, st, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_page_release(const int *page_table, const int *from_lens, const int *to_lens, int *free_pages,
@@ -360,8 +424,8 @@ int gdn_page_release(const int *page_table, const int *from_lens, const int *to_
     if (!status || opt_in() != GDN_OK) return GDN_ERR_CUDA;
     const Release s{page_table, from_lens, to_lens, free_pages, free_count, status, n_seqs, page_size, max_pages,
                     n_pages};
-    return launch(release_kernel, s, (long long)n_seqs * max_pages, ((size_t)n_seqs + 1) * sizeof(int),
-                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return launch_cluster(s, (long long)n_seqs * max_pages, (2 * (size_t)n_seqs + 1) * sizeof(int),
+                          reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"
