@@ -254,6 +254,7 @@ int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *
     a.n_rb = plan.share.units;
     a.blocks = plan.share.blocks;
     a.groups = plan.share.groups;
+    a.ring = plan.share.ring;
     a.n_pages = n_pages;
     a.tpp = page_size / kTile;
     a.max_pages = max_pages;

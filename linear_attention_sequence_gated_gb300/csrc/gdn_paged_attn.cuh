@@ -56,6 +56,7 @@ struct Attn {
     long long q_seq, q_head, q_query;  // in elements
     int n_seqs, H, Hkv, n_q, R, n_rb;  // R rows a kv head in n_rb units,
     int blocks, groups;                // each of `blocks` blocks of 8, one a warp of each of a CTA's groups
+    int ring;                          // stages of the ring
     int n_pages, tpp, max_pages;       // tpp: tiles of a page
     float scale;
     int out_type, cluster;             // CTAs a unit, or 0: equal runs
@@ -88,26 +89,26 @@ constexpr Room room_of(int dk, int dv, int elt, int warps, int most) {
     return r;
 }
 
-// How the rows of a kv head and the warps of a CTA are shared out.  A group of warps streams tiles through a ring of
-// its own, each warp for another block of 8 rows, so that the cache is read once for all of them.  Up to 8
-// rows: 8 groups of one warp with tiles of 8 KB, fewer with larger ones, so that the rings hold 2 or 3 each.
-// More rows: 12 warps where 168 registers hold a block's output, else 8, as so many groups as there are blocks and
-// tiles in shared memory for.
+// How the rows of a kv head and the warps of a CTA are shared out.  Tiles go round the groups of warps; each
+// warp of a group takes another block of 8 rows of the same tile, so that the cache is read once for all of them:
+// 12 warps where 152 registers hold a block's output, else 8, as so many groups as there are blocks and tiles for.
+// Four more warps fill the ring.
+// A stage of the ring is filled by one warp and, within a segment, emptied by one group only, so the
+// ring is a whole number of tiles a group: a barrier's parity tells a phase from the next, but not from the
+// one after, so whoever waits for a stage has to have seen its last use end.
 struct Share {
-    int warps, most;                   // warps, and blocks of rows of a unit at most
+    int warps, most;                   // warps that compute; blocks of rows of a unit at most
     int blocks, groups, units;         // blocks of a unit, groups of so many warps, units of a kv head
+    int ring;                          // stages
 };
+constexpr int kFillers = 4;
 constexpr Share share_of(int dk, int dv, int elt, int R) {
-    const int tile = kTile * (dk + dv) * elt;
     const bool wide = elt == 4 || dk > 128 || dv > 128;
-    if (R <= kBlock) {
-        const int warps = tile <= 8192 ? 8 : tile <= 16384 ? 4 : 2;
-        return {warps, 1, 1, warps, 1};
-    }
-    const int warps = wide ? 8 : 12, most = wide ? 4 : 6, tiles = room_of(dk, dv, elt, warps, most).tiles;
+    const int warps = wide ? 8 : 12, most = !wide ? 6 : elt == 2 || R > kBlock ? 4 : 1;
     const int all = (R + kBlock - 1) / kBlock, units = (all + most - 1) / most, blocks = (all + units - 1) / units;
-    const int groups = warps / blocks, fed = tiles / 2;
-    return {warps, most, blocks, groups < fed ? groups : fed, units};
+    const int tiles = room_of(dk, dv, elt, warps, most).tiles;
+    const int groups = warps / blocks < tiles ? warps / blocks : tiles;
+    return {warps, most, blocks, groups, units, tiles - tiles % groups};
 }
 
 // The kernel for rows of type T and keys of width DK (one translation unit each).
@@ -129,7 +130,12 @@ struct Geo {
     static constexpr bool MMA16 = E == 2;
     static constexpr int BOX = 128 / E;                // elements of a box's row
     static constexpr int KB = kTile * DK * E, VB = kTile * DV * E, STAGE = KB + VB;
-    static constexpr int THREADS = WARPS * 32;
+    static constexpr int THREADS = WARPS * 32, ALL = THREADS + 32 * kFillers;
+    // Registers a thread: the launch's, and after the warps that fill the ring have given theirs up.
+    static constexpr int REGS = WARPS == 12 ? 128 : 168;
+    static constexpr int FILL_REGS = 56, WORK_REGS = WARPS == 12 ? 152 : 224;
+    static_assert(WARPS % 4 == 0 && THREADS * WORK_REGS + 32 * kFillers * FILL_REGS <= ALL * REGS,
+                  "a split of more registers than the launch has would wait forever");
     static constexpr Room R = room_of(DK, DV, E, WARPS, MOST);
     static constexpr int MC = R.columns, QROW = R.q_row, STAGES = R.tiles, RING = STAGES * STAGE;
     static constexpr int SMEM = 1024 + RING + R.merge + R.q + R.weights + R.sums;
@@ -341,90 +347,6 @@ struct Walk {
     }
 };
 
-// What fills a group's ring: a walk that runs ahead of the computation, by the group's first warp.
-template <typename G>
-struct Feed {
-    Walk w;
-    bool more;
-    int at;                            // the group's next tile of the segment
-    int page, off;                     // lane i: page and first token in it of its tile first + i * groups
-    int first;
-
-    __device__ __forceinline__ void look(const Attn &a, int lane) {
-        first = at;
-        const int tile = at + lane * a.groups;
-        page = -1;
-        off = 0;
-        if (more && tile < w.end) {
-            const int slot = tile / a.tpp;
-            page = a.table[(size_t)w.b * a.max_pages + slot];
-            off = (tile - slot * a.tpp) * kTile;
-        }
-    }
-    __device__ __forceinline__ void start(const Attn &a, const Walk &run, bool any, int group, int lane) {
-        w = run;
-        more = any;
-        at = w.begin + group;
-        settle(a, group);
-        look(a, lane);
-    }
-    // on to a segment in which this group has a tile
-    __device__ __forceinline__ bool settle(const Attn &a, int group) {
-        bool moved = false;
-        while (more && at >= w.end) {
-            more = w.next(a);
-            at = w.begin + group;
-            moved = true;
-        }
-        return moved;
-    }
-    // the next tile into a stage; *none: it is in no page of the cache
-    __device__ __forceinline__ void issue(const Attn &a, const CUtensorMap *km, const CUtensorMap *vm, uint8_t *stage,
-                                          uint64_t *bar, uint8_t *none, int group, int lane) {
-        if (!more) return;
-        const int i = (at - first) / a.groups;
-        const int p = __shfl_sync(0xffffffffu, page, i), o = __shfl_sync(0xffffffffu, off, i);
-        if (lane == 0) {
-            const bool ok = (unsigned)p < (unsigned)a.n_pages;
-            *none = !ok;
-            if (!ok) {
-                *a.status = GDN_ERR_PAGE;
-                ptx::mbar_arrive(bar);
-            } else {
-                ptx::mbar_arrive_expect_tx(bar, G::STAGE);
-                const int h = w.j / a.n_rb;
-                auto pick = [&](int order) { return (order & 3) == 0 ? o : (order & 3) == 1 ? h : p; };
-                const int k1 = pick(a.k_order), k2 = pick(a.k_order >> 2), k3 = pick(a.k_order >> 4);
-                const int v1 = pick(a.v_order), v2 = pick(a.v_order >> 2), v3 = pick(a.v_order >> 4);
-#pragma unroll
-                for (int c = 0; c < G::KB / 2048; ++c)
-                    ptx::tma_load_4d(stage + c * 2048, km, bar, c * G::BOX, k1, k2, k3);
-#pragma unroll
-                for (int c = 0; c < G::VB / 2048; ++c)
-                    ptx::tma_load_4d(stage + G::KB + c * 2048, vm, bar, c * G::BOX, v1, v2, v3);
-            }
-        }
-        at += a.groups;
-        if (settle(a, group) || i == 31) look(a, lane);
-    }
-};
-
-// The warps of a group, which use one tile at a time together.
-struct Group {
-    int id, threads;                   // named barrier; 32: a warp by itself
-    __device__ __forceinline__ void sync() const {
-        if (threads == 32) __syncwarp();
-        else ptx::named_sync(id, threads);
-    }
-    __device__ __forceinline__ bool any(bool x) const {
-        if (threads == 32) return __any_sync(0xffffffffu, x);
-        int y;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
-                     "selp.s32 %0, 1, 0, q;\n\t}" : "=r"(y) : "r"((int)x), "r"(id), "r"(threads) : "memory");
-        return y != 0;
-    }
-};
-
 // One warp's share of one unit: an online softmax of 8 rows over tiles.
 template <typename T, int DK, int DV, typename G, bool COLS>
 struct Unit {
@@ -499,56 +421,61 @@ struct Unit {
         const int g = lane >> 2, t = lane & 3;
         if constexpr (MMA16) {
             const uint32_t row = k + (lane & 15) * 128, x = lane & 7, half = lane >> 4;
-            float s2[4];               // two chains of products
+            float d[4][4];             // four chains of products: one alone waits for each product's latency
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
                 uint32_t A[4];
                 ldsm4(A, row + (c >> 2) * 2048 + (((2 * (c & 3) + half) ^ x) << 4));
-                if (c == 0) mma0<T>(s, A, qf[c][0], qf[c][1]);
-                else if (c == 1) mma0<T>(s2, A, qf[c][0], qf[c][1]);
-                else if (c & 1) mma<T>(s2, A, qf[c][0], qf[c][1]);
-                else mma<T>(s, A, qf[c][0], qf[c][1]);
+                if (c < 4) mma0<T>(d[c], A, qf[c][0], qf[c][1]);
+                else mma<T>(d[c & 3], A, qf[c][0], qf[c][1]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += s2[e];
+            for (int e = 0; e < 4; ++e) s[e] = (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
         } else {
             // Lane (g, t) has elements 4t .. 4t + 3 of each 16 of tokens g and g + 8: the first two
             // are columns t and t + 4 of one k8 product, the others of the next (the queries' likewise).
             // Odd g read the second 16 of each 32 first, so that 8 lanes read 8 different pieces.
             const uint32_t ra = k + g * 128, x = g & 7, odd = g & 1;
             const uint8_t *q = sq + g * G::QROW + t * 16;
-            float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+            float d[6][4];             // chains of products: hi hi, lo hi, hi lo of the first and second 16
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = 0.f;
+            for (int n = 0; n < 6; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll 2
             for (int c = 0; c < DK / 32; ++c) {
                 const uint32_t p0 = ra + c * 2048 + (((t + 4 * odd) ^ x) << 4);
                 const uint32_t p1 = ra + c * 2048 + (((t + 4 * (odd ^ 1)) ^ x) << 4);
                 const uint4 u0 = lds16(p0), u1 = lds16(p1), v0 = lds16(p0 + 1024), v1 = lds16(p1 + 1024);
+                uint4 qh[2], ql[2];
+                uint32_t hi[2][2][4], lo[2][2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint4 u = h == (int)odd ? u0 : u1, v = h == (int)odd ? v0 : v1;
-                    const uint4 qh = *reinterpret_cast<const uint4 *>(q + c * 128 + h * 64);
-                    const uint4 ql = *reinterpret_cast<const uint4 *>(q + DK * 4 + c * 128 + h * 64);
-                    uint32_t hi[4], lo[4];
-                    split_tf32(__uint_as_float(u.x), hi[0], lo[0]);
-                    split_tf32(__uint_as_float(v.x), hi[1], lo[1]);
-                    split_tf32(__uint_as_float(u.y), hi[2], lo[2]);
-                    split_tf32(__uint_as_float(v.y), hi[3], lo[3]);
-                    mma<T>(s1, lo, qh.x, qh.y);
-                    mma<T>(s2, hi, ql.x, ql.y);
-                    mma<T>(s, hi, qh.x, qh.y);
-                    split_tf32(__uint_as_float(u.z), hi[0], lo[0]);
-                    split_tf32(__uint_as_float(v.z), hi[1], lo[1]);
-                    split_tf32(__uint_as_float(u.w), hi[2], lo[2]);
-                    split_tf32(__uint_as_float(v.w), hi[3], lo[3]);
-                    mma<T>(s1, lo, qh.z, qh.w);
-                    mma<T>(s2, hi, ql.z, ql.w);
-                    mma<T>(s, hi, qh.z, qh.w);
+                    qh[h] = *reinterpret_cast<const uint4 *>(q + c * 128 + h * 64);
+                    ql[h] = *reinterpret_cast<const uint4 *>(q + DK * 4 + c * 128 + h * 64);
+                    split_tf32(__uint_as_float(u.x), hi[h][0][0], lo[h][0][0]);
+                    split_tf32(__uint_as_float(v.x), hi[h][0][1], lo[h][0][1]);
+                    split_tf32(__uint_as_float(u.y), hi[h][0][2], lo[h][0][2]);
+                    split_tf32(__uint_as_float(v.y), hi[h][0][3], lo[h][0][3]);
+                    split_tf32(__uint_as_float(u.z), hi[h][1][0], lo[h][1][0]);
+                    split_tf32(__uint_as_float(v.z), hi[h][1][1], lo[h][1][1]);
+                    split_tf32(__uint_as_float(u.w), hi[h][1][2], lo[h][1][2]);
+                    split_tf32(__uint_as_float(v.w), hi[h][1][3], lo[h][1][3]);
                 }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t h0 = n ? qh[h].z : qh[h].x, h1 = n ? qh[h].w : qh[h].y;
+                        const uint32_t l0 = n ? ql[h].z : ql[h].x, l1 = n ? ql[h].w : ql[h].y;
+                        mma<T>(d[3 * h], hi[h][n], h0, h1);
+                        mma<T>(d[3 * h + 1], lo[h][n], h0, h1);
+                        mma<T>(d[3 * h + 2], hi[h][n], l0, l1);
+                    }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += s1[e] + s2[e];
+            for (int e = 0; e < 4; ++e) s[e] = ((d[1][e] + d[4][e]) + (d[2][e] + d[5][e])) + (d[0][e] + d[3][e]);
         }
     }
 
@@ -562,16 +489,10 @@ struct Unit {
     }
 
     // Values of tokens that some row must not see may be anything, infinities and NaN among them, and
-    // a weight of 0 does not silence those in a product.  Where such a tile has any, the rows that
-    // see them take them one by one, and the products take zeros for them.  (p: weights, x: scores.)
-    __device__ __forceinline__ void odd_values(const Group &grp, uint8_t *v, const float (&p)[4], const float (&x)[4],
-                                               float (&cf)[2], int lane) {
+    // a weight of 0 does not silence those in a product.  Where such a tile has any, its values are taken
+    // one by one by the rows that see them.  (p: weights, x: scores.)
+    __device__ __forceinline__ void odd_values(const uint8_t *v, const float (&p)[4], const float (&x)[4], int lane) {
         const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] *= cf[e & 1];
-        cf[0] = cf[1] = 1.f;
 #pragma unroll 1
         for (int tok = 0; tok < kTile; ++tok) {
             const int src = (tok & 7) * 4 + t;
@@ -586,17 +507,10 @@ struct Unit {
 #pragma unroll
                     for (int e = r; e < 4; e += 2) {
                         const float y = to_float<T>(*reinterpret_cast<const T *>(v + value_at(tok, element_of(i, e, g))));
-                        if (!isfinite(y)) o[i][e] = fmaf(w, y, o[i][e]);
+                        o[i][e] = fmaf(w, y, o[i][e]);
                     }
             }
         }
-        grp.sync();
-        for (int i = lane; i < kTile * DV; i += 32) {  // (every warp of the group alike)
-            T *y = reinterpret_cast<T *>(v + value_at(i / DV, i % DV));
-            if (!isfinite(to_float<T>(*y))) *y = T(0.f);
-        }
-        ptx::fence_proxy_async_smem();                 // (the next copy into this stage comes after these stores)
-        grp.sync();
     }
     __device__ __forceinline__ static bool any_odd(const uint8_t *v, int lane) {
         bool bad = false;
@@ -618,7 +532,7 @@ struct Unit {
     }
 
     // One tile or (U = 2) two: tokens pos[u] .. pos[u] + 15 of the sequence, in stage[u].
-    __device__ __forceinline__ void tiles(const Attn &a, const Group &grp, uint8_t *const (&stage)[U], const int (&pos)[U],
+    __device__ __forceinline__ void tiles(const Attn &a, uint8_t *const (&stage)[U], const int (&pos)[U],
                                           bool two, const uint8_t *sq, float *pt, int lane) {
         const int g = lane >> 2, t = lane & 3;
         float s[U][4], x[U][4], cf[2];
@@ -680,10 +594,14 @@ struct Unit {
             }
             l[r] = fmaf(l[r], cf[r], sum);
         }
-        if (!plain) {
+        if (!plain && (any_odd(stage[0] + G::KB, lane) || (U == 2 && two && any_odd(stage[U - 1] + G::KB, lane)))) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u == 0 || two) && any_odd(stage[u] + G::KB, lane)) odd_values(grp, stage[u] + G::KB, s[u], x[u], cf, lane);
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= cf[e & 1];
+            odd_values(stage[0] + G::KB, s[0], x[0], lane);
+            if (U == 2 && two) odd_values(stage[U - 1] + G::KB, s[U - 1], x[U - 1], lane);
+            return;
         }
         if constexpr (MMA16) {
             // Weights as 16-bit terms, largest first: two, and a third of bf16 where the outputs are fp32.  In
@@ -709,38 +627,40 @@ struct Unit {
                 }
             const uint32_t tok = (lane & 7) + ((lane >> 4) << 3);
             const uint32_t row = tok * 128 + G::KB, sw = lane & 7, half = (lane >> 3) & 1;
+            // four blocks of 16 elements at a time, whose products do not wait for one another
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const uint32_t at = row + (i >> 2) * 2048 + (((2 * (i & 3) + half) ^ sw) << 4);
-                uint32_t A[4];
-                float d[4];
-                ldsm4_t(A, ptx::smem_u32(stage[0]) + at);
-                if constexpr (COLS) {  // small terms first
-                    if (third) {
-                        mma0<T>(d, A, p2[0][0], p2[0][1]);
-                        mma<T>(d, A, p1[0][0], p1[0][1]);
-                    } else {
-                        mma0<T>(d, A, p1[0][0], p1[0][1]);
-                    }
-                } else {
-                    if (third) {
-                        mma0<T>(d, A, p3[0][0], p3[0][1]);
-                        mma<T>(d, A, p2[0][0], p2[0][1]);
-                    } else {
-                        mma0<T>(d, A, p2[0][0], p2[0][1]);
-                    }
-                    mma<T>(d, A, p1[0][0], p1[0][1]);
-                }
-                if constexpr (U == 2) {
-                    if (two) {
-                        ldsm4_t(A, ptx::smem_u32(stage[1]) + at);
-                        if (!COLS && third) mma<T>(d, A, p3[1][0], p3[1][1]);
-                        if (!COLS || third) mma<T>(d, A, p2[1][0], p2[1][1]);
-                        mma<T>(d, A, p1[1][0], p1[1][1]);
+            for (int i0 = 0; i0 < MT; i0 += 4) {
+                float d[4][4];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u == 1 && !two) break;
+                    uint32_t A[4][4];
+                    const uint32_t at = ptx::smem_u32(stage[u]) + row + (i0 >> 2) * 2048;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ldsm4_t(A[i], at + (((2 * i + half) ^ sw) << 4));
+                    // small terms first
+                    if (!COLS && third)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (u == 0) mma0<T>(d[i], A[i], p3[u][0], p3[u][1]);
+                            else mma<T>(d[i], A[i], p3[u][0], p3[u][1]);
+                        }
+                    if (!COLS || third)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (u == 0 && (COLS || !third)) mma0<T>(d[i], A[i], p2[u][0], p2[u][1]);
+                            else mma<T>(d[i], A[i], p2[u][0], p2[u][1]);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (u == 0 && COLS && !third) mma0<T>(d[i], A[i], p1[u][0], p1[u][1]);
+                        else mma<T>(d[i], A[i], p1[u][0], p1[u][1]);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] = fmaf(o[i][e], cf[e & 1], d[e]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i0 + i][e] = fmaf(o[i0 + i][e], cf[e & 1], d[i][e]);
             }
         } else {
             static_assert(MMA16 || U == 1, "one tile of fp32 rows at a time");
@@ -771,9 +691,9 @@ struct Unit {
                     const uint4 y = lds16(v + c * 2048 + tok * 128 + ((g ^ (tok & 7)) << 4));
                     w[n][0] = y.x; w[n][1] = y.y; w[n][2] = y.z; w[n][3] = y.w;
                 }
+                float d[2][2][4];      // of two M tiles: products of lo parts, and of hi ones
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float d[4];
                     uint32_t hi[2][4], lo[2][4];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
@@ -782,15 +702,17 @@ struct Unit {
                         split_tf32(__uint_as_float(w[2 * n + 1][2 * i]), hi[n][2], lo[n][2]);
                         split_tf32(__uint_as_float(w[2 * n + 1][2 * i + 1]), hi[n][3], lo[n][3]);
                     }
-                    mma0<T>(d, lo[0], ph[0], ph[1]);
-                    mma<T>(d, lo[1], ph[2], ph[3]);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) mma<T>(d, hi[n], pl[2 * n], pl[2 * n + 1]);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) mma<T>(d, hi[n], ph[2 * n], ph[2 * n + 1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[2 * c + i][e] = fmaf(o[2 * c + i][e], cf[e & 1], d[e]);
+                    mma0<T>(d[i][0], lo[0], ph[0], ph[1]);
+                    mma0<T>(d[i][1], hi[0], ph[0], ph[1]);
+                    mma<T>(d[i][0], lo[1], ph[2], ph[3]);
+                    mma<T>(d[i][1], hi[1], ph[2], ph[3]);
+                    mma<T>(d[i][0], hi[0], pl[0], pl[1]);
+                    mma<T>(d[i][0], hi[1], pl[2], pl[3]);
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[2 * c + i][e] = fmaf(o[2 * c + i][e], cf[e & 1], d[i][0][e] + d[i][1][e]);
             }
             __syncwarp();
         }
@@ -841,7 +763,7 @@ __device__ __forceinline__ long long out_row(const Attn &a, int b, int hk, int r
 }
 
 template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
-__global__ void __launch_bounds__(WARPS * 32, 1)
+__global__ void __launch_bounds__(WARPS * 32 + 32 * kFillers, 1)
 attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const Attn a) {
     using G = Geo<T, DK, DV, WARPS, MOST, U>;
     using Part = Unit<T, DK, DV, G, COLS>;
@@ -852,7 +774,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     float *pts = reinterpret_cast<float *>(sq + G::R.q);
     float *sm = reinterpret_cast<float *>(sq + G::R.q + G::R.weights);     // [WARPS][8] maxima, then the CTA's
     float *sl = sm + (WARPS + MOST) * kBlock;                              // ... and sums
-    __shared__ uint64_t full[G::STAGES];
+    __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
     __shared__ uint8_t none[G::STAGES];
     __shared__ int part[32], start[2], gave_up;
     __shared__ long long place[MOST * kBlock];
@@ -860,12 +782,13 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // groups of a.blocks warps (the warps left over only help to join)
     const int group = warp / a.blocks, block = warp - group * a.blocks;
-    const bool works = group < a.groups, leads = works && block == 0;
-    const Group grp{1 + group, 32 * a.blocks};
-    const int stages = min(G::STAGES / a.groups, 8);
+    const bool works = group < a.groups;
     if (tid == 0) {
         gave_up = 0;
-        for (int s = 0; s < G::STAGES; ++s) ptx::mbar_init(&full[s], 1);
+        for (int s = 0; s < G::STAGES; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], a.blocks);
+        }
         ptx::fence_mbar_init();
         if (a.n_pages) {
             ptx::prefetch_tmap(&km);
@@ -891,7 +814,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         __syncthreads();
     } else {
         cta = (int)blockIdx.x;
-        const int total = total_steps(a, part, G::THREADS);
+        const int total = total_steps(a, part, G::ALL);
         const int runs = runs_of(a, total);
         const int from = cta < runs ? run_begin(total, runs, cta) : 0;
         run.left = cta < runs ? run_begin(total, runs, cta + 1) - from : 0;
@@ -906,7 +829,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         // rows of empty sequences
         for (int b = cta; b < a.n_seqs; b += gridDim.x)
             if (tiles_at(a, b) == 0)
-                for (int i = tid; i < a.n_q * a.H * (DV / 4); i += G::THREADS)
+                for (int i = tid; i < a.n_q * a.H * (DV / 4); i += G::ALL)
                     store4(a.out, a.out_type, (size_t)b * a.n_q * a.H * DV + 4 * (size_t)i, make_float4(0.f, 0.f, 0.f, 0.f));
         __syncthreads();
         if (run.left > 0) {
@@ -918,35 +841,114 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         }
     }
 
-    const int slot0 = group * stages;  // the group's ring
-    float *pt = pts + (G::MMA16 ? 0 : warp * kBlock * 20);
-    Feed<G> feed;
-    if (leads) {
-        feed.start(a, run, any, group, lane);
-        for (int s = slot0; s < slot0 + stages; ++s)
-            feed.issue(a, &km, &vm, ring + s * G::STAGE, &full[s], &none[s], group, lane);
+    // ---- the last warps fill the ring with the run's tiles, each every kFillers-th of them (one alone would need
+    // 700 cycles a tile, twice what HBM does)
+    int s = 0;                         // a stage of the ring, and its phase
+    uint32_t phase = 0;
+    auto advance = [&](int by) {
+        s += by;
+        while (s >= a.ring) {
+            s -= a.ring;
+            phase ^= 1;
+        }
+        while (s < 0) {                // (a group whose last tiles in a segment were not there)
+            s += a.ring;
+            phase ^= 1;
+        }
+    };
+    if (warp >= WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::FILL_REGS));
+        const int who = warp - WARPS;  // stages who, who + kFillers, ...
+        s = who;
+        bool more = any && who < a.ring;
+        int skip = who;                // of the segment's tiles, before this warp's first
+        Walk w = run;
+        while (more) {
+            const int h = w.j / a.n_rb;
+            int tile = w.begin + skip;
+            while (more && tile < w.end) {
+                // lane i: page of tile first + i, and that tile's first token in it
+                const int first = tile;
+                int page = -1, off = 0;
+                if (first + lane < w.end) {
+                    const int slot = (first + lane) / a.tpp;
+                    page = a.table[(size_t)w.b * a.max_pages + slot];
+                    off = (first + lane - slot * a.tpp) * kTile;
+                }
+                while (tile < first + 32 && tile < w.end) {
+                    const int p = __shfl_sync(0xffffffffu, page, tile - first);
+                    const int y = __shfl_sync(0xffffffffu, off, tile - first);
+                    const bool came = ptx::mbar_wait(&empty[s], phase ^ 1, &gave_up);
+                    if (__any_sync(0xffffffffu, !came)) {
+                        gave_up = 1;
+                        *a.status = GDN_ERR_TIMEOUT;
+                        more = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const bool there = (unsigned)p < (unsigned)a.n_pages;
+                        none[s] = !there;
+                        if (!there) {
+                            *a.status = GDN_ERR_PAGE;
+                            ptx::mbar_arrive(&full[s]);
+                        } else {
+                            ptx::mbar_arrive_expect_tx(&full[s], G::STAGE);
+                            auto pick = [&](int x) { return (x & 3) == 0 ? y : (x & 3) == 1 ? h : p; };
+                            uint8_t *stage = ring + s * G::STAGE;
+                            const int k1 = pick(a.k_order), k2 = pick(a.k_order >> 2), k3 = pick(a.k_order >> 4);
+#pragma unroll
+                            for (int c = 0; c < G::KB / 2048; ++c)
+                                ptx::tma_load_4d(stage + c * 2048, &km, &full[s], c * G::BOX, k1, k2, k3);
+                            const int v1 = pick(a.v_order), v2 = pick(a.v_order >> 2), v3 = pick(a.v_order >> 4);
+#pragma unroll
+                            for (int c = 0; c < G::VB / 2048; ++c)
+                                ptx::tma_load_4d(stage + G::KB + c * 2048, &vm, &full[s], c * G::BOX, v1, v2, v3);
+                        }
+                    }
+                    // the next of this warp's stages, in this lap of the ring or the next
+                    if (s + kFillers < a.ring) {
+                        s += kFillers;
+                        tile += kFillers;
+                    } else {
+                        tile += a.ring - s + who;
+                        s = who;
+                        phase ^= 1;
+                    }
+                }
+            }
+            skip = tile - w.end;       // tiles go on in order over the segments
+            more = more && w.next(a);
+        }
+        if (a.cluster > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::WORK_REGS));
+    auto consumers_sync = [] { ptx::named_sync(1, G::THREADS); };
 
     // ---- segments
-    int s = 0;                         // the ring's next stage, and its phase
-    uint32_t phase = 0;
+    float *pt = pts + (G::MMA16 ? 0 : warp * kBlock * 20);
     bool dead = false;
     uint32_t next_q[Part::MMA16 ? Part::KS : 1][2];    // the next segment's queries, loaded while this one's parts join
     auto row0_of = [&](const Walk &w) { return w.j % a.n_rb * a.blocks * kBlock; };
     if (any || a.cluster) Part::load_queries(a, run.b, run.j / a.n_rb, row0_of(run) + block * kBlock, lane, next_q);
+    if (works) advance(group);         // s: where the group's next tile comes
     for (bool more = any || a.cluster; more;) {
         const int hk = run.j / a.n_rb, row0 = row0_of(run);
         Part u;
         if constexpr (G::R.q != 0) {
             Part::stage_queries(a, run.b, hk, row0, sq);
-            __syncthreads();
+            consumers_sync();
         }
 #pragma unroll
         for (int i = 0; i < (Part::MMA16 ? Part::KS : 1); ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) u.qf[i][e] = next_q[i][e];
         u.begin(a, run, row0 + block * kBlock, lane);
-        for (int tile = works ? run.begin + group : run.end; tile < run.end; tile += U * a.groups) {
+        int tile = run.begin + group;
+        while (works && tile < run.end) {
             const bool pair = U == 2 && tile + a.groups < run.end;
             uint8_t *stage[U];
             int at[U], pos[U];
@@ -954,18 +956,16 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
 #pragma unroll
             for (int x = 0; x < U; ++x) {
                 if (x == 1 && !pair) break;
-                at[x] = slot0 + s;
-                stage[x] = ring + at[x] * G::STAGE;
-                pos[x] = (tile + x * a.groups) * kTile;
-                if (!dead) came &= ptx::mbar_wait(&full[at[x]], phase, &gave_up);
-                there[x] = !none[at[x]];
-                if (++s == stages) {
-                    s = 0;
-                    phase ^= 1;
-                }
+                at[x] = s;
+                stage[x] = ring + s * G::STAGE;
+                pos[x] = tile * kTile;
+                if (!dead) came &= ptx::mbar_wait(&full[s], phase, &gave_up);
+                there[x] = !none[s];
+                advance(a.groups);
+                tile += a.groups;
             }
             if (!dead) {
-                dead = grp.any(!came); // (the same for all warps of a group: they meet at its barriers)
+                dead = __any_sync(0xffffffffu, !came);
                 if (dead) {
                     gave_up = 1;
                     *a.status = GDN_ERR_TIMEOUT;
@@ -985,15 +985,16 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                     two = false;
                 }
             }
-            if (one) u.tiles(a, grp, stage, pos, two, sq + block * kBlock * G::QROW, pt, lane);
-            grp.sync();
-            if (leads) {
+            if (one) u.tiles(a, stage, pos, two, sq + block * kBlock * G::QROW, pt, lane);
+            __syncwarp();
+            if (lane == 0) {
 #pragma unroll
                 for (int x = 0; x < U; ++x)
-                    if (x == 0 || pair)
-                        feed.issue(a, &km, &vm, ring + at[x] * G::STAGE, &full[at[x]], &none[at[x]], group, lane);
+                    if (x == 0 || pair) ptx::mbar_arrive(&empty[at[x]]);
             }
         }
+        // to the group's first tile of the next segment: tiles go on in order
+        if (works) advance(run.end - (tile - group));
         u.finish();
         Walk next = run;
         more = any && next.next(a);
@@ -1015,7 +1016,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                 sm[warp * kBlock + 2 * t + r] = u.m[r];
                 sl[warp * kBlock + 2 * t + r] = u.l[r];
             }
-        __syncthreads();               // (every group is done with the ring, too)
+        consumers_sync();               // (every group is done with the ring, too)
         // a thread a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output
         if (tid < valid) {
             float M = -INFINITY, L = 0.f;
@@ -1057,7 +1058,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
             }
             if (last && c0 + G::MC < DV) continue;
             const int from = last ? 0 : c0;
-            __syncthreads();
+            consumers_sync();
 #pragma unroll 1
             for (int x = tid; x < valid * (width / 4); x += G::THREADS) {
                 const int row = x / (width / 4), c = x - row * (width / 4);    // (a power of two)
@@ -1074,7 +1075,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                     *reinterpret_cast<float4 *>(parts + row * pitch + 4 * c) = y;
                 }
             }
-            if (!last) __syncthreads();
+            if (!last) consumers_sync();
         }
         if (a.cluster > 1) {           // ... and the CTAs': each takes its share of the rows' elements
             cluster_sync();
@@ -1182,6 +1183,10 @@ cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn 
     using G = Geo<T, DK, DV, WARPS, MOST, U>;
     static PerDeviceOnce setup;
     cudaError_t e = setup.run([] {
+        cudaFuncAttributes f;
+        const cudaError_t q = cudaFuncGetAttributes(&f, attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>);
+        if (q != cudaSuccess) return q;
+        if (f.numRegs < G::REGS) return cudaErrorInvalidConfiguration;   // (the split counts on them)
         return cudaFuncSetAttribute(attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
@@ -1194,7 +1199,7 @@ cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(G::THREADS);
+    cfg.blockDim = dim3(G::ALL);
     cfg.dynamicSmemBytes = G::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1209,14 +1214,13 @@ template <typename T, int DK, int DV>
 cudaError_t launch_rows(const CUtensorMap &km, const CUtensorMap &vm, const Attn &a, int grid, cudaStream_t stream) {
     constexpr int E = (int)sizeof(T);
     constexpr Share few = share_of(DK, DV, E, 1), many = share_of(DK, DV, E, kBlock + 1);
-    // two tiles at a time where registers and the groups' rings allow
-    constexpr int U = many.warps == 12 ? 2 : 1;
-    if (a.R > kBlock) return launch_one<T, DK, DV, many.warps, many.most, U, false>(km, vm, a, grid, stream);
-    if constexpr (E == 2) {
+    if constexpr (E == 4) {
+        if (a.R <= kBlock) return launch_one<T, DK, DV, few.warps, few.most, 1, false>(km, vm, a, grid, stream);
+    } else {
         // of at most 4 rows, the weights' second terms enter in the free columns of the same MMAs
-        if (a.R <= 4) return launch_one<T, DK, DV, few.warps, 1, 1, true>(km, vm, a, grid, stream);
+        if (a.R <= 4) return launch_one<T, DK, DV, few.warps, few.most, 1, true>(km, vm, a, grid, stream);
     }
-    return launch_one<T, DK, DV, few.warps, 1, 1, false>(km, vm, a, grid, stream);
+    return launch_one<T, DK, DV, many.warps, many.most, 1, false>(km, vm, a, grid, stream);
 }
 
 }  // namespace
