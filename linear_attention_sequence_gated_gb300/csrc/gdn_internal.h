@@ -103,6 +103,25 @@ int check_cache(const void *cache, const void *table, const void *lens, int n_se
                 int dv, int n_pages, int page_size, int max_pages, Span *span);
 }  // namespace kv4
 
+// Quotients by a number that the host knows, of 0 <= x < 2^31.  With 2^l >= d, m = ceil(2^(31 + l) / d) has 32
+// bits, and its excess times x is below 2^31: below 1 / d of the quotient's unit, which no
+// remainder reaches.
+struct Divisor {
+    uint32_t m, l;                     // l = 0: d = 1
+    static Divisor of(int d) {
+        Divisor r{0, 0};
+        if (d > 1) {
+            r.l = 1;
+            while ((1ll << r.l) < d) ++r.l;
+            r.m = (uint32_t)(((1ull << (31 + r.l)) + (unsigned)d - 1) / (unsigned)d);
+        }
+        return r;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int into(int x) const { return l ? (int)(__umulhi((uint32_t)x, m) >> (l - 1)) : x; }
+#endif
+};
+
 // Host-side argument checks shared by the C-ABI front ends.
 namespace host {
 

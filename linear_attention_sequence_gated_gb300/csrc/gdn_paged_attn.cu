@@ -111,7 +111,9 @@ struct Plan {
 };
 
 // CTAs a unit, or 0 for equal runs, by the room that the tables have (the lengths are on the device): what the
-// slowest CTA streams, in bytes, and for runs the second kernel's time as 128 KB more.
+// slowest CTA streams, in bytes, and the joins' time as bytes: a cluster's 2 us, a second kernel's and the scans' 7 us.
+// A cluster grows while each group of its CTAs has two tiles and more.
+constexpr long long kClusterCost = 96 << 10, kRunsCost = 320 << 10;
 bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int max_pages, int elt, Plan *p) {
     p->share = share_of(dk, dv, elt, H / Hkv * n_q);
     const long long units = (long long)n_seqs * Hkv * p->share.units, groups = p->share.groups;
@@ -120,10 +122,10 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     if (units > INT_MAX || steps > INT_MAX || (steps > 0 && units > INT_MAX / steps)) return false;
     const long long stage = (long long)kTile * (dk + dv) * elt;
     long long cl = 1;
-    while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * groups) cl *= 2;
+    while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * groups * 2) cl *= 2;
     const long long waves = (units * cl + kGrid - 1) / kGrid;
-    const long long by_cluster = waves * ((tiles + cl - 1) / cl) * stage;
-    const long long by_runs = (units * tiles + kGrid - 1) / kGrid * stage + (128 << 10);
+    const long long by_cluster = waves * ((tiles + cl - 1) / cl) * stage + (cl > 1 ? kClusterCost : 0);
+    const long long by_runs = (units * tiles + kGrid - 1) / kGrid * stage + kRunsCost;
     p->cluster = by_cluster <= by_runs ? (int)cl : 0;
     const long long runs = (units * steps + groups - 1) / groups;
     p->grid = p->cluster ? (int)(units * cl) : (int)(runs < kGrid ? runs : kGrid);
@@ -166,6 +168,7 @@ int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *
                          void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
     using namespace gdn::host;
     using namespace gdn::paged;
+    using gdn::Divisor;
     if (n_seqs < 0 || n_heads < 0 || n_heads_kv < 0 || n_q < 0 || n_pages < 0 || max_pages < 0) return GDN_ERR_ARG;
     if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F16) return GDN_ERR_ARG;
     if (out_dtype != GDN_DTYPE_F32 && out_dtype != GDN_DTYPE_BF16 && out_dtype != GDN_DTYPE_F16) return GDN_ERR_ARG;
@@ -261,6 +264,12 @@ int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *
     a.scale = scale;
     a.out_type = out_dtype;
     a.cluster = plan.cluster;
+    for (a.cluster_log = 0; (1 << a.cluster_log) < plan.cluster; ++a.cluster_log) {}
+    a.rep = n_heads / n_heads_kv;
+    a.by_q = Divisor::of(n_q);
+    a.by_rb = Divisor::of(plan.share.units);
+    a.by_tpp = Divisor::of(page_size / kTile);
+    a.by_units = Divisor::of(n_heads_kv * plan.share.units);
     a.causal = causal != 0;
     a.k_order = kl.order;
     a.v_order = vl.order;

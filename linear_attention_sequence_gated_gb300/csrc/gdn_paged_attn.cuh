@@ -59,7 +59,10 @@ struct Attn {
     int ring;                          // stages of the ring
     int n_pages, tpp, max_pages;       // tpp: tiles of a page
     float scale;
-    int out_type, cluster;             // CTAs a unit, or 0: equal runs
+    int out_type;
+    int cluster, cluster_log;          // CTAs a unit (a power of two), or 0: equal runs
+    int rep;                           // H / Hkv
+    Divisor by_q, by_rb, by_tpp, by_units;     // n_q, n_rb, tpp, units of a sequence
     bool causal;
     int k_order, v_order;              // of the tensor maps' outer coordinates: two bits each, 0 token, 1 head, 2 page
 };
@@ -83,8 +86,8 @@ constexpr Room room_of(int dk, int dv, int elt, int warps, int most) {
     r.q = elt == 2 ? 0 : most * kBlock * r.q_row;
     r.weights = elt == 2 ? 0 : warps * kBlock * 20 * 4;
     r.sums = 2 * (warps + most) * kBlock * 4;
-    // (1 KB for the ring's alignment, 1 KB for barriers and the like)
-    const int tiles = (kSmemMax - 2048 - r.merge - r.q - r.weights - r.sums) / (kTile * (dk + dv) * elt);
+    // (1 KB for the ring's alignment, 2 KB for barriers and the like)
+    const int tiles = (kSmemMax - 3072 - r.merge - r.q - r.weights - r.sums) / (kTile * (dk + dv) * elt);
     r.tiles = tiles < 48 ? tiles : 48;
     return r;
 }
@@ -364,8 +367,8 @@ struct Unit {
     int b;
 
     __device__ __forceinline__ static const T *q_row(const Attn &a, int b, int hk, int row) {
-        const int h = hk * (a.H / a.Hkv) + row / a.n_q, i = row % a.n_q;
-        return static_cast<const T *>(a.q) + b * a.q_seq + h * a.q_head + i * a.q_query;
+        const int h = a.by_q.into(row), i = row - h * a.n_q;
+        return static_cast<const T *>(a.q) + b * a.q_seq + (hk * a.rep + h) * a.q_head + i * a.q_query;
     }
 
     // fp32 queries of the unit's blocks to shared memory, by the whole CTA (a barrier follows).
@@ -406,7 +409,7 @@ struct Unit {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = COLS ? (2 * t + r) & 3 : row0 + 2 * t + r;
-            qi[r] = row < a.R ? row % a.n_q : -1;
+            qi[r] = row < a.R ? row - a.by_q.into(row) * a.n_q : -1;
             m[r] = -INFINITY;
             l[r] = 0.f;
         }
@@ -513,7 +516,10 @@ struct Unit {
         }
     }
     __device__ __forceinline__ static bool any_odd(const uint8_t *v, int lane) {
-        bool bad = false;
+        // 0 times what is not finite is NaN
+        using T2 = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+        float acc = 0.f;
+        uint32_t acc2 = 0;
 #pragma unroll 4
         for (int i = 0; i < G::VB / 512; ++i) {
             const uint4 w = *reinterpret_cast<const uint4 *>(v + (i * 32 + lane) * 16);
@@ -521,22 +527,36 @@ struct Unit {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (MMA16) {
-                    constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
-                    bad |= (u[e] & INF) == INF || (u[e] >> 16 & INF) == INF;
+                    const uint32_t zero = 0;
+                    const T2 r = __hfma2(*reinterpret_cast<const T2 *>(&u[e]), *reinterpret_cast<const T2 *>(&zero),
+                                         *reinterpret_cast<const T2 *>(&acc2));
+                    acc2 = *reinterpret_cast<const uint32_t *>(&r);
                 } else {
-                    bad |= (u[e] & 0x7f800000u) == 0x7f800000u;
+                    acc = fmaf(__uint_as_float(u[e]), 0.f, acc);
                 }
             }
         }
-        return __any_sync(0xffffffffu, bad);
+        return __any_sync(0xffffffffu, MMA16 ? (acc2 & 0x7fff7fffu) != 0 : acc != acc);
     }
 
     // One tile or (U = 2) two: tokens pos[u] .. pos[u] + 15 of the sequence, in stage[u].
     __device__ __forceinline__ void tiles(const Attn &a, uint8_t *const (&stage)[U], const int (&pos)[U],
                                           bool two, const uint8_t *sq, float *pt, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        float s[U][4], x[U][4], cf[2];
+        float s[U][4], x[U][4], cf[2], add[U][4];
         bool plain = true;
+        if (a.mask) {                  // loaded ahead of the products
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = qi[e & 1], j = pos[u] + g + 8 * (e >> 1);
+                    add[u][e] = -INFINITY;
+                    if ((u == 0 || two) && i >= 0 && j < len)
+                        add[u][e] = to_float<T>(
+                            static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j]);
+                }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u == 0 || two) {
@@ -560,9 +580,7 @@ struct Unit {
                         if (i < 0 || j >= lim) {
                             x[u][e] = -INFINITY;
                         } else if (a.mask) {
-                            const float add = to_float<T>(
-                                static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j]);
-                            x[u][e] = add == -INFINITY ? add : x[u][e] + add;
+                            x[u][e] = add[u][e] == -INFINITY ? -INFINITY : x[u][e] + add[u][e];
                         }
                     }
                 }
@@ -756,10 +774,22 @@ __device__ __forceinline__ float4 fma4(float w, float4 x, float4 y) {
     return make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
 }
 
+// Over the 16 lanes of half a warp
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+    return x;
+}
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
 // Which row of the output, (n_seqs, n_q, n_heads), belongs to row `row` of (b, hk)
 __device__ __forceinline__ long long out_row(const Attn &a, int b, int hk, int row) {
-    const int h = row / a.n_q, i = row - h * a.n_q;
-    return ((long long)b * a.n_q + i) * a.H + hk * (a.H / a.Hkv) + h;
+    const int h = a.by_q.into(row), i = row - h * a.n_q;
+    return ((long long)b * a.n_q + i) * a.H + hk * a.rep + h;
 }
 
 template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
@@ -778,6 +808,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     __shared__ uint8_t none[G::STAGES];
     __shared__ int part[32], start[2], gave_up;
     __shared__ long long place[MOST * kBlock];
+    __shared__ float shares[kMaxCluster][MOST * kBlock];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // groups of a.blocks warps (the warps left over only help to join)
@@ -802,14 +833,14 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     int rank = 0, cta = 0;
     bool any = false;
     if (a.cluster) {
-        rank = (int)(blockIdx.x % (unsigned)a.cluster);
-        const int unit = (int)(blockIdx.x / (unsigned)a.cluster);
-        run.b = unit / units_of(a);
+        rank = (int)(blockIdx.x & (unsigned)(a.cluster - 1));
+        const int unit = (int)(blockIdx.x >> a.cluster_log);
+        run.b = a.by_units.into(unit);
         run.j = unit - run.b * units_of(a);
         run.set(a);
         if (tid == 0 && run.raw > capacity(a)) *a.status = GDN_ERR_PAGE;
-        run.begin = (int)((long long)run.n * rank / a.cluster);
-        run.end = (int)((long long)run.n * (rank + 1) / a.cluster);
+        run.begin = run.n * rank >> a.cluster_log;     // (below 2^30: a length has 2^27 tiles at most)
+        run.end = run.n * (rank + 1) >> a.cluster_log;
         any = run.begin < run.end;
         __syncthreads();
     } else {
@@ -864,14 +895,14 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         int skip = who;                // of the segment's tiles, before this warp's first
         Walk w = run;
         while (more) {
-            const int h = w.j / a.n_rb;
+            const int h = a.by_rb.into(w.j);
             int tile = w.begin + skip;
             while (more && tile < w.end) {
                 // lane i: page of tile first + i, and that tile's first token in it
                 const int first = tile;
                 int page = -1, off = 0;
                 if (first + lane < w.end) {
-                    const int slot = (first + lane) / a.tpp;
+                    const int slot = a.by_tpp.into(first + lane);
                     page = a.table[(size_t)w.b * a.max_pages + slot];
                     off = (first + lane - slot * a.tpp) * kTile;
                 }
@@ -932,11 +963,11 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     float *pt = pts + (G::MMA16 ? 0 : warp * kBlock * 20);
     bool dead = false;
     uint32_t next_q[Part::MMA16 ? Part::KS : 1][2];    // the next segment's queries, loaded while this one's parts join
-    auto row0_of = [&](const Walk &w) { return w.j % a.n_rb * a.blocks * kBlock; };
-    if (any || a.cluster) Part::load_queries(a, run.b, run.j / a.n_rb, row0_of(run) + block * kBlock, lane, next_q);
+    auto row0_of = [&](const Walk &w) { return (w.j - a.by_rb.into(w.j) * a.n_rb) * a.blocks * kBlock; };
+    if (any || a.cluster) Part::load_queries(a, run.b, a.by_rb.into(run.j), row0_of(run) + block * kBlock, lane, next_q);
     if (works) advance(group);         // s: where the group's next tile comes
     for (bool more = any || a.cluster; more;) {
-        const int hk = run.j / a.n_rb, row0 = row0_of(run);
+        const int hk = a.by_rb.into(run.j), row0 = row0_of(run);
         Part u;
         if constexpr (G::R.q != 0) {
             Part::stage_queries(a, run.b, hk, row0, sq);
@@ -998,7 +1029,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         u.finish();
         Walk next = run;
         more = any && next.next(a);
-        if (more) Part::load_queries(a, next.b, next.j / a.n_rb, row0_of(next) + block * kBlock, lane, next_q);
+        if (more) Part::load_queries(a, next.b, a.by_rb.into(next.j), row0_of(next) + block * kBlock, lane, next_q);
 
         // ---- the groups' parts of the segment join: MC columns at a time, or, when no more tiles come, all of
         // them in the ring
@@ -1017,34 +1048,25 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                 sl[warp * kBlock + 2 * t + r] = u.l[r];
             }
         consumers_sync();               // (every group is done with the ring, too)
-        // a thread a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output
-        if (tid < valid) {
-            float M = -INFINITY, L = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-                if (w < a.groups) M = fmaxf(M, sm[w * rows + tid]);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-                if (w < a.groups) {
-                    const float lw = sl[w * rows + tid];
-                    // (a part of NaN scores has no maximum: the row is NaN)
-                    const float f = lw == lw ? weight(sm[w * rows + tid], M) : lw;
-                    L = fmaf(f, lw, L);
-                    sm[w * rows + tid] = f;
+        // half a warp a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output
+        for (int row = tid >> 4; row < (valid + 1) / 2 * 2; row += G::THREADS / 16) {
+            const int w = tid & 15;
+            const float mw = w < a.groups && row < valid ? sm[w * rows + row] : -INFINITY;
+            const float lw = w < a.groups && row < valid ? sl[w * rows + row] : 0.f;
+            const float M = max16(mw);
+            // (a part of NaN scores has no maximum: the row is NaN)
+            const float f = lw == lw ? weight(mw, M) : lw, L = sum16(f * lw);
+            if (row < valid) {
+                if (w < a.groups) sm[w * rows + row] = !final ? f : L == 0.f ? 0.f : f * __frcp_rn(L);
+                if (w == 15) place[row] = row0 + row < a.R ? out_row(a, run.b, hk, row0 + row) : -1;
+                if (w == 0 && part_out) {
+                    part_out[rows * DV + row] = M;
+                    part_out[rows * (DV + 1) + row] = L;
+                } else if (w == 0) {
+                    sm[WARPS * kBlock + row] = M;
+                    sl[WARPS * kBlock + row] = L;
                 }
-            if (final) {
-                const float f = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w)
-                    if (w < a.groups) sm[w * rows + tid] *= f;
-            } else if (part_out) {
-                part_out[rows * DV + tid] = M;
-                part_out[rows * (DV + 1) + tid] = L;
-            } else {
-                sm[WARPS * kBlock + tid] = M;
-                sl[WARPS * kBlock + tid] = L;
             }
-            place[tid] = row0 + tid < a.R ? out_row(a, run.b, hk, row0 + tid) : -1;
         }
 #pragma unroll
         for (int c0 = 0; c0 < DV; c0 += G::MC) {
@@ -1080,31 +1102,23 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         if (a.cluster > 1) {           // ... and the CTAs': each takes its share of the rows' elements
             cluster_sync();
             // (a CTA whose waits gave up has joined them elsewhere: the outputs are lost, the status says so)
+            for (int row = tid >> 4; row < (valid + 1) / 2 * 2; row += G::THREADS / 16) {
+                const int p = tid & 15;
+                const bool there = p < a.cluster && row < valid;
+                const float mp = there ? peer_float(sm + WARPS * kBlock + row, p) : -INFINITY;
+                const float lp = there ? peer_float(sl + WARPS * kBlock + row, p) : 0.f;
+                const float M = max16(mp);
+                const float f = lp == lp ? weight(mp, M) : lp, L = sum16(f * lp);
+                if (there) shares[p][row] = L == 0.f ? 0.f : f * __frcp_rn(L);
+            }
+            consumers_sync();
             for (int x = rank * G::THREADS + tid; x < valid * (DV / 4); x += a.cluster * G::THREADS) {
                 const int row = x / (DV / 4), c = x - row * (DV / 4);
-                float mk[kMaxCluster], lk[kMaxCluster], M = -INFINITY, L = 0.f;
-                float4 yk[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int p = 0; p < kMaxCluster; ++p) {
-                    const int q = p < a.cluster ? p : 0;
-                    mk[p] = peer_float(sm + WARPS * kBlock + row, q);
-                    lk[p] = peer_float(sl + WARPS * kBlock + row, q);
-                    yk[p] = peer_float4(reinterpret_cast<float *>(ring) + row * (DV + 4) + 4 * c, q);
-                }
-#pragma unroll
-                for (int p = 0; p < kMaxCluster; ++p)
-                    if (p < a.cluster) M = fmaxf(M, mk[p]);
-#pragma unroll
-                for (int p = 0; p < kMaxCluster; ++p) {
-                    const float f = lk[p] == lk[p] ? weight(mk[p], M) : lk[p];
-                    if (p < a.cluster) {
-                        L = fmaf(f, lk[p], L);
-                        y = fma4(f, yk[p], y);
-                    }
-                }
-                const float f = L == 0.f ? 0.f : 1.f / L;
-                if (place[row] >= 0)
-                    store4(a.out, a.out_type, (size_t)place[row] * DV + 4 * c, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int p = 0; p < a.cluster; ++p)
+                    y = fma4(shares[p][row], peer_float4(reinterpret_cast<float *>(ring) + row * (DV + 4) + 4 * c, p), y);
+                if (place[row] >= 0) store4(a.out, a.out_type, (size_t)place[row] * DV + 4 * c, y);
             }
             cluster_sync();            // peers are done reading
         }
@@ -1142,7 +1156,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
     if (cut <= first) return;
     const int r0 = run_of(total, runs, first), r1 = run_of(total, runs, first + n - 1);
     if (c != r0 + 1) return;
-    const int hk = j / a.n_rb, rb = j - hk * a.n_rb, parts = r1 - r0 + 1;
+    const int hk = a.by_rb.into(j), rb = j - hk * a.n_rb, parts = r1 - r0 + 1;
     const int group = tid / COLS4, col = tid - group * COLS4;
     // part p: of run r0 + p; the unit begins in run r0
     auto at = [&](int p) { return a.ws + partial_slot(r0 + p, p == 0) * partial_size(rows, DV); };
@@ -1170,7 +1184,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
                 y = fma4(1.f, sums[k * COLS4 + col], y);
                 L += sums_l[k];
             }
-            const float f = L == 0.f ? 0.f : 1.f / L;
+            const float f = L == 0.f ? 0.f : __frcp_rn(L);
             store4(a.out, a.out_type, (size_t)out_row(a, b, hk, rb * rows + row) * DV + 4 * col,
                    make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
         }

@@ -38,7 +38,7 @@ struct Step {
     int *slots, *positions, *offsets;
     int *status;
     int n_seqs, n_new, n_tokens, page, max_pages, n_pages;
-    uint32_t magic, shift;             // p / page = umulhi(p, magic) >> shift
+    Divisor by_page;
     bool packed;
 };
 
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const Step s) {
             if (b < s.n_seqs) q = seq_of(s, b, &past);
         }
         const int p = i - base < q.n ? q.first + i - base : -1;
-        const int j = p < 0 ? s.max_pages : (int)(s.page == 1 ? (uint32_t)p : __umulhi((uint32_t)p, s.magic) >> s.shift);
+        const int j = p < 0 ? s.max_pages : s.by_page.into(p);
         int slot = -1, pos = 0;
         if (j < s.max_pages) {
             const int page = j < q.held ? s.table[(size_t)b * s.max_pages + j] : page_at(pg[b] + j - q.held);
@@ -386,17 +386,8 @@ int gdn_page_assign(int *page_table, const int *seq_lens, const int *new_lens, c
     }
     int *status = gdn::status_word();
     if (!status || opt_in() != GDN_OK) return GDN_ERR_CUDA;
-    // p / page for 0 <= p < 2^31: with 2^l >= page, ceil(2^(31 + l) / page) has 32 bits, and its excess times p is
-    // below 2^31, 1 / page of the quotient's unit at most
-    uint32_t magic = 0, shift = 0;
-    if (page_size > 1) {
-        int l = 1;
-        while ((1ll << l) < page_size) ++l;
-        magic = (uint32_t)(((1ull << (31 + l)) + (unsigned)page_size - 1) / (unsigned)page_size);
-        shift = (uint32_t)(l - 1);
-    }
     const Step s{page_table, seq_lens, new_lens, free_pages, free_count, slots, positions, token_offsets, status,
-                 n_seqs, n_new, n_tokens, page_size, max_pages, n_pages, magic, shift, packed};
+                 n_seqs, n_new, n_tokens, page_size, max_pages, n_pages, gdn::Divisor::of(page_size), packed};
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // a thread takes two tokens or more before there are more CTAs
     const long long work = items + n_seqs;

@@ -278,6 +278,16 @@ def test_uneven_batches_and_runs(dtype, n_q):
         c.check(causal=n_q == 3)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 256), (64, 256), (256, 128), (128, 64), (64, 128),
+                                   (128, 256), (256, 64)])
+@pytest.mark.parametrize("H", [4, 6, 20, 33])
+def test_many_laps_of_the_ring(dtype, dk, dv, H):
+    """Tiles enough for hundreds of uses of every stage, in runs and in clusters, of 1 to 5 blocks of rows."""
+    Case([16000, 5, 9100], H, 1, 1, dk, dv, page=64, dtype=dtype, seed=dk + dv + H).check()
+    Case([1900] * 40, H, 1, 1, dk, dv, page=256, dtype=dtype, seed=H).check()
+
+
 @pytest.mark.parametrize("lens,room", [([7000, 300], 0), ([300, 3, 0], 2000), ([20000], 0)])
 def test_one_call_is_the_next(lens, room):
     """Results do not depend on timing: the same bits again, and with a workspace of the caller's."""

@@ -8,6 +8,7 @@ import ctypes
 import math
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -17,6 +18,7 @@ from linear_attention_sequence_gated_gb300 import _build
 from oracle import paged
 from oracle.attn import attention
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BASE, MB = 1 << 40, 1 << 20
 ptr = lambda x: None if x is None else ctypes.c_void_p(x)  # noqa: E731
 host = lambda x: None if x is None else (ctypes.c_longlong * len(x))(*x)  # noqa: E731
@@ -105,6 +107,40 @@ def test_plan_deals_axes_and_refuses():
     assert gdn.lib().gdn_rotary_plan(None, None, 0, None) == gdn.OK
     neg = (ctypes.c_int * 1)(-1)
     assert gdn.lib().gdn_rotary_plan((ctypes.c_double * 1)(1.0), neg, 1, (ctypes.c_int * 4)()) == gdn.ERR_ARG
+
+
+# ------------------------------------------------------------ how attention is shared out
+
+@pytest.fixture(scope="module")
+def H(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("paged") / "paged_host.so")
+    subprocess.check_call([_build.nvcc()] + _build.ARCH + ["-std=c++17", "--expt-relaxed-constexpr", "-shared", "-Xcompiler", "-fPIC",
+                                                          "-o", so, os.path.join(ROOT, "tests", "paged_host.cu")])
+    return ctypes.CDLL(so)
+
+
+@pytest.mark.parametrize("elt", [2, 4])
+@pytest.mark.parametrize("dk", [64, 128, 256])
+@pytest.mark.parametrize("dv", [64, 128, 256])
+def test_rings_are_a_whole_number_of_tiles_a_group(H, elt, dk, dv):
+    """A barrier's parity tells a phase from the next only, so a stage belongs to one group; and all rows have a block."""
+    out = (ctypes.c_int * 7)()
+    for R in list(range(1, 200)) + [760, 5000]:
+        H.paged_share(dk, dv, elt, R, out)
+        warps, most, blocks, groups, units, ring, tiles = out
+        assert ring % groups == 0 and groups <= ring <= tiles and 1 <= groups * blocks <= warps
+        assert blocks <= most and 8 * blocks * units >= R and 8 * blocks * (units - 1) < R
+        assert (3 << 10) + tiles * 16 * (dk + dv) * elt <= 227 << 10
+
+
+def test_quotients_by_a_known_number(H):
+    rng = np.random.default_rng(3)
+    for d in list(range(1, 300)) + [2 ** k + e for k in range(9, 31) for e in (-1, 0, 1)] + [2 ** 31 - 1]:
+        x = np.unique(np.concatenate([[0, 1, d - 1, min(d, 2 ** 31 - 1), 2 ** 31 - 1], rng.integers(0, 2 ** 31, 50),
+                                      np.minimum(rng.integers(0, 2 ** 31 // d + 1, 50) * d, 2 ** 31 - 1)])).astype(np.int32)
+        got = np.zeros_like(x)
+        H.paged_quotients(d, ctypes.c_void_p(x.ctypes.data), x.size, ctypes.c_void_p(got.ctypes.data))
+        assert np.array_equal(got, x // d)
 
 
 # ------------------------------------------------------------ refusals
@@ -330,8 +366,7 @@ def test_binding_refuses():
 
 # ------------------------------------------------------------ the sources
 
-CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
-                    "linear_attention_sequence_gated_gb300", "csrc")
+CSRC = os.path.join(ROOT, "linear_attention_sequence_gated_gb300", "csrc")
 
 
 @pytest.mark.parametrize("name", ["gdn_pages.cu", "gdn_paged.cu", "gdn_paged_attn.cuh"])
@@ -343,5 +378,6 @@ def test_kernels_that_start_early_read_with_ordinary_loads(name):
     assert not re.findall(r"\b__ld(?:g|cg|ca|cs|lu|cv)\s*\(", text)
     assert not re.findall(r"ld\.global(?:\.\w+)*\.nc", text)
     assert len(re.findall(r"__global__", text)) == len(re.findall(r"after_the_kernel_before\(\);", text))
-    for init in re.finditer(r"\bmbar_init\s*\(", text):      # the thread that initialises barriers fences them
-        assert "fence_mbar_init()" in text[init.start():text.index("}", init.start())]
+    # the thread that initialises barriers fences them: in its condition's block, behind the loop at most
+    for init in re.finditer(r"\bmbar_init\s*\(", text):
+        assert re.match(r"[^{}]*(?:\}\s*)?ptx::fence_mbar_init\(\);", text[init.start():]), text[init.start():][:200]
