@@ -130,7 +130,8 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     const long long runs = (units * steps + groups - 1) / groups;
     p->grid = p->cluster ? (int)(units * cl) : (int)(runs < kGrid ? runs : kGrid);
     p->bytes = p->cluster || p->grid < 2 ? 0
-                                         : (size_t)2 * p->grid * p->share.blocks * kBlock * (dv + 2) * sizeof(float);
+                                         : p->grid * (2 * partial_size(p->share.blocks * kBlock, dv) * sizeof(float) +
+                                                      sizeof(int) * 4);
     return units * cl <= INT_MAX;
 }
 

@@ -114,6 +114,10 @@ constexpr Share share_of(int dk, int dv, int elt, int R) {
     return {warps, most, blocks, groups, units, tiles - tiles % groups};
 }
 
+// A run that covers a unit in part leaves a partial result in the workspace: [rows][dv] outputs, [rows] maxima,
+// [rows] sums, so many floats.
+__host__ __device__ inline size_t partial_size(int rows, int dv) { return (size_t)rows * (dv + 2); }
+
 // The kernel for rows of type T and keys of width DK (one translation unit each).
 template <typename T, int DK>
 cudaError_t launch_attn(int dv, const CUtensorMap &km, const CUtensorMap &vm, const Attn &a, int grid,
@@ -268,8 +272,13 @@ __device__ __forceinline__ int tiles_at(const Attn &a, int b) {
 }
 __device__ __forceinline__ int units_of(const Attn &a) { return a.Hkv * a.n_rb; }     // of a sequence
 
-// A partial result: [rows][DV] outputs, [rows] maxima, [rows] sums.
-__device__ __forceinline__ size_t partial_size(int rows, int dv) { return (size_t)rows * (dv + 2); }
+// Behind the partial results of all runs: which unit a run leaves to those after it, and in how many parts it lies.
+struct Open {
+    int b, j, parts, unused;
+};
+__device__ __forceinline__ Open *open_of(const Attn &a, int grid, int dv) {
+    return reinterpret_cast<Open *>(a.ws + 2 * grid * partial_size(a.blocks * kBlock, dv));
+}
 
 // Sum of x over the block, in every thread; `part` is 32 ints, free again after the next barrier.
 __device__ __forceinline__ int block_sum(int x, int *part, int warps) {
@@ -278,6 +287,16 @@ __device__ __forceinline__ int block_sum(int x, int *part, int warps) {
     __syncthreads();
     const int lane = threadIdx.x & 31;
     return __reduce_add_sync(0xffffffffu, lane < warps ? part[lane] : 0);
+}
+
+// Sum of x over this lane and those before it.
+__device__ __forceinline__ int warp_sum(int x, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += o;
+    }
+    return x;
 }
 
 // Steps of a unit of n tiles: the first kUnitCost stand for its beginning and end.
@@ -298,13 +317,7 @@ __device__ __forceinline__ int find_step(const Attn &a, int x, int lane, int *be
     int done = 0;
     for (int base = 0;; base += 32) {
         const int n = base + lane < a.n_seqs ? steps_of(tiles_at(a, base + lane)) * units_of(a) : 0;
-        int incl = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
-        }
-        incl += done;
+        const int incl = done + warp_sum(n, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, incl > x);
         if (hit || base + 32 >= a.n_seqs) {            // (x is below the total, so there is one)
             const int src = hit ? __ffs(hit) - 1 : 31;
@@ -830,7 +843,8 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
 
     // ---- this CTA's run
     Walk run{0, 0, 0, 0, 0, 0, 0, 0, 0};
-    int rank = 0, cta = 0;
+    int rank = 0, cta = 0, total = 0, runs = 0;
+    unsigned empty_seqs = 0;           // of up to 32
     bool any = false;
     if (a.cluster) {
         rank = (int)(blockIdx.x & (unsigned)(a.cluster - 1));
@@ -845,33 +859,51 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         __syncthreads();
     } else {
         cta = (int)blockIdx.x;
-        const int total = total_steps(a, part, G::ALL);
-        const int runs = runs_of(a, total);
-        const int from = cta < runs ? run_begin(total, runs, cta) : 0;
-        run.left = cta < runs ? run_begin(total, runs, cta + 1) - from : 0;
-        if (warp == 0 && run.left > 0) {
-            int before;
-            const int b = find_step(a, from, lane, &before);
-            if (lane == 0) {
-                start[0] = b;
-                start[1] = from - before;
+        if (a.n_seqs <= 32) {          // each warp by itself, with one look at the lengths
+            const int raw = lane < a.n_seqs ? max(a.lens[lane], 0) : 0;
+            const int n = (min(raw, capacity(a)) + kTile - 1) / kTile, steps = steps_of(n) * units_of(a);
+            if (warp == 0 && raw > capacity(a)) *a.status = GDN_ERR_PAGE;
+            const int incl = warp_sum(steps, lane);
+            total = __shfl_sync(0xffffffffu, incl, 31);
+            runs = runs_of(a, total);
+            const int from = cta < runs ? run_begin(total, runs, cta) : total;
+            run.left = cta < runs ? run_begin(total, runs, cta + 1) - from : 0;
+            const int src = __ffs(__ballot_sync(0xffffffffu, incl > from)) - 1;
+            if (run.left > 0) {
+                run.b = src;
+                run.from = from - __shfl_sync(0xffffffffu, incl - steps, src);
+                run.n = __shfl_sync(0xffffffffu, n, src);
+                run.raw = __shfl_sync(0xffffffffu, raw, src);
+            }
+            empty_seqs = __ballot_sync(0xffffffffu, lane < a.n_seqs && n == 0);
+            __syncthreads();
+        } else {
+            total = total_steps(a, part, G::ALL);
+            runs = runs_of(a, total);
+            const int from = cta < runs ? run_begin(total, runs, cta) : total;
+            run.left = cta < runs ? run_begin(total, runs, cta + 1) - from : 0;
+            if (warp == 0 && run.left > 0) {
+                int before;
+                const int b = find_step(a, from, lane, &before);
+                if (lane == 0) {
+                    start[0] = b;
+                    start[1] = from - before;
+                }
+            }
+            __syncthreads();
+            if (run.left > 0) {
+                run.b = start[0];
+                run.from = start[1];
+                run.set(a);
             }
         }
-        // rows of empty sequences
-        for (int b = cta; b < a.n_seqs; b += gridDim.x)
-            if (tiles_at(a, b) == 0)
-                for (int i = tid; i < a.n_q * a.H * (DV / 4); i += G::ALL)
-                    store4(a.out, a.out_type, (size_t)b * a.n_q * a.H * DV + 4 * (size_t)i, make_float4(0.f, 0.f, 0.f, 0.f));
-        __syncthreads();
         if (run.left > 0) {
-            run.b = start[0];
-            run.set(a);
-            run.j = start[1] / steps_of(run.n);
-            run.from = start[1] - run.j * steps_of(run.n);
+            run.j = run.from / steps_of(run.n);
+            run.from -= run.j * steps_of(run.n);
             any = run.cut();
         }
+        if (tid == 0 && gridDim.x > 1) open_of(a, gridDim.x, DV)[cta].parts = 0;
     }
-
     // ---- the last warps fill the ring with the run's tiles, each every kFillers-th of them (one alone would need
     // 700 cycles a tile, twice what HBM does)
     int s = 0;                         // a stage of the ring, and its phase
@@ -957,6 +989,11 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::WORK_REGS));
+    if (!a.cluster)                    // rows of empty sequences
+        for (int b = cta; b < a.n_seqs; b += gridDim.x)
+            if (a.n_seqs <= 32 ? empty_seqs >> b & 1 : tiles_at(a, b) == 0)
+                for (int i = tid; i < a.n_q * a.H * (DV / 4); i += G::THREADS)
+                    store4(a.out, a.out_type, (size_t)b * a.n_q * a.H * DV + 4 * (size_t)i, make_float4(0.f, 0.f, 0.f, 0.f));
     auto consumers_sync = [] { ptx::named_sync(1, G::THREADS); };
 
     // ---- segments
@@ -1039,6 +1076,10 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         const bool last = !more && !dead, final = whole && a.cluster < 2;
         float *part_out = whole || a.cluster ? nullptr
                                              : a.ws + partial_slot(cta, run.begin == 0) * partial_size(rows, DV);
+        if (part_out && run.begin == 0 && tid == 0) {  // the runs up to that of the unit's last step go on with it
+            const int end = run_begin(total, runs, cta + 1) + run.n + kUnitCost - run.to;
+            open_of(a, gridDim.x, DV)[cta] = {run.b, run.j, run_of(total, runs, end - 1) - cta + 1, 0};
+        }
         const int width = last ? DV : G::MC, pitch = width + 4;
         float *parts = last ? reinterpret_cast<float *>(ring) : merge;
         if (g == 0 && mine)
@@ -1126,66 +1167,53 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     }
 }
 
-// Joins the parts of units that runs cut: block (c - 1, y) is for the unit that the boundary between runs c - 1
-// and c cuts, if it is the first to cut it, and rows y, y + gridDim.y, ... of it.
+// Joins the parts of units that runs cut: block (c, y) is for the unit that run c leaves open, and rows y, y +
+// gridDim.y, ... of it.  Groups of threads take parts in turn, each with its own running maximum.
 constexpr int kJoinThreads = 256;
 template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a) {
-    constexpr int COLS4 = DV / 4, GROUPS = kJoinThreads / COLS4;           // groups of threads share a row's parts
-    __shared__ int part[32], found[2];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const int runs) {
+    constexpr int COLS4 = DV / 4, GROUPS = kJoinThreads / COLS4;
     __shared__ float4 sums[kJoinThreads];
-    __shared__ float sums_l[GROUPS];
+    __shared__ float tops[GROUPS], totals[GROUPS];
     kv4::after_the_kernel_before();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int total = total_steps(a, part, kJoinThreads);
-    const int runs = runs_of(a, total), rows = a.blocks * kBlock;
-    const int c = (int)blockIdx.x + 1;
-    if (c >= runs) return;
-    const int cut = run_begin(total, runs, c);
-    if (tid < 32) {
-        int before;
-        const int b = find_step(a, cut, lane, &before);
-        if (lane == 0) {
-            found[0] = b;
-            found[1] = before;
-        }
-    }
-    __syncthreads();
-    const int b = found[0], n = tiles_at(a, b);
-    const int j = (cut - found[1]) / steps_of(n), first = found[1] + j * steps_of(n) + kUnitCost;      // its first tile
-    if (cut <= first) return;
-    const int r0 = run_of(total, runs, first), r1 = run_of(total, runs, first + n - 1);
-    if (c != r0 + 1) return;
-    const int hk = a.by_rb.into(j), rb = j - hk * a.n_rb, parts = r1 - r0 + 1;
-    const int group = tid / COLS4, col = tid - group * COLS4;
-    // part p: of run r0 + p; the unit begins in run r0
-    auto at = [&](int p) { return a.ws + partial_slot(r0 + p, p == 0) * partial_size(rows, DV); };
-    for (int row = (int)blockIdx.y; row < rows && rb * rows + row < a.R; row += gridDim.y) {
-        float M = -INFINITY;
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, at(p)[rows * DV + row]);
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const int c = (int)blockIdx.x, rows = a.blocks * kBlock;
+    const Open open = open_of(a, runs, DV)[c];
+    if (open.parts < 2) return;
+    const int hk = a.by_rb.into(open.j), row0 = (open.j - hk * a.n_rb) * rows;
+    const int group = threadIdx.x / COLS4, col = threadIdx.x - group * COLS4;
+    for (int row = (int)blockIdx.y; row < rows && row0 + row < a.R; row += gridDim.y) {
+        float M = -INFINITY, L = 0.f;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
 #pragma unroll 4
-        for (int p = group; p < parts; p += GROUPS) {
-            const float *q = at(p);
+        for (int p = group; p < open.parts; p += GROUPS) {
+            // (the unit begins in run c: its part in that run's second place)
+            const float *q = a.ws + partial_slot(c + p, p == 0) * partial_size(rows, DV);
             const float m = q[rows * DV + row], l = q[rows * (DV + 1) + row];
             const float4 x = *reinterpret_cast<const float4 *>(q + row * DV + 4 * col);
-            const float f = l == l ? weight(m, M) : l;
-            L = fmaf(f, l, L);
-            y = fma4(f, x, y);
+            const float top = fmaxf(M, m), g = weight(M, top), f = l == l ? weight(m, top) : l;
+            M = top;
+            L = fmaf(f, l, L * g);
+            y = fma4(f, x, make_float4(y.x * g, y.y * g, y.z * g, y.w * g));
         }
-        sums[tid] = y;
-        if (col == 0) sums_l[group] = L;
+        sums[threadIdx.x] = y;
+        if (col == 0) {
+            tops[group] = M;
+            totals[group] = L;
+        }
         __syncthreads();
         if (group == 0) {
-            for (int k = 1; k < GROUPS; ++k) {
-                y = fma4(1.f, sums[k * COLS4 + col], y);
-                L += sums_l[k];
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) M = fmaxf(M, tops[k]);
+            L = 0.f;
+            y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) {
+                const float f = totals[k] == totals[k] ? weight(tops[k], M) : totals[k];
+                L = fmaf(f, totals[k], L);
+                y = fma4(f, sums[k * COLS4 + col], y);
             }
             const float f = L == 0.f ? 0.f : __frcp_rn(L);
-            store4(a.out, a.out_type, (size_t)out_row(a, b, hk, rb * rows + row) * DV + 4 * col,
+            store4(a.out, a.out_type, (size_t)out_row(a, open.b, hk, row0 + row) * DV + 4 * col,
                    make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
         }
         __syncthreads();
@@ -1221,7 +1249,7 @@ cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn 
     e = cudaLaunchKernelEx(&cfg, attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, km, vm, a);
     if (e != cudaSuccess || a.cluster || grid < 2) return e;
     return kv4::launch_early(join_kernel<DV>, dim3((unsigned)grid - 1, (unsigned)(a.R < 8 ? a.R : 8)), kJoinThreads, 0, stream,
-                             a);
+                             a, grid);
 }
 
 template <typename T, int DK, int DV>
