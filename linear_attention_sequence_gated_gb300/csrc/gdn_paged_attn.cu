@@ -111,9 +111,10 @@ struct Plan {
 };
 
 // CTAs a unit, or 0 for equal runs, by the room that the tables have (the lengths are on the device): what the
-// slowest CTA streams, in bytes, and the joins' time as bytes: a cluster's 2 us, a second kernel's and the scans' 7 us.
-// A cluster grows while each group of its CTAs has two tiles and more.
-constexpr long long kClusterCost = 96 << 10, kRunsCost = 320 << 10;
+// slowest CTA streams, in bytes, and as bytes the time of what does not overlap it: each wave of CTAs' start and
+// join, 4 us; a cluster's join, 2 us; for runs 8 us once, the second kernel's among them.  A cluster grows while
+// each group of its CTAs has two tiles and more.
+constexpr long long kWaveCost = 160 << 10, kClusterCost = 80 << 10, kRunsCost = 320 << 10;
 bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int max_pages, int elt, Plan *p) {
     p->share = share_of(dk, dv, elt, H / Hkv * n_q);
     const long long units = (long long)n_seqs * Hkv * p->share.units, groups = p->share.groups;
@@ -124,8 +125,8 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     long long cl = 1;
     while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * groups * 2) cl *= 2;
     const long long waves = (units * cl + kGrid - 1) / kGrid;
-    const long long by_cluster = waves * ((tiles + cl - 1) / cl) * stage + (cl > 1 ? kClusterCost : 0);
-    const long long by_runs = (units * tiles + kGrid - 1) / kGrid * stage + kRunsCost;
+    const long long by_cluster = waves * ((tiles + cl - 1) / cl * stage + kWaveCost + (cl > 1 ? kClusterCost : 0));
+    const long long by_runs = (units * steps + kGrid - 1) / kGrid * stage + kRunsCost;
     p->cluster = by_cluster <= by_runs ? (int)cl : 0;
     const long long runs = (units * steps + groups - 1) / groups;
     p->grid = p->cluster ? (int)(units * cl) : (int)(runs < kGrid ? runs : kGrid);

@@ -45,7 +45,7 @@ constexpr int kBlock = 8;              // rows of an MMA column tile
 constexpr int kGrid = 152;             // runs at most: one CTA per SM of the GPU this is written for (the
                                        // workspace's size goes by it on any device)
 constexpr int kMaxCluster = 8;         // the largest portable size
-constexpr int kUnitCost = 4;           // tiles that beginning and ending a unit counts for when runs are cut
+constexpr int kUnitCost = 16;           // tiles that beginning and ending a unit counts for when runs are cut
 
 struct Attn {
     const void *q, *mask;
@@ -72,9 +72,10 @@ struct Attn {
 struct Room {
     int columns;                       // the warps' outputs are joined so many columns at a time,
     int merge;                         // in rows padded against bank conflicts
-    int q_row, q;                      // fp32 queries as hi and lo, in padded rows (16-bit ones are in registers)
     int weights, sums;                 // fp32 weights on their way to B operands; maxima and sums
-    int tiles;                         // of all rings
+    int q_row, q_block;                // fp32 queries as hi and lo, in padded rows; bytes of a block (16-bit ones are
+                                       // in registers)
+    int pool;                          // bytes for the ring and the queries
 };
 constexpr int kSmemMax = 227 * 1024;
 constexpr Room room_of(int dk, int dv, int elt, int warps, int most) {
@@ -82,15 +83,15 @@ constexpr Room room_of(int dk, int dv, int elt, int warps, int most) {
     Room r{};
     r.columns = row * (dv + 4) <= limit ? dv : dv > 128 && row * 132 <= limit ? 128 : 64;
     r.merge = row * (r.columns + 4);
-    r.q_row = dk * 8 + 64;
-    r.q = elt == 2 ? 0 : most * kBlock * r.q_row;
     r.weights = elt == 2 ? 0 : warps * kBlock * 20 * 4;
     r.sums = 2 * (warps + most) * kBlock * 4;
-    // (1 KB for the ring's alignment, 2 KB for barriers and the like)
-    const int tiles = (kSmemMax - 3072 - r.merge - r.q - r.weights - r.sums) / (kTile * (dk + dv) * elt);
-    r.tiles = tiles < 48 ? tiles : 48;
+    r.q_row = dk * 8 + 64;
+    r.q_block = elt == 2 ? 0 : kBlock * r.q_row;
+    // (1 KB for the ring's alignment, 3 KB for barriers and the like)
+    r.pool = (kSmemMax - 4096 - r.merge - r.weights - r.sums) / 16 * 16;
     return r;
 }
+constexpr int kMaxRing = 48;
 
 // How the rows of a kv head and the warps of a CTA are shared out.  Tiles go round the groups of warps; each
 // warp of a group takes another block of 8 rows of the same tile, so that the cache is read once for all of them:
@@ -109,7 +110,9 @@ constexpr Share share_of(int dk, int dv, int elt, int R) {
     const bool wide = elt == 4 || dk > 128 || dv > 128;
     const int warps = wide ? 8 : 12, most = !wide ? 6 : elt == 2 || R > kBlock ? 4 : 1;
     const int all = (R + kBlock - 1) / kBlock, units = (all + most - 1) / most, blocks = (all + units - 1) / units;
-    const int tiles = room_of(dk, dv, elt, warps, most).tiles;
+    const Room room = room_of(dk, dv, elt, warps, most);
+    int tiles = (room.pool - blocks * room.q_block) / (kTile * (dk + dv) * elt);
+    if (tiles > kMaxRing) tiles = kMaxRing;
     const int groups = warps / blocks < tiles ? warps / blocks : tiles;
     return {warps, most, blocks, groups, units, tiles - tiles % groups};
 }
@@ -130,10 +133,10 @@ using kv4::run_begin;
 using kv4::run_of;
 using kv4::partial_slot;
 
-// Shape of the kernel for widths DK and DV, type T and WARPS warps, which take U tiles at a time.
-template <typename T, int DK, int DV, int WARPS, int MOST, int U_>
+// Shape of the kernel for widths DK and DV, type T, WARPS warps and up to MOST blocks of rows.
+template <typename T, int DK, int DV, int WARPS, int MOST>
 struct Geo {
-    static constexpr int E = (int)sizeof(T), U = U_;
+    static constexpr int E = (int)sizeof(T);
     static constexpr bool MMA16 = E == 2;
     static constexpr int BOX = 128 / E;                // elements of a box's row
     static constexpr int KB = kTile * DK * E, VB = kTile * DV * E, STAGE = KB + VB;
@@ -144,11 +147,13 @@ struct Geo {
     static_assert(WARPS % 4 == 0 && THREADS * WORK_REGS + 32 * kFillers * FILL_REGS <= ALL * REGS,
                   "a split of more registers than the launch has would wait forever");
     static constexpr Room R = room_of(DK, DV, E, WARPS, MOST);
-    static constexpr int MC = R.columns, QROW = R.q_row, STAGES = R.tiles, RING = STAGES * STAGE;
-    static constexpr int SMEM = 1024 + RING + R.merge + R.q + R.weights + R.sums;
-    static_assert(STAGES >= 4, "ring");
-    static_assert(R.merge % 16 == 0 && R.q % 16 == 0 && R.weights % 16 == 0 && DV % MC == 0, "alignment");
-    static_assert(WARPS * kBlock * (DV + 4) * 4 <= RING, "a cluster's CTAs join in the ring");
+    static constexpr int MC = R.columns, QROW = R.q_row;
+    static constexpr int QBLOCK = R.q_block, RING = R.pool - MOST * QBLOCK;    // (the least that a ring has)
+    static constexpr int SMEM = 1024 + R.pool + R.merge + R.weights + R.sums;
+    static_assert(RING / STAGE >= 4, "ring");
+    static_assert(17 * kMaxRing + 160 + (8 + 4 * kMaxCluster) * MOST * kBlock <= 3072, "barriers and the like");
+    static_assert(R.merge % 16 == 0 && QROW % 16 == 0 && R.weights % 16 == 0 && DV % MC == 0, "alignment");
+    static_assert(WARPS * kBlock * (DV + 4) * 4 <= RING / STAGE / 4 * 4 * STAGE, "the last unit is joined in the ring");
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -367,7 +372,6 @@ struct Walk {
 template <typename T, int DK, int DV, typename G, bool COLS>
 struct Unit {
     static constexpr bool MMA16 = G::MMA16;
-    static constexpr int U = G::U;
     static constexpr int KS = DK / 16, MT = DV / 16;   // 16-element steps of a key, blocks of a value row
     // weights of f16 rows are scaled by 2^12, so that small ones keep their bits
     static constexpr float kBits = std::is_same<T, __half>::value ? 12.f : 0.f;
@@ -400,16 +404,17 @@ struct Unit {
     }
 
     // 16-bit queries of rows row0 .. row0 + 7 of kv head hk, as B operands.
-    __device__ __forceinline__ static void load_queries(const Attn &a, int b, int hk, int row0, int lane,
+    __device__ __forceinline__ static void load_queries(const Attn &a, const Walk &w, int row0, int lane,
                                                         uint32_t (&q)[MMA16 ? KS : 1][2]) {
         if constexpr (MMA16) {
-            const int g = lane >> 2, t = lane & 3, row = COLS ? g & 3 : row0 + g;
-            const bool ok = row < a.R;
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(q_row(a, b, hk, ok ? row : 0)) + t;
+            // (a row that is not there takes the last one's, for columns that nobody reads: nothing here may wait
+            // for the loads)
+            const int g = lane >> 2, t = lane & 3, row = min(COLS ? g & 3 : row0 + g, a.R - 1);
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(q_row(a, w.b, a.by_rb.into(w.j), row)) + t;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                q[s][0] = ok ? p[s * 8] : 0u;
-                q[s][1] = ok ? p[s * 8 + 4] : 0u;
+                q[s][0] = p[s * 8];
+                q[s][1] = p[s * 8 + 4];
             }
         }
     }
@@ -552,58 +557,36 @@ struct Unit {
         return __any_sync(0xffffffffu, MMA16 ? (acc2 & 0x7fff7fffu) != 0 : acc != acc);
     }
 
-    // One tile or (U = 2) two: tokens pos[u] .. pos[u] + 15 of the sequence, in stage[u].
-    __device__ __forceinline__ void tiles(const Attn &a, uint8_t *const (&stage)[U], const int (&pos)[U],
-                                          bool two, const uint8_t *sq, float *pt, int lane) {
+    // The tile in `stage`, tokens pos .. pos + 15 of the sequence.
+    __device__ __forceinline__ void tile(const Attn &a, const uint8_t *stage, int pos, const uint8_t *sq, float *pt, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        float s[U][4], x[U][4], cf[2], add[U][4];
-        bool plain = true;
+        float s[4], x[4], cf[2], add[4];
         if (a.mask) {                  // loaded ahead of the products
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = qi[e & 1], j = pos[u] + g + 8 * (e >> 1);
-                    add[u][e] = -INFINITY;
-                    if ((u == 0 || two) && i >= 0 && j < len)
-                        add[u][e] = to_float<T>(
-                            static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j]);
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u == 0 || two) {
-                scores(ptx::smem_u32(stage[u]), sq, lane, s[u]);
-                plain &= pos[u] + kTile <= all;
+            for (int e = 0; e < 4; ++e) {
+                const int i = qi[e & 1], j = pos + g + 8 * (e >> 1);
+                add[e] = i >= 0 && j < len
+                             ? to_float<T>(static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j])
+                             : -INFINITY;
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[u][e] = u == 0 || two ? s[u][e] * a.scale : -INFINITY;
         }
+        scores(ptx::smem_u32(stage), sq, lane, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = s[e] * a.scale;
+        const bool plain = pos + kTile <= all;
         if (!plain) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u == 1 && !two) break;
+            for (int r = 0; r < 2; ++r) {
+                const int i = qi[r];
+                const long long lim = a.causal ? min((long long)len, (long long)raw - a.n_q + 1 + i) : len;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = qi[r];
-                    const long long lim = a.causal ? min((long long)len, (long long)raw - a.n_q + 1 + i) : len;
-#pragma unroll
-                    for (int e = r; e < 4; e += 2) {
-                        const int j = pos[u] + g + 8 * (e >> 1);
-                        if (i < 0 || j >= lim) {
-                            x[u][e] = -INFINITY;
-                        } else if (a.mask) {
-                            x[u][e] = add[u][e] == -INFINITY ? -INFINITY : x[u][e] + add[u][e];
-                        }
-                    }
+                for (int e = r; e < 4; e += 2) {
+                    if (i < 0 || pos + g + 8 * (e >> 1) >= lim) x[e] = -INFINITY;
+                    else if (a.mask) x[e] = add[e] == -INFINITY ? -INFINITY : x[e] + add[e];
                 }
             }
         }
-        float mx[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
-        if constexpr (U == 2) {
-            mx[0] = fmaxf(mx[0], fmaxf(x[1][0], x[1][2]));
-            mx[1] = fmaxf(mx[1], fmaxf(x[1][1], x[1][3]));
-        }
+        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
@@ -616,22 +599,16 @@ struct Unit {
             const float old = m[r], mn = fmaxf(old, mx[r]), base = mn == -INFINITY ? 0.f : mn;
             m[r] = mn;
             cf[r] = exp2_approx((old - base) * kLog2e);
-            float sum = 0.f;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                s[u][r] = exp2_approx(fmaf(x[u][r] - base, kLog2e, kBits));
-                s[u][r + 2] = exp2_approx(fmaf(x[u][r + 2] - base, kLog2e, kBits));
-                sum += s[u][r] + s[u][r + 2];
-            }
-            l[r] = fmaf(l[r], cf[r], sum);
+            s[r] = exp2_approx(fmaf(x[r] - base, kLog2e, kBits));
+            s[r + 2] = exp2_approx(fmaf(x[r + 2] - base, kLog2e, kBits));
+            l[r] = fmaf(l[r], cf[r], s[r] + s[r + 2]);
         }
-        if (!plain && (any_odd(stage[0] + G::KB, lane) || (U == 2 && two && any_odd(stage[U - 1] + G::KB, lane)))) {
+        if (!plain && any_odd(stage + G::KB, lane)) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] *= cf[e & 1];
-            odd_values(stage[0] + G::KB, s[0], x[0], lane);
-            if (U == 2 && two) odd_values(stage[U - 1] + G::KB, s[U - 1], x[U - 1], lane);
+            odd_values(stage + G::KB, s, x, lane);
             return;
         }
         if constexpr (MMA16) {
@@ -639,54 +616,45 @@ struct Unit {
             // COLS the second stands in columns 4 .. 7 of the first's products, where the rows' queries stand again.
             constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
             const bool third = BF && a.out_type == GDN_DTYPE_F32;
-            uint32_t p1[U][2], p2[U][2], p3[U][2];
+            uint32_t p1[2], p2[2], p3[2];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float y = s[u][2 * h], z = s[u][2 * h + 1];
-                    p1[u][h] = round2<T>(y, z);
-                    p2[u][h] = round2<T>(y, z);
-                    if constexpr (BF) p3[u][h] = third ? round2<T>(y, z) : 0u;
-                    if constexpr (COLS) {
-                        p1[u][h] = t >= 2 ? p2[u][h] : p1[u][h];
-                        if constexpr (BF) p2[u][h] = t >= 2 ? 0u : p3[u][h];
-                    }
-                    p1[u][h] = transpose8(p1[u][h]);
-                    if (!COLS || third) p2[u][h] = transpose8(p2[u][h]);
-                    if (!COLS && third) p3[u][h] = transpose8(p3[u][h]);
+            for (int h = 0; h < 2; ++h) {
+                float y = s[2 * h], z = s[2 * h + 1];
+                p1[h] = round2<T>(y, z);
+                p2[h] = round2<T>(y, z);
+                if constexpr (BF) p3[h] = third ? round2<T>(y, z) : 0u;
+                if constexpr (COLS) {
+                    p1[h] = t >= 2 ? p2[h] : p1[h];
+                    if constexpr (BF) p2[h] = t >= 2 ? 0u : p3[h];
                 }
+                p1[h] = transpose8(p1[h]);
+                if (!COLS || third) p2[h] = transpose8(p2[h]);
+                if (!COLS && third) p3[h] = transpose8(p3[h]);
+            }
             const uint32_t tok = (lane & 7) + ((lane >> 4) << 3);
             const uint32_t row = tok * 128 + G::KB, sw = lane & 7, half = (lane >> 3) & 1;
             // four blocks of 16 elements at a time, whose products do not wait for one another
 #pragma unroll
             for (int i0 = 0; i0 < MT; i0 += 4) {
                 float d[4][4];
+                uint32_t A[4][4];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (u == 1 && !two) break;
-                    uint32_t A[4][4];
-                    const uint32_t at = ptx::smem_u32(stage[u]) + row + (i0 >> 2) * 2048;
+                for (int i = 0; i < 4; ++i)
+                    ldsm4_t(A[i], ptx::smem_u32(stage) + row + (i0 >> 2) * 2048 + (((2 * i + half) ^ sw) << 4));
+                // small terms first
+                if (!COLS && third)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ldsm4_t(A[i], at + (((2 * i + half) ^ sw) << 4));
-                    // small terms first
-                    if (!COLS && third)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (u == 0) mma0<T>(d[i], A[i], p3[u][0], p3[u][1]);
-                            else mma<T>(d[i], A[i], p3[u][0], p3[u][1]);
-                        }
-                    if (!COLS || third)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (u == 0 && (COLS || !third)) mma0<T>(d[i], A[i], p2[u][0], p2[u][1]);
-                            else mma<T>(d[i], A[i], p2[u][0], p2[u][1]);
-                        }
+                    for (int i = 0; i < 4; ++i) mma0<T>(d[i], A[i], p3[0], p3[1]);
+                if (!COLS || third)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (u == 0 && COLS && !third) mma0<T>(d[i], A[i], p1[u][0], p1[u][1]);
-                        else mma<T>(d[i], A[i], p1[u][0], p1[u][1]);
+                        if (COLS || !third) mma0<T>(d[i], A[i], p2[0], p2[1]);
+                        else mma<T>(d[i], A[i], p2[0], p2[1]);
                     }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (COLS && !third) mma0<T>(d[i], A[i], p1[0], p1[1]);
+                    else mma<T>(d[i], A[i], p1[0], p1[1]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -694,13 +662,12 @@ struct Unit {
                     for (int e = 0; e < 4; ++e) o[i0 + i][e] = fmaf(o[i0 + i][e], cf[e & 1], d[i][e]);
             }
         } else {
-            static_assert(MMA16 || U == 1, "one tile of fp32 rows at a time");
-            const uint32_t v = ptx::smem_u32(stage[0]) + G::KB;
+            const uint32_t v = ptx::smem_u32(stage) + G::KB;
             // weights to [row][token]; lane (g, t) takes row g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
-            pt[(2 * t) * 20 + g] = s[0][0];
-            pt[(2 * t + 1) * 20 + g] = s[0][1];
-            pt[(2 * t) * 20 + g + 8] = s[0][2];
-            pt[(2 * t + 1) * 20 + g + 8] = s[0][3];
+            pt[(2 * t) * 20 + g] = s[0];
+            pt[(2 * t + 1) * 20 + g] = s[1];
+            pt[(2 * t) * 20 + g + 8] = s[2];
+            pt[(2 * t + 1) * 20 + g + 8] = s[3];
             __syncwarp();
             uint32_t ph[4], pl[4];
             {
@@ -805,20 +772,20 @@ __device__ __forceinline__ long long out_row(const Attn &a, int b, int hk, int r
     return ((long long)b * a.n_q + i) * a.H + hk * a.rep + h;
 }
 
-template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
+template <typename T, int DK, int DV, int WARPS, int MOST, bool COLS>
 __global__ void __launch_bounds__(WARPS * 32 + 32 * kFillers, 1)
 attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const Attn a) {
-    using G = Geo<T, DK, DV, WARPS, MOST, U>;
+    using G = Geo<T, DK, DV, WARPS, MOST>;
     using Part = Unit<T, DK, DV, G, COLS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
-    float *merge = reinterpret_cast<float *>(ring + G::RING);              // [WARPS][8][MC + 4]
-    uint8_t *sq = ring + G::RING + G::R.merge;
-    float *pts = reinterpret_cast<float *>(sq + G::R.q);
-    float *sm = reinterpret_cast<float *>(sq + G::R.q + G::R.weights);     // [WARPS][8] maxima, then the CTA's
+    uint8_t *sq = ring + a.ring * G::STAGE;            // queries, behind the ring
+    float *merge = reinterpret_cast<float *>(ring + G::R.pool);            // [WARPS][8][MC + 4]
+    float *pts = reinterpret_cast<float *>(ring + G::R.pool + G::R.merge);
+    float *sm = reinterpret_cast<float *>(ring + G::R.pool + G::R.merge + G::R.weights);   // [WARPS][8] maxima, then the CTA's
     float *sl = sm + (WARPS + MOST) * kBlock;                              // ... and sums
-    __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
-    __shared__ uint8_t none[G::STAGES];
+    __shared__ uint64_t full[kMaxRing], empty[kMaxRing];
+    __shared__ uint8_t none[kMaxRing];
     __shared__ int part[32], start[2], gave_up;
     __shared__ long long place[MOST * kBlock];
     __shared__ float shares[kMaxCluster][MOST * kBlock];
@@ -829,7 +796,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     const bool works = group < a.groups;
     if (tid == 0) {
         gave_up = 0;
-        for (int s = 0; s < G::STAGES; ++s) {
+        for (int s = 0; s < a.ring; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], a.blocks);
         }
@@ -999,14 +966,14 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     // ---- segments
     float *pt = pts + (G::MMA16 ? 0 : warp * kBlock * 20);
     bool dead = false;
-    uint32_t next_q[Part::MMA16 ? Part::KS : 1][2];    // the next segment's queries, loaded while this one's parts join
     auto row0_of = [&](const Walk &w) { return (w.j - a.by_rb.into(w.j) * a.n_rb) * a.blocks * kBlock; };
-    if (any || a.cluster) Part::load_queries(a, run.b, a.by_rb.into(run.j), row0_of(run) + block * kBlock, lane, next_q);
+    uint32_t next_q[Part::MMA16 ? Part::KS : 1][2];    // the next segment's queries, loaded while this one's parts join
+    if (any || a.cluster) Part::load_queries(a, run, row0_of(run) + block * kBlock, lane, next_q);
     if (works) advance(group);         // s: where the group's next tile comes
     for (bool more = any || a.cluster; more;) {
         const int hk = a.by_rb.into(run.j), row0 = row0_of(run);
         Part u;
-        if constexpr (G::R.q != 0) {
+        if constexpr (!G::MMA16) {
             Part::stage_queries(a, run.b, hk, row0, sq);
             consumers_sync();
         }
@@ -1017,56 +984,28 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         u.begin(a, run, row0 + block * kBlock, lane);
         int tile = run.begin + group;
         while (works && tile < run.end) {
-            const bool pair = U == 2 && tile + a.groups < run.end;
-            uint8_t *stage[U];
-            int at[U], pos[U];
-            bool there[U], came = true;
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                if (x == 1 && !pair) break;
-                at[x] = s;
-                stage[x] = ring + s * G::STAGE;
-                pos[x] = tile * kTile;
-                if (!dead) came &= ptx::mbar_wait(&full[s], phase, &gave_up);
-                there[x] = !none[s];
-                advance(a.groups);
-                tile += a.groups;
-            }
             if (!dead) {
-                dead = __any_sync(0xffffffffu, !came);
+                dead = __any_sync(0xffffffffu, !ptx::mbar_wait(&full[s], phase, &gave_up));
                 if (dead) {
                     gave_up = 1;
                     *a.status = GDN_ERR_TIMEOUT;
                 }
             }
-            if (dead) continue;
-            bool two = false, one = there[0];
-            if constexpr (U == 2) {
-                two = pair && there[1];
-                if (!pair) {
-                    stage[1] = stage[0];
-                    pos[1] = pos[0];
-                } else if (two && !there[0]) {         // only the second is there: it stands for the first
-                    stage[0] = stage[1];
-                    pos[0] = pos[1];
-                    one = true;
-                    two = false;
-                }
+            if (!dead) {
+                if (!none[s])
+                    u.tile(a, ring + s * G::STAGE, tile * kTile, sq + block * G::QBLOCK, pt, lane);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&empty[s]);
             }
-            if (one) u.tiles(a, stage, pos, two, sq + block * kBlock * G::QROW, pt, lane);
-            __syncwarp();
-            if (lane == 0) {
-#pragma unroll
-                for (int x = 0; x < U; ++x)
-                    if (x == 0 || pair) ptx::mbar_arrive(&empty[at[x]]);
-            }
+            advance(a.groups);
+            tile += a.groups;
         }
         // to the group's first tile of the next segment: tiles go on in order
         if (works) advance(run.end - (tile - group));
         u.finish();
         Walk next = run;
         more = any && next.next(a);
-        if (more) Part::load_queries(a, next.b, a.by_rb.into(next.j), row0_of(next) + block * kBlock, lane, next_q);
+        if (more) Part::load_queries(a, next, row0_of(next) + block * kBlock, lane, next_q);
 
         // ---- the groups' parts of the segment join: MC columns at a time, or, when no more tiles come, all of
         // them in the ring
@@ -1220,16 +1159,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Attn a, const 
     }
 }
 
-template <typename T, int DK, int DV, int WARPS, int MOST, int U, bool COLS>
+template <typename T, int DK, int DV, int WARPS, int MOST, bool COLS>
 cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn &a, int grid, cudaStream_t stream) {
-    using G = Geo<T, DK, DV, WARPS, MOST, U>;
+    using G = Geo<T, DK, DV, WARPS, MOST>;
     static PerDeviceOnce setup;
     cudaError_t e = setup.run([] {
         cudaFuncAttributes f;
-        const cudaError_t q = cudaFuncGetAttributes(&f, attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>);
+        const cudaError_t q = cudaFuncGetAttributes(&f, attn_kernel<T, DK, DV, WARPS, MOST, COLS>);
         if (q != cudaSuccess) return q;
         if (f.numRegs < G::REGS) return cudaErrorInvalidConfiguration;   // (the split counts on them)
-        return cudaFuncSetAttribute(attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_kernel<T, DK, DV, WARPS, MOST, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     G::SMEM);
     });
     if (e != cudaSuccess) return e;
@@ -1246,7 +1185,7 @@ cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const Attn 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, DK, DV, WARPS, MOST, U, COLS>, km, vm, a);
+    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, DK, DV, WARPS, MOST, COLS>, km, vm, a);
     if (e != cudaSuccess || a.cluster || grid < 2) return e;
     return kv4::launch_early(join_kernel<DV>, dim3((unsigned)grid - 1, (unsigned)(a.R < 8 ? a.R : 8)), kJoinThreads, 0, stream,
                              a, grid);
@@ -1257,12 +1196,12 @@ cudaError_t launch_rows(const CUtensorMap &km, const CUtensorMap &vm, const Attn
     constexpr int E = (int)sizeof(T);
     constexpr Share few = share_of(DK, DV, E, 1), many = share_of(DK, DV, E, kBlock + 1);
     if constexpr (E == 4) {
-        if (a.R <= kBlock) return launch_one<T, DK, DV, few.warps, few.most, 1, false>(km, vm, a, grid, stream);
+        if (a.R <= kBlock) return launch_one<T, DK, DV, few.warps, few.most, false>(km, vm, a, grid, stream);
     } else {
         // of at most 4 rows, the weights' second terms enter in the free columns of the same MMAs
-        if (a.R <= 4) return launch_one<T, DK, DV, few.warps, few.most, 1, true>(km, vm, a, grid, stream);
+        if (a.R <= 4) return launch_one<T, DK, DV, few.warps, few.most, true>(km, vm, a, grid, stream);
     }
-    return launch_one<T, DK, DV, many.warps, many.most, 1, false>(km, vm, a, grid, stream);
+    return launch_one<T, DK, DV, many.warps, many.most, false>(km, vm, a, grid, stream);
 }
 
 }  // namespace

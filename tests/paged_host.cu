@@ -4,8 +4,9 @@
 extern "C" void paged_share(int dk, int dv, int elt, int R, int *out) {
     using namespace gdn::paged;
     const Share s = share_of(dk, dv, elt, R);
-    const int x[7] = {s.warps, s.most, s.blocks, s.groups, s.units, s.ring, room_of(dk, dv, elt, s.warps, s.most).tiles};
-    for (int i = 0; i < 7; ++i) out[i] = x[i];
+    const Room r = room_of(dk, dv, elt, s.warps, s.most);
+    const int x[8] = {s.warps, s.most, s.blocks, s.groups, s.units, s.ring, r.pool, s.blocks * r.q_block};
+    for (int i = 0; i < 8; ++i) out[i] = x[i];
 }
 
 // The quotients as the device takes them: the upper half of a 32 x 32-bit product, shifted.

@@ -124,13 +124,14 @@ def H(tmp_path_factory):
 @pytest.mark.parametrize("dv", [64, 128, 256])
 def test_rings_are_a_whole_number_of_tiles_a_group(H, elt, dk, dv):
     """A barrier's parity tells a phase from the next only, so a stage belongs to one group; and all rows have a block."""
-    out = (ctypes.c_int * 7)()
+    out = (ctypes.c_int * 8)()
     for R in list(range(1, 200)) + [760, 5000]:
         H.paged_share(dk, dv, elt, R, out)
-        warps, most, blocks, groups, units, ring, tiles = out
-        assert ring % groups == 0 and groups <= ring <= tiles and 1 <= groups * blocks <= warps
+        warps, most, blocks, groups, units, ring, pool, queries = out
+        assert ring % groups == 0 and groups <= ring <= 48 and 1 <= groups * blocks <= warps
         assert blocks <= most and 8 * blocks * units >= R and 8 * blocks * (units - 1) < R
-        assert (3 << 10) + tiles * 16 * (dk + dv) * elt <= 227 << 10
+        assert ring * 16 * (dk + dv) * elt + queries <= pool <= 224 << 10
+        assert warps * 8 * (dv + 4) * 4 <= ring * 16 * (dk + dv) * elt       # the last unit is joined in the ring
 
 
 def test_quotients_by_a_known_number(H):
