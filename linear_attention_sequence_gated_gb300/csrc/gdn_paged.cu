@@ -7,14 +7,16 @@
 // moved each way: HBM bounds long runs, latency short ones.
 //
 // A lane takes 32 bytes of a row, as two 16-byte pieces that hold whole pairs (piece p of each
-// half, or two neighbouring ones), and the same pieces of further heads of the token, whose
-// angles are the same: cosines and sines are computed once a lane, in registers, without a
-// table in memory.  A warp's lanes cover whole rows.
+// half, or two neighbouring ones), and a warp's lanes cover whole rows.  Rows that turn are shared out by
+// tokens: a lane goes on to the same pieces of further heads, queries' and keys', whose angles are the same, so
+// cosines and sines are computed once a lane, in registers, without a table in memory.  Rows that are
+// copied are shared out one after another, whatever their token.
 //
 // The angle is exact modulo a turn: a frequency is kept as a fraction of a turn with 64
 // bits, the product with the 32-bit position is taken modulo 2^64, and its upper 32 bits
 // are the fraction of a turn, split into a quadrant and a rest of at most an eighth of a turn,
-// which fp32 holds to 2^-28 of a turn.  So position 10^6 is as accurate as position 1.
+// which fp32 holds to 2^-28 of a turn.  So position 10^6 is as accurate as position 1.  On that rest the series of
+// sine and cosine end after a few terms.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -32,29 +34,47 @@ namespace {
 
 constexpr int kWarps = 4;              // warps of a block, each with rows of its own
 
+constexpr int kRows = 4;               // rows of a lane in flight
+
 // Rows of one tensor, (n_tokens, heads, d), and where they go.
 struct Rows {
     const uint8_t *src;
     uint8_t *dst;
     long long src_token, src_head;     // strides in bytes
     long long dst_token, dst_head, dst_page;   // of a cache: within its page, across heads, pages
-    int heads, lanes;                  // lanes a row: d * width / 32
-    int per_warp;                      // rows (of one token) that a warp takes at a time
-    int split;                         // warps that share the heads of a token
-    bool turn, cache;
+    int heads;
+    bool cache;
+};
+// How the rows of one width lie on a warp's lanes.
+struct Lanes {
+    int lanes, rows;                   // lanes of a row (32 bytes each), rows of a warp
 };
 
 struct Job {
-    Rows rows[3];
-    int begin[4];                      // warps before each tensor's, of one token; their total
+    Rows turned[2];                    // queries and keys; of no heads where they are not turned
+    Rows copied[3];                    // the others, one after another
+    Lanes on, on_copied[3];
+    int pieces;                        // lanes of a turned row that turn (the others copy)
+    int tokens, heads, split;          // a warp that turns takes so many tokens, so many heads of each at a time, and
+                                       // shares the tokens with split - 1 others
+    int begin[4];                      // warps that turn, and those that copy the first, the second, the third behind them
     const int *positions;              // (n_axes, n_tokens)
     const uint4 *plan;                 // (r / 2): fraction of a turn (64 bits), axis
     const int *slots;                  // (n_tokens)
     int *status;
-    int n_tokens, n_axes;
-    int turned;                        // lanes of a row that turn (the others copy)
-    int page, n_slots;
+    int n_tokens, n_axes, page, n_slots;
+    Divisor by_split, by_heads, by_page, by_rows[3];   // `split`, `heads`; tokens of a page; heads of the copied
 };
+
+// Where token t's rows go, or NULL: nowhere.
+__device__ __forceinline__ uint8_t *place_of(const Job &job, const Rows &r, int t) {
+    if (!r.cache) return r.dst + t * r.dst_token;
+    const int slot = job.slots[t];
+    if (slot >= job.n_slots) *job.status = GDN_ERR_PAGE;
+    if (slot < 0 || slot >= job.n_slots) return nullptr;
+    const int page = job.by_page.into(slot);
+    return r.dst + page * r.dst_page + (slot - page * job.page) * r.dst_token;
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[16 / sizeof(T)]) {
@@ -91,13 +111,16 @@ __device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// cos and sin of pos turns of a frequency, the sine's sign flipped for the inverse.
+// cos and sin of pos turns of a frequency, the sine's sign flipped for the inverse.  The Taylor polynomials of degree 9
+// and 10 are off by less than x^11 / 11! = 2e-9 and x^12 / 12! = 2e-10 for |x| <= pi / 4.
 __device__ __forceinline__ void angle(uint64_t turns, int pos, bool inverse, float &c, float &s) {
     const uint32_t f = (uint32_t)((turns * (uint64_t)(int64_t)pos) >> 32);   // fraction of a turn, 2^-32
     const uint32_t quadrant = (f + 0x20000000u) >> 30;
     const int rest = (int)(f - (quadrant << 30));                           // |rest| <= 2^29
-    float cr, sr;
-    sincospif((float)rest * 0x1p-31f, &sr, &cr);
+    const float x = (float)rest * (0x1p-31f * 3.14159265358979f), x2 = x * x;
+    const float sr = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), 1.f);
+    const float cr = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24),
+                                   -0.5f), 1.f);
     c = quadrant & 1 ? sr : cr;
     s = quadrant & 1 ? cr : sr;
     if (quadrant == 1 || quadrant == 2) c = -c;
@@ -124,38 +147,54 @@ __device__ __forceinline__ void turn(uint4 &wa, uint4 &wb, const float (&c)[16 /
     wb = pack<T>(b);
 }
 
+// Up to kRows rows a warp holds at a time, one after another.
+__device__ __forceinline__ void copy_rows(const Job &job, int which, int warp, int lane) {
+    const Rows &r = job.copied[which];
+    const Lanes on = job.on_copied[which];
+    const int row = lane / on.lanes, at = 32 * (lane - row * on.lanes);
+    if (row >= on.rows) return;
+    const long long first = (long long)warp * kRows * on.rows + row, n = (long long)job.n_tokens * r.heads;
+    uint4 x[kRows], y[kRows];
+    uint8_t *dst[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long i = first + u * on.rows;
+        dst[u] = nullptr;
+        if (i >= n) continue;
+        const int t = job.by_rows[which].into((int)i), h = (int)i - t * r.heads;
+        const uint8_t *p = r.src + t * r.src_token + h * r.src_head + at;
+        x[u] = *reinterpret_cast<const uint4 *>(p);
+        y[u] = *reinterpret_cast<const uint4 *>(p + 16);
+        dst[u] = place_of(job, r, t);
+        if (dst[u]) dst[u] += h * r.dst_head + at;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (dst[u]) {
+            *reinterpret_cast<uint4 *>(dst[u]) = x[u];
+            *reinterpret_cast<uint4 *>(dst[u] + 16) = y[u];
+        }
+}
+
 // KIND 0: copies only; 1: pairs are the halves of the turned part; 2: neighbours.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const __grid_constant__ Job job, const bool inverse) {
-    constexpr int E = 16 / (int)sizeof(T), U = 4;      // elements of a piece; rows in flight
+__global__ void __launch_bounds__(kWarps * 32, KIND == 0 ? 8 : 6) rows_kernel(const __grid_constant__ Job job, const bool inverse) {
+    constexpr int E = 16 / (int)sizeof(T);             // elements of a piece
     kv4::after_the_kernel_before();
-    const int lane = threadIdx.x & 31;
-    const long long warp = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int t = (int)(warp / job.begin[3]);
-    if (t >= job.n_tokens) return;
-    int part = (int)(warp - (long long)t * job.begin[3]);
-    const int which = part >= job.begin[2] ? 2 : part >= job.begin[1] ? 1 : 0;
-    const Rows &r = job.rows[which];
-    part -= job.begin[which];
-    const int row = lane / r.lanes, piece = lane - row * r.lanes;
-    const int step = r.per_warp * r.split;
-    int h = part * r.per_warp + row;
-    if (row >= r.per_warp || h >= r.heads) return;
-    // the lane's two pieces of a row, in bytes
-    const bool turned = KIND != 0 && r.turn && piece < job.turned;
-    const int a = turned && KIND == 1 ? 16 * piece : 32 * piece;
-    const int b = turned && KIND == 1 ? 16 * (piece + job.turned) : 32 * piece + 16;
-    const uint8_t *src = r.src + t * r.src_token;
-    uint8_t *dst = r.dst;
-    if (r.cache) {
-        const int slot = job.slots[t];
-        if (slot >= job.n_slots && lane == 0) *job.status = GDN_ERR_PAGE;
-        if (slot < 0 || slot >= job.n_slots) return;
-        const int page = slot / job.page;
-        dst += page * r.dst_page + (slot - page * job.page) * r.dst_token;
-    } else {
-        dst += t * r.dst_token;
+    const int lane = threadIdx.x & 31, warp = (int)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (KIND == 0 || warp >= job.begin[0]) {
+        const int which = warp < job.begin[1] ? 0 : warp < job.begin[2] ? 1 : 2;
+        if (warp < job.begin[3]) copy_rows(job, which, warp - job.begin[which], lane);
+        return;
     }
+    const int group = job.by_split.into(warp), part = warp - group * job.split;
+    const int row = lane / job.on.lanes, piece = lane - row * job.on.lanes;
+    const int ahead = job.by_heads.into(row), t = group * job.tokens + ahead;
+    if (row >= job.on.rows || ahead >= job.tokens || t >= job.n_tokens) return;
+    // the lane's two pieces of a row, in bytes
+    const bool turned = piece < job.pieces;
+    const int a = turned && KIND == 1 ? 16 * piece : 32 * piece;
+    const int b = turned && KIND == 1 ? 16 * (piece + job.pieces) : 32 * piece + 16;
     float c[E], s[E];
     if (turned) {
 #pragma unroll
@@ -165,23 +204,33 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const __grid_constant
             angle((uint64_t)f.y << 32 | f.x, job.positions[(size_t)axis * job.n_tokens + t], inverse, c[i], s[i]);
         }
     }
-    for (; h < r.heads; h += U * step) {
-        uint4 x[U], y[U];
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const Rows &r = job.turned[which];
+        const int step = job.heads * job.split;
+        const uint8_t *src = r.src + t * r.src_token;
+        int h = part * job.heads + row - ahead * job.heads;
+        if (h >= r.heads) continue;
+        uint8_t *dst = place_of(job, r, t);
+        if (!dst) continue;
+        for (; h < r.heads; h += kRows * step) {
+            uint4 x[kRows], y[kRows];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (h + u * step < r.heads) {
-                const uint8_t *p = src + (h + u * step) * r.src_head;
-                x[u] = *reinterpret_cast<const uint4 *>(p + a);
-                y[u] = *reinterpret_cast<const uint4 *>(p + b);
-            }
+            for (int u = 0; u < kRows; ++u)
+                if (h + u * step < r.heads) {
+                    const uint8_t *p = src + (h + u * step) * r.src_head;
+                    x[u] = *reinterpret_cast<const uint4 *>(p + a);
+                    y[u] = *reinterpret_cast<const uint4 *>(p + b);
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (h + u * step < r.heads) {
-                if (turned) turn<T, KIND == 2>(x[u], y[u], c, s);
-                uint8_t *p = dst + (h + u * step) * r.dst_head;
-                *reinterpret_cast<uint4 *>(p + a) = x[u];
-                *reinterpret_cast<uint4 *>(p + b) = y[u];
-            }
+            for (int u = 0; u < kRows; ++u)
+                if (h + u * step < r.heads) {
+                    if (turned) turn<T, KIND == 2>(x[u], y[u], c, s);
+                    uint8_t *p = dst + (h + u * step) * r.dst_head;
+                    *reinterpret_cast<uint4 *>(p + a) = x[u];
+                    *reinterpret_cast<uint4 *>(p + b) = y[u];
+                }
+        }
     }
 }
 
@@ -328,43 +377,57 @@ int run(const Call &c, cudaStream_t stream) {
     job.slots = c.slots;
     job.n_tokens = c.n_tokens;
     job.n_axes = c.n_axes;
-    job.turned = (int)(c.rot * elt / 32);
+    job.pieces = (int)(c.rot * elt / 32);
     job.page = c.page;
     job.n_slots = c.n_slots;
+    job.by_page = Divisor::of(c.page);
     job.status = status_word();
     if (!job.status) return GDN_ERR_CUDA;
-    // warps that share a token's heads: as many as keep lanes busy while tokens alone leave the GPU
-    // short of warps
-    const long long want = 152 * 32;
-    for (int i = 0; i < 3; ++i) {
+    auto rows = [&](int i) {
         const Tensor &a = c.in[i], &b = c.out[i];
-        Rows &r = job.rows[i];
-        int split = 0;
-        if (a.heads) {
-            r.src = static_cast<const uint8_t *>(a.p);
-            r.dst = static_cast<uint8_t *>(const_cast<void *>(b.p));
-            const long long e = (long long)elt;
-            r.src_token = a.token * e;
-            r.src_head = a.head * e;
-            r.dst_token = b.token * e;
-            r.dst_head = b.head * e;
-            r.dst_page = b.page * e;
-            r.heads = a.heads;
-            r.lanes = (int)(a.d * elt / 32);
-            r.per_warp = 32 / r.lanes;
-            const int passes = (a.heads + r.per_warp - 1) / r.per_warp;
-            const long long room = (want + c.n_tokens - 1) / c.n_tokens;
-            split = (int)(room < passes ? room : passes);
-            // no warp without a row of its own
-            split = (passes + (passes + split - 1) / split - 1) / ((passes + split - 1) / split);
-            r.split = split;
-            r.turn = c.turn[i] && turns;
-            r.cache = c.cache[i];
+        const long long e = (long long)elt;
+        return Rows{static_cast<const uint8_t *>(a.p), static_cast<uint8_t *>(const_cast<void *>(b.p)), a.token * e, a.head * e,
+                    b.token * e, b.head * e, b.page * e, a.heads, c.cache[i]};
+    };
+    auto lanes = [&](int d) {
+        const int n = (int)(d * elt / 32);
+        return Lanes{n, 32 / n};
+    };
+    long long warps = 0;
+    int heads = 0, copies = 0;
+    for (int i = 0; i < 2; ++i)
+        if (c.turn[i] && turns) {
+            job.turned[i] = rows(i);
+            heads = c.in[i].heads > heads ? c.in[i].heads : heads;
+            if (c.in[i].heads) job.on = lanes(c.in[i].d);
         }
-        job.begin[i + 1] = job.begin[i] + split;
+    if (heads) {
+        // Few heads: rows of several tokens lie on a warp.  Many: the warps that share a token's are as many as there
+        // are passes over them while tokens alone leave the GPU short of warps.
+        job.heads = heads < job.on.rows ? heads : job.on.rows;
+        job.tokens = job.on.rows / job.heads;
+        const long long groups = (c.n_tokens + job.tokens - 1) / job.tokens, room = (152 * 64 + groups - 1) / groups;
+        const int passes = (heads + job.heads - 1) / job.heads, most = (int)(room < passes ? room : passes);
+        // no warp without a row of its own
+        job.split = (passes + (passes + most - 1) / most - 1) / ((passes + most - 1) / most);
+        job.by_heads = Divisor::of(job.heads);
+        job.by_split = Divisor::of(job.split);
+        warps = groups * job.split;
     }
-    const long long blocks = ((long long)c.n_tokens * job.begin[3] + kWarps - 1) / kWarps;
-    if (blocks > INT_MAX) return GDN_ERR_ARG;
+    job.begin[0] = (int)(warps < INT_MAX ? warps : INT_MAX);
+    for (int i = 0; i < 3; ++i) {
+        if (!c.in[i].heads || (c.turn[i] && turns)) continue;
+        job.copied[copies] = rows(i);
+        const Lanes on = job.on_copied[copies] = lanes(c.in[i].d);
+        job.by_rows[copies] = Divisor::of(c.in[i].heads);
+        const long long n = (long long)c.n_tokens * c.in[i].heads;
+        if (n > INT_MAX) return GDN_ERR_ARG;
+        warps += (n + kRows * on.rows - 1) / (kRows * on.rows);
+        job.begin[++copies] = (int)(warps < INT_MAX ? warps : INT_MAX);
+    }
+    for (; copies < 3; ++copies) job.begin[copies + 1] = job.begin[copies];
+    if (warps > INT_MAX - 32 * kWarps) return GDN_ERR_ARG;
+    const long long blocks = (warps + kWarps - 1) / kWarps;
     const bool inverse = (c.flags & GDN_ROTARY_INVERSE) != 0;
     const int kind = !turns ? 0 : c.flags & GDN_ROTARY_NEIGHBOURS ? 2 : 1;
     cudaError_t e;
