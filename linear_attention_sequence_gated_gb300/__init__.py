@@ -765,13 +765,19 @@ def paged_write(k, v, k_cache, v_cache, slots, *, stream=None):
 
     slots: (n_tokens,) int32 as page_assign gives them (a padded batch's flattened),
     negative: not written; they must differ."""
-    rotary_write(None, k, v, None, None, k_cache, v_cache, slots, stream=stream)
+    _write_rows(None, k, v, None, None, k_cache, v_cache, slots, None, stream)
     return k_cache, v_cache
 
 
 def rotary_write(q, k, v, positions, plan, k_cache, v_cache, slots, *, q_out=None, stream=None):
     """rotary of q and k and paged_write of the turned k and of v, in one launch; returns q_out (default: a new dense
     tensor; may be q itself).  Arguments as for rotary and paged_write."""
+    if q is None or plan is None:
+        raise TypeError("rotary_write takes queries and a plan (paged_write: neither)")
+    return _write_rows(q, k, v, positions, plan, k_cache, v_cache, slots, q_out, stream)
+
+
+def _write_rows(q, k, v, positions, plan, k_cache, v_cache, slots, q_out, stream):
     L, torch = _lib or lib(), _torch or _kv4_torch()
     dtype, dev, ks, vs, cs, ws, i32 = k.dtype, k.get_device(), k.shape, v.shape, k_cache.shape, v_cache.shape, torch.int32
     dt = _KV4_DTYPES.get(dtype)
@@ -789,7 +795,7 @@ def rotary_write(q, k, v, positions, plan, k_cache, v_cache, slots, *, q_out=Non
                  ("v_cache", v_cache, tuple(cs[:1]) + (H,) + tuple(cs[2:3]) + (vs[-1],), dtype, dev),
                  ("slots", slots, (ks[0],), i32, dev)))
     if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _there(dev, stream, rotary_write, q, k, v, positions, plan, k_cache, v_cache, slots, q_out=q_out)
+        return _there(dev, stream, _write_rows, q, k, v, positions, plan, k_cache, v_cache, slots, q_out, None)
     T, H, dk = ks
     rows = pages = None
     if not (k.is_contiguous() and v.is_contiguous()):

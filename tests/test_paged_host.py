@@ -360,7 +360,9 @@ def test_binding_refuses():
             call()
     for call in (lambda: gdn.paged_write(k.double(), k.double(), kc, vc, i32(3)),
                  lambda: gdn.rotary(k.int(), None, i32(3), plan),
-                 lambda: gdn.flash_attn_paged(q.double(), kc, vc, i32(3, 2), i32(3))):
+                 lambda: gdn.flash_attn_paged(q.double(), kc, vc, i32(3, 2), i32(3)),
+                 lambda: gdn.rotary_write(k, k, k, i32(3), None, kc, vc, i32(3)),
+                 lambda: gdn.rotary_write(None, k, k, i32(3), plan, kc, vc, i32(3))):
         with pytest.raises(TypeError):
             call()
 
