@@ -112,9 +112,11 @@ struct Plan {
 
 // CTAs a unit, or 0 for equal runs, by the room that the tables have (the lengths are on the device): what the
 // slowest CTA streams, in bytes, and as bytes the time of what does not overlap it: each wave of CTAs' start and
-// join, 4 us; a cluster's join, 2 us; for runs 8 us once, the second kernel's among them.  A cluster grows while
-// each group of its CTAs has two tiles and more.
-constexpr long long kWaveCost = 160 << 10, kClusterCost = 80 << 10, kRunsCost = 320 << 10;
+// join, 4 us; a cluster's join, 2 us; for runs 11 us once, the second kernel's among them.  A cluster grows while
+// each group of its CTAs has two tiles and more.  Runs adapt to lengths below the tables' room, so clusters have to be
+// ahead by an eighth.  (Runs and clusters, us, 32/8 heads x 128: 1 x 1000 tokens 9.0 and 8.0, 1 x 4000 10.8 and 10.2,
+// 1 x 16000 19.7 and 21.1, 1 x 60000 45 and 60; 16 x 1000 20.9 and 14.5, 38 x 1500 47 and 43.)
+constexpr long long kWaveCost = 160 << 10, kClusterCost = 80 << 10, kRunsCost = 448 << 10;
 bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int max_pages, int elt, Plan *p) {
     p->share = share_of(dk, dv, elt, H / Hkv * n_q);
     const long long units = (long long)n_seqs * Hkv * p->share.units, groups = p->share.groups;
@@ -127,7 +129,7 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     const long long waves = (units * cl + kGrid - 1) / kGrid;
     const long long by_cluster = waves * ((tiles + cl - 1) / cl * stage + kWaveCost + (cl > 1 ? kClusterCost : 0));
     const long long by_runs = (units * steps + kGrid - 1) / kGrid * stage + kRunsCost;
-    p->cluster = by_cluster <= by_runs ? (int)cl : 0;
+    p->cluster = by_cluster + by_cluster / 8 <= by_runs ? (int)cl : 0;
     const long long runs = (units * steps + groups - 1) / groups;
     p->grid = p->cluster ? (int)(units * cl) : (int)(runs < kGrid ? runs : kGrid);
     p->bytes = p->cluster || p->grid < 2 ? 0

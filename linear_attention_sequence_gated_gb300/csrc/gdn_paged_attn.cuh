@@ -1028,6 +1028,8 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                 sl[warp * kBlock + 2 * t + r] = u.l[r];
             }
         consumers_sync();               // (every group is done with the ring, too)
+        if (last && tid == 0)          // the second kernel may be set up meanwhile (0.3 us)
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // half a warp a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output
         for (int row = tid >> 4; row < (valid + 1) / 2 * 2; row += G::THREADS / 16) {
             const int w = tid & 15;
