@@ -441,9 +441,8 @@ int gdn_page_release(const int *page_table, const int *from_lens, const int *to_
  *     (x, y) -> (x cos - y sin, y cos + x sin)
  * where (x, y) are elements j and j + rot_dim / 2, or 2j and 2j + 1 with GDN_ROTARY_NEIGHBOURS.  Elements from
  * rot_dim on are copied.  GDN_ROTARY_INVERSE turns by -angle: the inverse, and the gradient (of q and k
- * from those of q_out and k_out).  Computed in fp32 and rounded once; angles are exact modulo a turn to 2^-31 of
- * it for every 32-bit position (with frequencies of up to one radian a position; beyond that fp64's share of
- * a turn limits them).
+ * from those of q_out and k_out).  Computed in fp32 and rounded once; angles are reduced modulo a turn to 2^-31 of it, whatever
+ * the 32-bit position and the frequency.
  * positions: (n_axes, n_tokens) int32, negative ones too.
  * plan: (rot_dim / 2) entries of 16 bytes in device memory, 16-byte aligned, as gdn_rotary_plan fills them in
  *   host memory from freqs and axes (NULL: all 0).  An axis from n_axes on counts as n_axes - 1.
@@ -463,7 +462,8 @@ int gdn_page_release(const int *page_table, const int *from_lens, const int *to_
  *   v_cache (a cache whose pages are token-major has them so); rows and addresses as above, no two rows of a
  *   cache may overlap.
  *
- * gdn_rotary_write is both in one launch: q is turned into q_out, k on its way into the cache, v is copied.
+ * gdn_rotary_write is both in one launch: q is turned into q_out, k on its way into the cache, v is copied.  flags: 0 or
+ * GDN_ROTARY_NEIGHBOURS (else GDN_ERR_ARG).
  * q_strides: NULL, or token and head strides of q and q_out; kv_strides and cache_strides as for gdn_paged_write.
  */
 #define GDN_ROTARY_NEIGHBOURS 1
@@ -504,8 +504,9 @@ int gdn_rotary_write(const void *q, void *q_out, const void *k, const void *v, c
  * A row that sees no token is zeros.  Tokens that a row does not see (behind its sequence's end, after its own place, hidden
  * by -inf) have no effect on it, whatever their rows hold, NaN and infinities among them.  A mask of the type's
  * lowest finite value takes part in the softmax as the number it is.
- * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 16 bits (bf16) or 22 (f16); fp32 q, k, v
- * and weights with 22 bits (infinite elements of fp32 rows make NaN).  Results do not depend on timing.
+ * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 22 bits (f16), 24 (bf16, out_dtype fp32)
+ * or 16 (bf16, 16-bit out); fp32 q, k, v and weights with 22 bits (infinite elements of fp32 rows make NaN).  Results
+ * do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), head_dim_k and head_dim_v each 64, 128 or 256 (else
  *   GDN_ERR_HEADDIM; gdn_flash_attn_paged_supports), page_size a multiple of 16 (else GDN_ERR_SHAPE), n_heads_kv
  *   dividing n_heads, tables with room for fewer than 2^31 tiles of 16 tokens over all sequences, kv heads

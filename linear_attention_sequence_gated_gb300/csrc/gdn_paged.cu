@@ -465,6 +465,20 @@ Tensor cache_of(void *p, const long long *strides, int n_pages, int heads, int p
     return t;
 }
 
+// x modulo 1 in units of 2^-64, toward zero.
+uint64_t fraction(double x) {
+    x -= std::round(x);
+    if (x >= 0.5) x -= 1.0;
+    return (uint64_t)(int64_t)std::ldexp(x, 64);
+}
+// A frequency as a fraction of a turn, to 2 units of 2^-64: 1 / (2 pi) and the product are sums of two doubles
+// (a position of 2^31 would make 2^-24 of a turn of one double's rounding).
+uint64_t turn_of(double freq) {
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+    const double x = freq * hi;
+    return fraction(x) + fraction(std::fma(freq, hi, -x) + freq * lo);
+}
+
 int cache_sizes(int n_pages, int page_size) {
     if (n_pages < 0) return GDN_ERR_ARG;
     if (page_size < 1) return GDN_ERR_SHAPE;
@@ -483,9 +497,7 @@ int gdn_rotary_plan(const double *freqs, const int *axes, int n, void *plan) {
         if (!std::isfinite(freqs[i]) || (axes && axes[i] < 0)) return GDN_ERR_ARG;
     uint32_t *out = static_cast<uint32_t *>(plan);
     for (int i = 0; i < n; ++i) {
-        const double turns = freqs[i] * 0.15915494309189533576888376337251436;   // 1 / (2 pi)
-        const double part = turns - std::floor(turns);
-        const uint64_t f = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;      // (1: just below a whole turn)
+        const uint64_t f = gdn::paged::turn_of(freqs[i]);
         out[4 * i] = (uint32_t)f;
         out[4 * i + 1] = (uint32_t)(f >> 32);
         out[4 * i + 2] = axes ? (uint32_t)axes[i] : 0u;

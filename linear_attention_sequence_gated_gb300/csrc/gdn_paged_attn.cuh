@@ -151,7 +151,7 @@ struct Geo {
     static constexpr int QBLOCK = R.q_block, RING = R.pool - MOST * QBLOCK;    // (the least that a ring has)
     static constexpr int SMEM = 1024 + R.pool + R.merge + R.weights + R.sums;
     static_assert(RING / STAGE >= 4, "ring");
-    static_assert(17 * kMaxRing + 160 + (8 + 4 * kMaxCluster) * MOST * kBlock <= 3072, "barriers and the like");
+    static_assert(17 * kMaxRing + 160 + (8 + 4 * kMaxCluster) * MOST * kBlock <= (3 << 10), "barriers and the like");
     static_assert(R.merge % 16 == 0 && QROW % 16 == 0 && R.weights % 16 == 0 && DV % MC == 0, "alignment");
     static_assert(WARPS * kBlock * (DV + 4) * 4 <= RING / STAGE / 4 * 4 * STAGE, "the last unit is joined in the ring");
 };

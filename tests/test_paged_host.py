@@ -9,6 +9,7 @@ import math
 import os
 import re
 import subprocess
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -87,6 +88,19 @@ def test_plan_holds_the_turns_of_each_frequency():
                      3 / (2 * math.pi), (-7 / (2 * math.pi)) % 1])
     off = np.abs(turns - want)
     assert (np.minimum(off, 1 - off) <= 2.0 ** -48).all()
+
+
+def test_plan_is_exact_to_64_bits():
+    """A 32-bit position multiplies what a frequency's share of a turn is off by."""
+    turn = Fraction("0.1591549430918953357688837633725143620344596457404564487476673440588968")      # 1 / (2 pi)
+    rng = np.random.default_rng(5)
+    freqs = [0.0, 1.0, -1.0, 0.1, 1e-4, -3e-7, 1e-20, -1e-30, 5e-324, 2 * math.pi, -2 * math.pi, math.pi, 12345.678, -1e9] + \
+        [1e6 ** (-j / 8) for j in range(8)] + list(rng.standard_normal(42))
+    plan = gdn.rotary_plan(128, freqs=freqs, device="cpu").data.numpy().view(np.uint64)
+    for f, p in zip(freqs, plan[:, 0]):
+        off = (int(p) - turn * Fraction(f) * 2 ** 64) % 2 ** 64
+        # two truncations; the second double's rounding, 2^-106 of the turns, and its product's are far below
+        assert min(off, 2 ** 64 - off) <= 2 + abs(f) * 2.0 ** -40, f
 
 
 def test_plan_deals_axes_and_refuses():
