@@ -363,3 +363,57 @@ def test_offsets_past_32_bits(dtype):
     used = table.flatten().long()
     ref = paged.attend(np64(q), np64(kc[used]), np64(vc[used]), np.arange(6).reshape(2, 3), [600, 700])
     assert oracle.parity_error(np64(got), ref) <= TOL
+
+
+@pytest.mark.parametrize("room", [0, 300])
+def test_thousands_of_sequences(room):
+    """Sums over more sequences than a CTA has threads, in runs (room) and in CTAs a unit."""
+    lens = [(37 * b) % 90 if b % 5 else 0 for b in range(1500)] + [900, 0, 3]
+    Case(lens, 4, 2, 2, 64, page=16, seed=31, room=room).check(causal=True)
+
+
+def test_masks_past_32_bits():
+    """Mask rows more than 2^31 elements into the mask of long tables."""
+    B, room, page, d = 65, 1 << 21, 16, 64
+    c = Case([40] * B, 4, 1, 1, d, page=page, seed=32)
+    table = torch.full((B, room), -1, dtype=torch.int32, device="cuda")
+    table[:, :3] = c.table
+    mask = torch.zeros((B, 1, 1, room * page), dtype=torch.bfloat16, device="cuda")
+    assert mask.numel() > 2 ** 31
+    mask[:, :, :, :48] = c.mask()
+    ref = paged.attend(np64(c.q), np64(c.kc), np64(c.vc), c.table.cpu().numpy(), c.lens_l, np64(mask[:, :, :, :48]))
+    got = gdn.flash_attn_paged(c.q, c.kc, c.vc, table, c.lens, mask)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == gdn.OK and oracle.parity_error(np64(got), ref) <= TOL
+
+
+def test_captured_calls_follow_the_lengths():
+    """Two graphs with the library's own workspace, replayed in turn (and both at once) while lengths grow."""
+    c = Case([4000, 3000, 100, 2500], 16, 4, 1, 128, seed=33, room=200)
+    lens = c.lens.clone()
+    graphs = []
+    for _ in range(2):
+        c.run()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = c.run()
+        graphs.append((g, out))
+    for step, now in enumerate(([1, 2, 3, 4], [0, 3000, 0, 1], [4000, 17, 100, 2500], [0, 0, 0, 0], [100, 2999, 64, 16])):
+        c.lens.copy_(i32(now))
+        want = c.run()
+        g, out = graphs[step % 2]
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    c.lens.copy_(lens)
+    want = c.run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for _, out in graphs)
+    c.check()
