@@ -541,57 +541,59 @@ struct Unit {
             }
         }
     }
+    // Whether any value of the tile is not finite: 0 times it is NaN.
     __device__ __forceinline__ static bool any_odd(const uint8_t *v, int lane) {
-        // 0 times what is not finite is NaN
-        using T2 = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
-        float acc = 0.f;
-        uint32_t acc2 = 0;
-#pragma unroll 4
-        for (int i = 0; i < G::VB / 512; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(v + (i * 32 + lane) * 16);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (MMA16) {
+            const uint32_t at = ptx::smem_u32(v) + ((lane & 7) + ((lane >> 4) << 3)) * 128, sw = lane & 7, half = (lane >> 3) & 1;
+            float d[2][4] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (MMA16) {
-                    const uint32_t zero = 0;
-                    const T2 r = __hfma2(*reinterpret_cast<const T2 *>(&u[e]), *reinterpret_cast<const T2 *>(&zero),
-                                         *reinterpret_cast<const T2 *>(&acc2));
-                    acc2 = *reinterpret_cast<const uint32_t *>(&r);
-                } else {
-                    acc = fmaf(__uint_as_float(u[e]), 0.f, acc);
-                }
+            for (int i = 0; i < MT; ++i) {
+                uint32_t A[4];
+                ldsm4_t(A, at + (i >> 2) * 2048 + (((2 * (i & 3) + half) ^ sw) << 4));
+                mma<T>(d[i & 1], A, 0u, 0u);
             }
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += d[0][e] + d[1][e];
+            return __any_sync(0xffffffffu, sum != sum);
+        } else {
+            float acc[4] = {};
+#pragma unroll 4
+            for (int i = 0; i < G::VB / 512; ++i) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(v + (i * 32 + lane) * 16);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(__uint_as_float(u[e]), 0.f, acc[e]);
+            }
+            const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            return __any_sync(0xffffffffu, sum != sum);
         }
-        return __any_sync(0xffffffffu, MMA16 ? (acc2 & 0x7fff7fffu) != 0 : acc != acc);
     }
 
     // The tile in `stage`, tokens pos .. pos + 15 of the sequence.
     __device__ __forceinline__ void tile(const Attn &a, const uint8_t *stage, int pos, const uint8_t *sq, float *pt, int lane) {
         const int g = lane >> 2, t = lane & 3;
         float s[4], x[4], cf[2], add[4];
-        if (a.mask) {                  // loaded ahead of the products
+        // tokens of the tile, from this lane's on, that a row sees
+        auto seen = [&](int r) {
+            return (qi[r] < 0 ? 0 : a.causal ? min(len, raw - a.n_q + 1 + qi[r]) : len) - pos - g;
+        };
+        if (a.mask)                    // loaded ahead of the products
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = qi[e & 1], j = pos + g + 8 * (e >> 1);
-                add[e] = i >= 0 && j < len
-                             ? to_float<T>(static_cast<const T *>(a.mask)[((size_t)b * a.n_q + i) * (size_t)capacity(a) + j])
-                             : -INFINITY;
+            for (int r = 0; r < 2; ++r) {
+                const T *p = static_cast<const T *>(a.mask) + ((size_t)b * a.n_q + qi[r]) * (size_t)capacity(a) + pos + g;
+                add[r] = seen(r) > 0 ? to_float<T>(p[0]) : -INFINITY;
+                add[r + 2] = seen(r) > 8 ? to_float<T>(p[8]) : -INFINITY;
             }
-        }
         scores(ptx::smem_u32(stage), sq, lane, s);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = s[e] * a.scale;
         const bool plain = pos + kTile <= all;
         if (!plain) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = qi[r];
-                const long long lim = a.causal ? min((long long)len, (long long)raw - a.n_q + 1 + i) : len;
-#pragma unroll
-                for (int e = r; e < 4; e += 2) {
-                    if (i < 0 || pos + g + 8 * (e >> 1) >= lim) x[e] = -INFINITY;
-                    else if (a.mask) x[e] = add[e] == -INFINITY ? -INFINITY : x[e] + add[e];
-                }
+            for (int e = 0; e < 4; ++e) {
+                if (a.mask) x[e] = add[e] == -INFINITY ? -INFINITY : x[e] + add[e];
+                else if (seen(e & 1) <= 8 * (e >> 1)) x[e] = -INFINITY;
             }
         }
         float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
