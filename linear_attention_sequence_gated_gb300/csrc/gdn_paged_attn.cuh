@@ -151,7 +151,7 @@ struct Geo {
     static constexpr int THREADS = WARPS * 32, ALL = THREADS + 32 * kFillers;
     // Registers a thread: the launch's, and after the warps that fill the ring have given theirs up.
     static constexpr int REGS = WARPS == 12 ? 128 : 168;
-    static constexpr int FILL_REGS = 56, WORK_REGS = WARPS == 12 ? 152 : 224;
+    static constexpr int FILL_REGS = WARPS == 12 || E == 4 ? 56 : 72, WORK_REGS = WARPS == 12 ? 152 : E == 4 ? 224 : 216;
     static_assert(WARPS % 4 == 0 && THREADS * WORK_REGS + 32 * kFillers * FILL_REGS <= ALL * REGS,
                   "a split of more registers than the launch has would wait forever");
     static constexpr Room R = room_of(DK, DV, E, WARPS, MOST);
