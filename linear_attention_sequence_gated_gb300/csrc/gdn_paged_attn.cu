@@ -112,10 +112,13 @@ struct Plan {
 
 // CTAs a unit, or 0 for equal runs, by the room that the tables have (the lengths are on the device): what the
 // slowest CTA streams, in bytes, and as bytes the time of what does not overlap it: each wave of CTAs' start and
-// join, 4 us; a cluster's join, 2 us; for runs 11 us once, the second kernel's among them.  A cluster grows while
-// each group of its CTAs has two tiles and more.  Runs adapt to lengths below the tables' room, so clusters have to be
-// ahead by an eighth.  (Runs and clusters, us, 32/8 heads x 128: 1 x 1000 tokens 9.0 and 8.0, 1 x 4000 10.8 and 10.2,
+// join, 4 us; a cluster's join, 2 us; for runs 11 us once, the second kernel's among them.  Each group of a
+// cluster's CTAs has a tile at least.  One CTA fits on an SM, and fewer clusters fit on the GPU's partitions than
+// SMs allow for (16 clusters of 8 x 250 tiles of 16 KB are two waves: 29 us, in runs 19).  Runs adapt to lengths below the
+// tables' room, so clusters have to be ahead by an eighth.  (Runs and clusters, us, 32/8 heads x 128: 1 x 1000 tokens 9.0 and 8.0, 1 x 4000 10.8 and 10.2,
 // 1 x 16000 19.7 and 21.1, 1 x 60000 45 and 60; 16 x 1000 20.9 and 14.5, 38 x 1500 47 and 43.)
+constexpr int kAtOnce[4] = {kGrid, 76, 36, 15};        // clusters of 1, 2, 4 and 8 CTAs
+static_assert(kMaxCluster == 8, "sizes");
 constexpr long long kWaveCost = 160 << 10, kClusterCost = 80 << 10, kRunsCost = 448 << 10;
 bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int max_pages, int elt, Plan *p) {
     p->share = share_of(dk, dv, elt, H / Hkv * n_q);
@@ -124,10 +127,14 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     const long long steps = tiles ? tiles + kUnitCost : 0;
     if (units > INT_MAX || steps > INT_MAX || (steps > 0 && units > INT_MAX / steps)) return false;
     const long long stage = (long long)kTile * (dk + dv) * elt;
-    long long cl = 1;
-    while (cl < kMaxCluster && units * cl * 2 <= kGrid && tiles > cl * groups * 2) cl *= 2;
-    const long long waves = (units * cl + kGrid - 1) / kGrid;
-    const long long by_cluster = waves * ((tiles + cl - 1) / cl * stage + kWaveCost + (cl > 1 ? kClusterCost : 0));
+    long long cl = 1, by_cluster = 0;
+    for (int i = 0; i < 4; ++i) {
+        const long long c = 1ll << i, waves = (units + kAtOnce[i] - 1) / kAtOnce[i];
+        const long long cost = waves * ((tiles + c - 1) / c * stage + kWaveCost + (i ? kClusterCost : 0));
+        if (i && (tiles <= c * groups || cost >= by_cluster)) continue;
+        by_cluster = cost;
+        cl = c;
+    }
     const long long by_runs = (units * steps + kGrid - 1) / kGrid * stage + kRunsCost;
     p->cluster = by_cluster + by_cluster / 8 <= by_runs ? (int)cl : 0;
     const long long runs = (units * steps + groups - 1) / groups;
