@@ -149,7 +149,8 @@ struct Geo {
     static constexpr int BOX = 128 / E;                // elements of a box's row
     static constexpr int KB = kTile * DK * E, VB = kTile * DV * E, STAGE = KB + VB;
     static constexpr int THREADS = WARPS * 32, ALL = THREADS + 32 * kFillers;
-    // Registers a thread: the launch's, and after the warps that fill the ring have given theirs up.
+    // Registers a thread: the launch's, and after the warps that fill the ring have given theirs up.  (Those keep 72 beside
+    // 16-bit rows of 256, which spill with 56: 8 x 16/2 heads x 4000 x 256 f16 28.7 and 31.6 us; fp32 rows need the 224.)
     static constexpr int REGS = WARPS == 12 ? 128 : 168;
     static constexpr int FILL_REGS = WARPS == 12 || E == 4 ? 56 : 72, WORK_REGS = WARPS == 12 ? 152 : E == 4 ? 224 : 216;
     static_assert(WARPS % 4 == 0 && THREADS * WORK_REGS + 32 * kFillers * FILL_REGS <= ALL * REGS,
