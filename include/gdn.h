@@ -504,9 +504,8 @@ int gdn_rotary_write(const void *q, void *q_out, const void *k, const void *v, c
  * A row that sees no token is zeros.  Tokens that a row does not see (behind its sequence's end, after its own place, hidden
  * by -inf) have no effect on it, whatever their rows hold, NaN and infinities among them.  A mask of the type's
  * lowest finite value takes part in the softmax as the number it is.
- * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 22 bits (f16), 24 (bf16, out_dtype fp32)
- * or 16 (bf16, 16-bit out); fp32 q, k, v and weights with 22 bits (infinite elements of fp32 rows make NaN).  Results
- * do not depend on timing.
+ * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 22 bits (f16) or 24 (bf16);
+ * fp32 q, k, v and weights with 22 bits (infinite elements of fp32 rows make NaN).  Results do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), head_dim_k and head_dim_v each 64, 128 or 256 (else
  *   GDN_ERR_HEADDIM; gdn_flash_attn_paged_supports), page_size a multiple of 16 (else GDN_ERR_SHAPE), n_heads_kv
  *   dividing n_heads, tables with room for fewer than 2^31 tiles of 16 tokens over all sequences, kv heads

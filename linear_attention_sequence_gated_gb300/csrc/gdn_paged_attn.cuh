@@ -14,8 +14,8 @@
 //   * Each tile goes to one group of the 8 or 12 warps that compute, where every warp takes another 8 rows.  Those
 //     warps get the registers that the others give up.
 //   * 16-bit rows: S^T = K Q^T (M = 16 tokens, N = 8 rows) and O^T += V^T P^T (M = 16 elements,
-//     N = 8 rows, K = 16 tokens) by m16n8k16 MMAs with fp32 accumulators, the weights as two 16-bit terms, or three of
-//     bf16 where the outputs are fp32 (f16: 22 bits, bf16: 24, else 16), transposed in registers by movmatrix.  Up to 4
+//     N = 8 rows, K = 16 tokens) by m16n8k16 MMAs with fp32 accumulators, the weights as two terms of f16 (22 bits) or
+//     three of bf16 (24), transposed in registers by movmatrix.  Up to 4
 //     rows, the second terms stand in the columns that no row needs.
 //   * fp32 rows: the same by m16n8k8 tf32 MMAs, each operand as hi + lo (22 bits), three products.
 //   * Scores, maxima, sums and outputs are fp32; each tile's products reach the outputs by one
@@ -623,20 +623,20 @@ struct Unit {
             return;
         }
         if constexpr (MMA16) {
-            // Weights as 16-bit terms, largest first: two, and a third of bf16 where the outputs are fp32.  In
-            // COLS the second stands in columns 4 .. 7 of the first's products, where the rows' queries stand again.
-            constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-            const bool third = BF && a.out_type == GDN_DTYPE_F32;
+            // Weights as 16-bit terms, largest first: two of f16 (22 bits), three of bf16 (24; two, 16 bits, would show in
+            // outputs of bf16: one value in a thousand rounded to its neighbour).  In COLS the second stands in columns
+            // 4 .. 7 of the first's products, where the rows' queries stand again.
+            constexpr bool third = std::is_same<T, __nv_bfloat16>::value;
             uint32_t p1[2], p2[2], p3[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float y = s[2 * h], z = s[2 * h + 1];
                 p1[h] = round2<T>(y, z);
                 p2[h] = round2<T>(y, z);
-                if constexpr (BF) p3[h] = third ? round2<T>(y, z) : 0u;
+                if constexpr (third) p3[h] = round2<T>(y, z);
                 if constexpr (COLS) {
                     p1[h] = t >= 2 ? p2[h] : p1[h];
-                    if constexpr (BF) p2[h] = t >= 2 ? 0u : p3[h];
+                    if constexpr (third) p2[h] = t >= 2 ? 0u : p3[h];
                 }
                 p1[h] = transpose8(p1[h]);
                 if (!COLS || third) p2[h] = transpose8(p2[h]);
