@@ -797,7 +797,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     float *sl = sm + (WARPS + MOST) * kBlock;                              // ... and sums
     __shared__ uint64_t full[kMaxRing], empty[kMaxRing];
     __shared__ uint8_t none[kMaxRing];
-    __shared__ int part[32], start[2], gave_up;
+    __shared__ int part[32], start[2], gave_up, never;
     __shared__ long long place[MOST * kBlock];
     __shared__ float shares[kMaxCluster][MOST * kBlock];
 
@@ -806,7 +806,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     const int group = warp / a.blocks, block = warp - group * a.blocks;
     const bool works = group < a.groups;
     if (tid == 0) {
-        gave_up = 0;
+        gave_up = never = 0;
         for (int s = 0; s < a.ring; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], a.blocks);
@@ -960,6 +960,13 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
             skip = tile - w.end;       // tiles go on in order over the segments
             more = more && w.next(a);
         }
+        // Copies land before the CTA can exit, whether those who wanted them still wait or gave up: the last use of each
+        // of this warp's stages, in this lap or the one before.
+        for (int i = who; i < a.ring; i += kFillers)
+            if (!ptx::mbar_wait(&full[i], i < s ? phase : phase ^ 1, &never)) {
+                *a.status = GDN_ERR_TIMEOUT;
+                break;
+            }
         if (a.cluster > 1) {
             cluster_sync();
             cluster_sync();
