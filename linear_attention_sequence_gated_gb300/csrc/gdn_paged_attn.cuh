@@ -797,7 +797,9 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     float *sl = sm + (WARPS + MOST) * kBlock;                              // ... and sums
     __shared__ uint64_t full[kMaxRing], empty[kMaxRing];
     __shared__ uint8_t none[kMaxRing];
-    __shared__ int part[32], start[2], gave_up, never;
+    __shared__ int part[32], start[2];
+    __shared__ int gave_up, never;     // (gave_up: a hint to other waits that they need not run out too)
+    __shared__ volatile int lost;      // tiles are missing: set by warps that compute, ahead of a barrier that all of them pass
     __shared__ long long place[MOST * kBlock];
     __shared__ float shares[kMaxCluster][MOST * kBlock];
 
@@ -807,6 +809,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
     const bool works = group < a.groups;
     if (tid == 0) {
         gave_up = never = 0;
+        lost = 0;
         for (int s = 0; s < a.ring; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], a.blocks);
@@ -1006,6 +1009,7 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                 dead = __any_sync(0xffffffffu, !ptx::mbar_wait(&full[s], phase, &gave_up));
                 if (dead) {
                     gave_up = 1;
+                    lost = 1;
                     *a.status = GDN_ERR_TIMEOUT;
                 }
             }
@@ -1030,15 +1034,13 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
         const int g = lane >> 2, t = lane & 3;
         const bool whole = run.begin == 0 && run.end == run.n, mine = works && !(COLS && t >= 2);
         const int rows = a.blocks * kBlock, valid = COLS ? 4 : rows;
-        const bool last = !more && !dead, final = whole && a.cluster < 2;
+        const bool final = whole && a.cluster < 2;
         float *part_out = whole || a.cluster ? nullptr
                                              : a.ws + partial_slot(cta, run.begin == 0) * partial_size(rows, DV);
         if (part_out && run.begin == 0 && tid == 0) {  // the runs up to that of the unit's last step go on with it
             const int end = run_begin(total, runs, cta + 1) + run.n + kUnitCost - run.to;
             open_of(a, gridDim.x, DV)[cta] = {run.b, run.j, run_of(total, runs, end - 1) - cta + 1, 0};
         }
-        const int width = last ? DV : G::MC, pitch = width + 4;
-        float *parts = last ? reinterpret_cast<float *>(ring) : merge;
         if (g == 0 && mine)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -1046,6 +1048,13 @@ attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUte
                 sl[warp * kBlock + 2 * t + r] = u.l[r];
             }
         consumers_sync();               // (every group is done with the ring, too)
+        // The same answer for all of them, whichever warp's wait it was that gave up: how many barriers follow goes by it.
+        // Then copies into the ring may still be under way, and nobody waits for a stage any more: in the next segment it
+        // could be another group's, which has not seen its last use end.
+        dead = lost;
+        const bool last = !more && !dead;
+        const int width = last ? DV : G::MC, pitch = width + 4;
+        float *parts = last ? reinterpret_cast<float *>(ring) : merge;
         if (last && tid == 0)          // the second kernel may be set up meanwhile (0.3 us)
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // half a warp a row: the parts' factors in place of their maxima, 1 / sum among them where they make the output

@@ -54,7 +54,27 @@ def test_copies_land_before_their_warp_ends(X, name):
     """Whoever else waits for them: a CTA whose other warps gave up must not exit under copies into its memory."""
     c = case_of(name)
     want = c.run()
-    assert X.look_at(1) == 0 and torch.equal(run(X, c), want)
+    assert X.look_at(1, -1, 0) == 0 and torch.equal(run(X, c), want)
     unseen = ctypes.c_int(-1)
     assert X.stages(ctypes.byref(unseen)) >= 4 and unseen.value == 0
     assert gdn.device_status() == gdn.OK
+
+
+@pytest.mark.parametrize("name", list(CASES))
+@pytest.mark.parametrize("warp", range(0, 16))
+@pytest.mark.parametrize("lives", [0, 1, 7])
+def test_a_wait_that_gives_up_ends_the_call(X, name, warp, lives):
+    """Whichever warp's it is, the others agree on how to end: the call is over at once, the status word says so, no copy is
+    left under way, and the next call is as ever."""
+    c = case_of(name)
+    want = c.run()
+    torch.cuda.synchronize()
+    assert gdn.device_status() == gdn.OK
+    assert X.look_at(1, warp, lives) == 0
+    run(X, c)
+    lost, unseen = X.was_lost(), ctypes.c_int(-1)
+    assert X.stages(ctypes.byref(unseen)) >= 0 and unseen.value == 0
+    # (a warp without so many tiles has lost nothing; the first one has some)
+    assert lost in (0, 1) and (lost or warp > 0 or lives > 0)
+    assert gdn.device_status() == (gdn.ERR_TIMEOUT if lost else gdn.OK)
+    assert torch.equal(c.run(), want)
