@@ -410,7 +410,8 @@ size_t gdn_flash_attn_kv4_workspace_bytes(int n_seqs, int n_heads, int n_heads_k
  *   there is none.  token_offsets NULL: (n_seqs, n_new), token i of sequence b at b * n_new + i.  Otherwise
  *   token_offsets is (n_seqs + 1) int32, written: sums of new_lens from 0 on, and slots and positions are
  *   (n_tokens), token i of sequence b at token_offsets[b] + i.
- * GDN_ERR_PAGE in the device status word, with every buffer left in order: the stack runs out (the
+ * GDN_ERR_PAGE in the device status word, with every buffer left in order: a new_lens entry above n_new (what it is
+ *   clamped by counts as there before the step), the stack runs out (the
  *   pages that are left go to the first that need them, the other entries and slots are -1), a length above
  *   max_pages * page_size (tokens behind have no slot), more packed tokens than n_tokens (the rest is not
  *   written), a slot in a page outside [0, n_pages) (-1), a count outside [0, n_pages] (clamped).

@@ -568,18 +568,19 @@ def _strides(*xs):
     return (ctypes.c_longlong * len(v))(*v)
 
 
-def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_new: int = 1, new_lens=None, *,
+def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_new=None, new_lens=None, *,
                 n_tokens=None, slots=None, positions=None, offsets=None, stream=None):
     """Pages, slots and positions for a step's new tokens; returns (slots, positions, offsets).
 
     page_table (n_seqs, max_pages), seq_lens (n_seqs), free_pages (n_pages),
-    free_count (1), new_lens (n_seqs) or None (n_new each): int32.  seq_lens count
-    the new tokens.  Pages that they are the first to need leave the stack
+    free_count (1), new_lens (n_seqs, at most n_new each) or None (n_new each): int32.
+    n_new defaults to 1, or to n_tokens where that and new_lens are given (as far as n_seqs times
+    it is below 2^31).  seq_lens count the new tokens.  Pages that they are the first to need leave the stack
     free_pages[:free_count] from its end and enter the table; free_count and the
     table are updated in place.  Without ``n_tokens`` slots and positions are
     (n_seqs, n_new), -1 and 0 where there is no token, and offsets is None; with it
     they are packed, (n_tokens,), sequence b's from offsets[b] on, offsets
-    (n_seqs + 1).  A stack that runs out, and whatever else only the device can
+    (n_seqs + 1).  A stack that runs out, a new_lens entry above n_new, and whatever else only the device can
     see, shows as ERR_PAGE in device_status().  The rest of the contract is with
     gdn_page_assign in include/gdn.h."""
     L, torch = _lib or lib(), _torch or _kv4_torch()
@@ -597,6 +598,8 @@ def page_assign(page_table, seq_lens, free_pages, free_count, page_size: int, n_
         _refuse((("page_table", page_table, (None, None), i32, dev), ("seq_lens", seq_lens, (B,), i32, dev),
                  ("free_pages", free_pages, (None,), i32, dev), ("free_count", free_count, (1,), i32, dev),
                  ("new_lens", new_lens, (B,), i32, dev)))
+    if n_new is None:
+        n_new = 1 if not packed or new_lens is None else min(n_tokens, 0x7fffffff // max(B, 1))
     if stream is not None or torch._C._cuda_getDevice() != dev:
         return _there(dev, stream, page_assign, page_table, seq_lens, free_pages, free_count, page_size, n_new, new_lens,
                       n_tokens=n_tokens, slots=slots, positions=positions, offsets=offsets)

@@ -117,7 +117,7 @@ __device__ __forceinline__ Seq seq_of(const Step &s, int b, bool *past) {
     q.first = raw - q.n;
     q.after = pages_of(min(raw, cap), s.page);
     q.held = min(pages_of(q.first, s.page), q.after);
-    *past = raw > cap;
+    *past = raw > cap || (s.counts && s.counts[b] > s.n_new);
     return q;
 }
 

@@ -24,7 +24,7 @@ def assign(table, lens, new, free, page, n_new, n_tokens=None):
     for b in range(len(lens)):
         n = n_new if new is None else min(max(int(new[b]), 0), n_new)
         size = max(int(lens[b]), 0)
-        ok &= size <= cap
+        ok &= size <= cap and (new is None or int(new[b]) <= n_new)
         held = -(-max(size - n, 0) // page)
         for j in range(held, -(-min(size, cap) // page)):
             if free:
