@@ -289,11 +289,13 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const Release s) {
         all += x;
     }
     cluster_sync();                    // every thread has read the count and its peers' shares
-    bad |= all != given || count + all > s.n_pages;
+    // (64 bits: the stack and the entries may be 2^31 - 1 each)
+    const long long full = (long long)count + all;
+    bad |= all != given || full > s.n_pages;
     for (int base = lo, turn = 1; base < hi; base += kBatch, turn ^= 1) {
         if (hi - lo > kBatch) n = load(base + tid * kRun, page);       // (else they are here already)
         int sum;
-        int at = count + all - 1 - before - block_scan(n, part[turn], &sum);
+        long long at = full - 1 - before - block_scan(n, part[turn], &sum);
 #pragma unroll
         for (int u = 0; u < kRun; ++u)
             if (page[u] >= 0) {
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const Release s) {
         before += sum;
     }
     if (bad) *s.status = GDN_ERR_PAGE;
-    if (rank == 0 && tid == 0) *s.count = min(count + all, s.n_pages);
+    if (rank == 0 && tid == 0) *s.count = (int)min(full, (long long)s.n_pages);
 }
 
 cudaError_t launch_cluster(const Release &args, long long items, size_t smem, cudaStream_t stream) {

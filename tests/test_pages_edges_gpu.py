@@ -49,3 +49,14 @@ def test_more_new_tokens_than_allowed_show(packed, B):
     lens = [2 + n for n in new]
     p.assign(lens, 2, new, 2 * B + 1 if packed else None, ok=False)
     p.assign([n + 2 for n in lens], 2, ok=True)
+
+
+def test_as_many_entries_as_a_full_stack_holds():
+    """The stack's entries and those given back are 2^31 together: nothing fits, and nothing is written anywhere."""
+    n = 1 << 30
+    table = torch.zeros((1, n), dtype=torch.int32, device="cuda")
+    both = torch.full((n + 1024,), -5, dtype=torch.int32, device="cuda")
+    free, count = both[512:512 + n], i32([n])
+    gdn.page_release(table, i32([n]), free, count, 1)
+    assert gdn.device_status() == gdn.ERR_PAGE and int(count) == n
+    assert all(bool((x == -5).all()) for x in both.split(1 << 28))
