@@ -452,7 +452,8 @@ int gdn_page_release(const int *page_table, const int *from_lens, const int *to_
  *   k; any other overlap of an output is GDN_ERR_ALIAS, except that tensors of one token stride may take turns
  *   in a buffer (the heads of a joint projection).
  * head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up to head_dim (0: copies), else GDN_ERR_HEADDIM.
- * n_heads or n_heads_kv may be 0 (and the pointers NULL).  All rows of one dtype: GDN_DTYPE_F32, _BF16, _F16.
+ * n_heads or n_heads_kv may be 0 (and the pointers NULL).  All rows of one dtype: GDN_DTYPE_F32, _BF16, _F16.  n_tokens up
+ * to 2^31 - 33 (here and below), and n_tokens * heads of tensors that are copied up to 2^31 - 1, else GDN_ERR_ARG.
  *
  * gdn_paged_write copies token t's rows of k (n_tokens, n_heads_kv, head_dim_k) and v to the slot slots[t] (as
  * gdn_page_assign gives them) of k_cache (n_pages, n_heads_kv, page_size, head_dim_k) and v_cache (...,

@@ -331,7 +331,7 @@ int run(const Call &c, cudaStream_t stream) {
     using namespace host;
     if (c.dtype != GDN_DTYPE_F32 && c.dtype != GDN_DTYPE_BF16 && c.dtype != GDN_DTYPE_F16) return GDN_ERR_ARG;
     const unsigned long long elt = c.dtype == GDN_DTYPE_F32 ? 4 : 2;
-    if (c.n_tokens < 0) return GDN_ERR_ARG;
+    if (c.n_tokens < 0 || c.n_tokens > INT_MAX - 32) return GDN_ERR_ARG;     // (a warp's tokens may end 31 behind the last)
     bool any = false, turns = false, caches = false;
     for (int i = 0; i < 3; ++i) {
         const Tensor &t = c.in[i];

@@ -1,0 +1,15 @@
+"""Sizes at the end of 32 bits that the calls of the 16- and 32-bit paged cache must refuse, without a GPU.  The addresses are
+made up: none of these calls reaches a launch.
+"""
+import pytest
+
+import linear_attention_sequence_gated_gb300 as gdn
+from test_paged_host import BASE, L, attend, turn  # noqa: F401
+
+FAR = dict(q=1 << 45, qo=1 << 46, k=None, ko=None, pos=1 << 47, plan=BASE)
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 31])
+def test_tokens_whose_last_warp_would_pass_32_bits(L, T):  # noqa: F811
+    """A warp takes up to 32 rows of 32 bytes, so the last one's tokens end up to 31 behind the last token."""
+    assert turn(L, T=T, H=1, Hk=0, d=16, r=16, **FAR) == gdn.ERR_ARG
