@@ -512,8 +512,8 @@ int gdn_rotary_write(const void *q, void *q_out, const void *k, const void *v, c
  * sum: sums of seen values beyond fp32's range are infinite.  Results do not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), head_dim_k and head_dim_v each 64, 128 or 256 (else
  *   GDN_ERR_HEADDIM; gdn_flash_attn_paged_supports), page_size a multiple of 16 (else GDN_ERR_SHAPE), n_heads_kv
- *   dividing n_heads, tables with room for fewer than 2^31 tiles of 16 tokens over all sequences, kv heads
- *   and blocks of rows.  out must not overlap an input.
+ *   dividing n_heads, tables with room for no more than 2^31 - 17 tiles of 16 tokens, and 16 tiles more for each table,
+ *   over all sequences, kv heads and blocks of rows.  out must not overlap an input.
  * workspace: as for gdn_flash_attn_kv4, gdn_flash_attn_paged_workspace_bytes of it (0 where the call needs none).
  */
 int gdn_flash_attn_paged(const void *q, const long long *q_strides, const void *k_cache, const void *v_cache,

@@ -125,7 +125,8 @@ bool plan_of(int n_seqs, int H, int Hkv, int n_q, int dk, int dv, int page, int 
     const long long units = (long long)n_seqs * Hkv * p->share.units, groups = p->share.groups;
     const long long tiles = ((long long)max_pages * page + kTile - 1) / kTile;
     const long long steps = tiles ? tiles + kUnitCost : 0;
-    if (units > INT_MAX || steps > INT_MAX || (steps > 0 && units > INT_MAX / steps)) return false;
+    // (steps are rounded up to whole groups)
+    if (units > INT_MAX || steps > INT_MAX || (steps > 0 && units > (INT_MAX - 16) / steps)) return false;
     const long long stage = (long long)kTile * (dk + dv) * elt;
     long long cl = 1, by_cluster = 0;
     for (int i = 0; i < 4; ++i) {

@@ -13,3 +13,12 @@ FAR = dict(q=1 << 45, qo=1 << 46, k=None, ko=None, pos=1 << 47, plan=BASE)
 def test_tokens_whose_last_warp_would_pass_32_bits(L, T):  # noqa: F811
     """A warp takes up to 32 rows of 32 bytes, so the last one's tokens end up to 31 behind the last token."""
     assert turn(L, T=T, H=1, Hk=0, d=16, r=16, **FAR) == gdn.ERR_ARG
+
+
+def test_tables_whose_tiles_fill_31_bits(L):  # noqa: F811
+    """Room for 2^31 - 2 steps (126 * 11 sequences of 16 + 1549395 tiles): rounding their number up to a CTA's groups would wrap."""
+    size = dict(B=1386, H=4, Hkv=1, page=16, max_pages=31 * 151 * 331 - 16)
+    assert size["B"] * (size["max_pages"] + 16) == 2 ** 31 - 2
+    assert attend(L, table=1 << 50, **size) == gdn.ERR_ARG
+    assert L.gdn_flash_attn_paged_workspace_bytes(1386, 4, 1, 1, 128, 128, 16, size["max_pages"], 1) == 0
+    assert L.gdn_flash_attn_paged_workspace_bytes(1386, 4, 1, 1, 128, 128, 16, size["max_pages"] - 1, 1) > 0
