@@ -507,9 +507,11 @@ int gdn_rotary_write(const void *q, void *q_out, const void *k, const void *v, c
  * by -inf) have no effect on it, whatever their rows hold, NaN and infinities among them.  A mask of the type's
  * lowest finite value takes part in the softmax as the number it is.
  * Accumulation is fp32.  16-bit q, k and v enter exactly, the softmax weights with 22 bits (f16) or 24 (bf16);
- * fp32 q, k, v and weights as two terms of 11 bits, off by 3 * 2^-23 of themselves at most and by 2^-24 on average (infinite
- * elements of fp32 rows make NaN).  Weights are 1 at most, and their products with v are summed before the division by their
- * sum: sums of seen values beyond fp32's range are infinite.  Results do not depend on timing.
+ * fp32 q, k, v and weights as two terms of 11 bits, off by 3 * 2^-23 of themselves at most and by 2^-24 on average.  Weights
+ * are 1 at most, and their products with v are summed before the division by their sum: sums of seen values beyond fp32's
+ * range are infinite.  An infinite element of v, of any type, makes that element infinite or NaN in the rows that see it,
+ * which of the two by where its tile lies (a term of its weight may be 0 or negative), and no other element.  Results do
+ * not depend on timing.
  * Supported: 1 <= n_q <= 19 (else GDN_ERR_SHAPE), head_dim_k and head_dim_v each 64, 128 or 256 (else
  *   GDN_ERR_HEADDIM; gdn_flash_attn_paged_supports), page_size a multiple of 16 (else GDN_ERR_SHAPE), n_heads_kv
  *   dividing n_heads, tables with room for no more than 2^31 - 17 tiles of 16 tokens, and 16 tiles more for each table,

@@ -64,3 +64,22 @@ def test_the_largest_numbers_are_numbers(dtype, big, heads, n_q):
     assert (np.abs(got[..., 7] - ref[..., 7]) <= TOL * np.abs(ref[..., 7]) + 1e-3).all()
     rest = np.arange(128) != 7
     assert oracle.parity_error(got[..., rest], ref[..., rest]) <= TOL
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("heads,n_q", [(4, 1), (16, 1), (8, 5)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_seen_infinities_reach_their_element_only(dtype, heads, n_q, bad):
+    """In the middle of a long sequence, at its end, in its only tile: not finite there, and everything else as before."""
+    c = Case([3000, 41, 16, 64], heads, 2, n_q, 128, dtype=dtype, seed=16)
+    want = c.run()
+    for b, tok in ((0, 1501), (1, 40), (2, 3)):
+        c.vc[int(c.table[b, tok // 32]), 1, tok % 32, 7] = bad
+    got = c.run()
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[:3, :, heads // 2:, 7] = True
+    assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[3], want[3]) and torch.equal(got[:, :, :heads // 2], want[:, :, :heads // 2])
+    # (a tile with such a value may be summed in another order)
+    assert oracle.parity_error(np64(got[~hit]), np64(want[~hit])) <= TOL
