@@ -694,6 +694,44 @@ def rotary_plan(rot_dim: int, base: float = 10000.0, *, freqs=None, sections=Non
     return RotaryPlan(host.to(device), rot_dim, n_axes, bool(neighbours))
 
 
+_rotary_node = None
+
+
+def _rotary_function():
+    """rotary as a node of autograd, whose backward pass is rotary again (so it has a gradient too)."""
+    global _rotary_node
+    if _rotary_node is not None:
+        return _rotary_node
+
+    def rows(g):
+        """g, or a dense copy where its rows are not as rotary takes them (the gradient of a sum is one element)."""
+        ok = g.stride(2) == 1 and g.data_ptr() % 16 == 0 and not any(
+            g.stride(i) * g.element_size() % 16 for i in (0, 1) if g.shape[i] > 1)
+        return g if ok else g.clone(memory_format=_torch.contiguous_format)
+
+    class Rotary(_torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, plan, inverse):
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(positions)
+            ctx.plan, ctx.inverse = plan, inverse
+            return rotary(q, k, positions, plan, inverse=inverse)
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            positions, = ctx.saved_tensors
+            grads = [rows(g) if g is not None and need else None for g, need in zip((dq, dk), ctx.needs_input_grad)]
+            some = [g for g in grads if g is not None]
+            if some:
+                turned = list(rotary(some[0], some[1] if len(some) > 1 else None, positions, ctx.plan,
+                                     inverse=not ctx.inverse))
+                grads = [None if g is None else turned.pop(0) for g in grads]
+            return (*grads, None, None, None)
+
+    _rotary_node = Rotary
+    return Rotary
+
+
 def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=None, stream=None):
     """Turn pairs of elements of q (n_tokens, n_heads, head_dim) and k (n_tokens, n_heads_kv, head_dim, or
     None) by their tokens' positions; returns (q_out, k_out).
@@ -702,7 +740,8 @@ def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=No
     axes.  fp32, bf16 or fp16; any strides with contiguous, 16-byte aligned rows.
     q_out and k_out may be q and k themselves (default: new dense tensors).
     ``inverse`` turns back, which is also the gradient: rotary(dq_out, dk_out,
-    positions, plan, inverse=True) is (dq, dk)."""
+    positions, plan, inverse=True) is (dq, dk).  Where q or k requires a gradient, autograd gets just that from the
+    results; given outputs are plain memory to it, as with every other call here."""
     L, torch = _lib or lib(), _torch or _kv4_torch()
     dtype, dev, qs, i32, axes, ps = q.dtype, q.get_device(), q.shape, torch.int32, plan.n_axes, positions.shape
     dt = _KV4_DTYPES.get(dtype)
@@ -720,6 +759,9 @@ def rotary(q, k, positions, plan, *, inverse: bool = False, q_out=None, k_out=No
                  ("positions", positions, (T,) if len(ps) == 1 and axes == 1 else (axes, T), i32, dev)))
     if stream is not None or torch._C._cuda_getDevice() != dev:
         return _there(dev, stream, rotary, q, k, positions, plan, inverse=inverse, q_out=q_out, k_out=k_out)
+    if (q.requires_grad or (k is not None and k.requires_grad)) and q_out is None and k_out is None \
+            and torch.is_grad_enabled():
+        return _rotary_function().apply(q, k, positions, plan, inverse)
     dense = q.is_contiguous() and (k is None or k.is_contiguous())
     if q_out is None:
         q_out = torch.empty_like(q) if dense else torch.empty(qs, dtype=dtype, device=q.device)
