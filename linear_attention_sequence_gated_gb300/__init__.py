@@ -797,7 +797,8 @@ def paged_cache(n_pages: int, n_heads_kv: int, page_size: int, head_dim_k: int, 
                 device="cuda"):
     """An empty cache of 16- or 32-bit rows: (k_cache, v_cache) of shapes (n_pages, n_heads_kv, page_size, dk) and
     (..., dv), bf16 where no dtype is given.  The calls below take any strides that nest (pages may be
-    token-major: a transposed view of (n_pages, page_size, n_heads_kv, dk))."""
+    token-major: a transposed view of (n_pages, page_size, n_heads_kv, dk)).  Rows of any multiple of 16 elements up to
+    256 can be written; flash_attn_paged reads widths of 64, 128 and 256 and pages of a multiple of 16 tokens."""
     torch = _kv4_torch()
     dtype = torch.bfloat16 if dtype is None else dtype
     _kv4_dtype(dtype, "dtype")

@@ -60,3 +60,20 @@ def test_as_many_entries_as_a_full_stack_holds():
     gdn.page_release(table, i32([n]), free, count, 1)
     assert gdn.device_status() == gdn.ERR_PAGE and int(count) == n
     assert all(bool((x == -5).all()) for x in both.split(1 << 28))
+
+
+@pytest.mark.parametrize("gaps", [False, True])
+def test_more_pages_back_than_a_cluster_holds_at_once(gaps):
+    """Over 65536 entries a CTA takes its share in several turns; with entries that name no page among them."""
+    rng = random.Random(4)
+    lens = [rng.randint(0, 60000) for _ in range(9)] + [0, 40000]
+    n = sum(lens)
+    assert n > 3 * 65536
+    p = Pool(len(lens), 60000, n + 5, 1, seed=5)
+    p.assign(lens, 60000, lens, n, ok=True)
+    if gaps:
+        for b, j in ((0, 7), (4, 0), (10, 39999)):
+            p.table[b, j] = p.h_table[b, j] = -1
+    stay = [a // 5 for a in lens]
+    p.release(lens, stay)
+    p.release(stay)
