@@ -29,9 +29,9 @@
 // in a fixed order.  A call of few tiles gives each unit a cluster of CTAs instead, which join
 // through distributed shared memory: one launch, no workspace.
 //
-// Measured (GPU time of captured calls): 64 sequences x 32/8 heads x 4096 tokens x 128, bf16: 165 us, 96 % of the rate of a
-// copy; 2 x 16/4 x (100003, 50001) x 128: 55 us, 82 % (runs start, fill, drain and join in about 9 us); 16 x 5 queries x 32/8 x
-// up to 5001 x 128, f16: 46 us, of which the stream alone takes 39; 64 queries' rows a kv head there: 105 us, the stream alone
+// Measured (GPU time of captured calls): 64 sequences x 32/8 heads x 4096 tokens x 128, bf16: 165 - 169 us, 94 - 96 % of the
+// rate of a copy; 2 x 16/4 x (100003, 50001) x 128: 55 us, 82 % (runs start, fill, drain and join in about 9 us); 16 x 5 queries x 32/8 x
+// up to 5001 x 128, f16: 45 us, of which the stream alone takes 39; 64 queries' rows a kv head there: 102 us, the stream alone
 // (two units, each tile twice) 62, at 30 % of the tensor pipe and half of all issue slots.
 #pragma once
 
