@@ -737,11 +737,12 @@ struct Unit {
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
             for (int r = 0; r < 2; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-        if constexpr (COLS)
+        if constexpr (COLS) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
+        }
     }
 };
 
