@@ -252,7 +252,7 @@ __device__ __forceinline__ uint32_t round2(float &x, float &y) {
     }
 }
 // fp32 as tf32 hi + lo, 11 bits each.  hi is cut off behind 0.36 to 0.72 of its last bit, added by a product that rounds
-// toward zero: it stays finite up to the largest numbers, and lo, of either sign, is two thirds of that bit at most, so few
+// toward zero: it stays finite up to the largest numbers, and lo, of either sign, is 0.72 of that bit at most, so few
 // lose more than one bit to its own cut: x is off by 3 * 2^-23 at most, 2^-24 in the root mean square.  (hi to nearest: 2^-23
 // and 0.7 * 2^-24, but 2^128 for the largest unless held back.  16 x 16 queries x 32/8 x 5001 x 128, us: so 527; to nearest
 // unprotected 518, by a minimum 596, by adding half of the last bit toward zero 580, by the conversion 692.)
